@@ -276,6 +276,64 @@ edge_status edge_rope(void* q_out, void* k_out, edge_dtype out_dt, const void* q
                       int64_t cache_len, float inv_scale, void* stream);
 
 /*
+ * Attention of a chunk of new tokens over a paged KV cache (the reader of the
+ * cache that edge_qkv_rope_cache writes).  A chunk of one token per sequence is
+ * the decode step; causal = 0 is cross attention to cached states of any
+ * length.
+ *
+ * Sequence b has lens[b] keys in the cache.  Its new tokens are the rows
+ * [q_starts[b], q_starts[b + 1]) of q, n of them, and they are the last n of
+ * its positions: query i sits at position lens[b] - n + i.  Key j of the
+ * sequence is in slot block_table[b][j / page_size] * page_size + j % page_size.
+ * For query head h, which reads key head h / (q_heads / kv_heads):
+ *   s_j   = scale * (q . k_j)  over the keys the query sees,
+ *   out   = sum_j softmax(s)_j v_j,   lse = ln(sum_j e^(s_j)).
+ * A query sees key j when 0 <= j < lens[b], the page number is inside
+ * [0, num_slots / page_size), and, if causal, j <= its position and (window
+ * > 0) position - j < window.  What the cache holds at other keys does not
+ * matter.  A query that sees no key, or only keys of score -infinity, gives
+ * out 0 and lse -infinity.
+ *
+ * q:           [tokens, q_heads, head_dim] of dt.
+ * k_cache, v_cache: [num_slots, kv_heads, head_dim] of dt (NULL allowed when
+ *              num_slots == 0).
+ * out:         [tokens, q_heads, head_dim] of out_dt.  Rows that belong to no
+ *              sequence are left as they were (in lse as well).
+ * lse:         [tokens, q_heads] fp32, or NULL.
+ * block_table: [num_seqs, max_pages] int32.   lens: [num_seqs] int32, clamped
+ *              to [0, max_pages * page_size].
+ * q_starts:    [num_seqs + 1] int32, not decreasing, inside [0, tokens]
+ *              (values outside are clamped); NULL for one token per sequence,
+ *              with tokens == num_seqs.
+ * scale:       finite and > 0.  window: 0 for none; 0 when causal == 0.
+ * workspace:   device memory of at least edge_paged_attention_workspace bytes,
+ *              16-byte aligned, overwritten by the call.  It needs no clearing
+ *              and holds nothing between calls; calls that may run at the same
+ *              time need one each.
+ * Scores, maxima, sums and outputs are held in fp32.  16-bit calls round the
+ * weights to dt for the product with the values; the output is rounded once.
+ * Results are the same from run to run.
+ * EDGE_ERR_SHAPE: q_heads not a multiple of kv_heads, or a workspace that is
+ * too small.  EDGE_ERR_UNSUPPORTED: head_dim above 256, or tokens * q_heads or
+ * max_pages * page_size above 2^30.
+ */
+edge_status edge_paged_attention(void* out, edge_dtype out_dt, float* lse, const void* q,
+                                 const void* k_cache, const void* v_cache, edge_dtype dt,
+                                 int64_t tokens, int32_t q_heads, int32_t kv_heads,
+                                 int32_t head_dim, int64_t num_slots, int32_t page_size,
+                                 const int32_t* block_table, int32_t num_seqs, int32_t max_pages,
+                                 const int32_t* lens, const int32_t* q_starts, float scale,
+                                 int causal, int32_t window, float inv_scale, void* workspace,
+                                 int64_t workspace_bytes, void* stream);
+
+/*
+ * Bytes of workspace that edge_paged_attention needs on the current device for
+ * any number of tokens, sequences and keys; -1 for arguments that it refuses.
+ */
+int64_t edge_paged_attention_workspace(edge_dtype dt, int32_t q_heads, int32_t kv_heads,
+                                       int32_t head_dim);
+
+/*
  * Plain device copy of `bytes` bytes from src to dst, in the launch form of the
  * operators above (a one-shot grid of 16-byte vectors, each CTA's source span
  * prefetched into L2 before the dependent-launch wait).  It computes nothing:

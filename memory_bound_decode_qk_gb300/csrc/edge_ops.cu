@@ -490,6 +490,99 @@ edge_status edge_rope(void* q_out, void* k_out, edge_dtype out_dt, const void* q
                     inv_scale, 0 /* rotate only */, stream);
 }
 
+int64_t edge_paged_attention_workspace(edge_dtype dt, int32_t q_heads, int32_t kv_heads,
+                                       int32_t head_dim) {
+    if (!act_dtype(dt) || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || head_dim < 1 ||
+        head_dim > edge::kMaxAttnHeadDim) {
+        return -1;
+    }
+    return edge::attn_workspace((int)dt, q_heads, kv_heads, head_dim);
+}
+
+edge_status edge_paged_attention(void* out, edge_dtype out_dt, float* lse, const void* q,
+                                 const void* k_cache, const void* v_cache, edge_dtype dt,
+                                 int64_t tokens, int32_t q_heads, int32_t kv_heads,
+                                 int32_t head_dim, int64_t num_slots, int32_t page_size,
+                                 const int32_t* block_table, int32_t num_seqs, int32_t max_pages,
+                                 const int32_t* lens, const int32_t* q_starts, float scale,
+                                 int causal, int32_t window, float inv_scale, void* workspace,
+                                 int64_t workspace_bytes, void* stream) {
+    edge_status st = check_out_dt(out_dt, dt);
+    if (st != EDGE_OK) return st;
+    if (q == nullptr || out == nullptr) return EDGE_ERR_NULL;
+    if (tokens < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || head_dim < 1 ||
+        num_slots < 0 || page_size < 1 || num_seqs < 0 || max_pages < 0) {
+        return EDGE_ERR_SHAPE;
+    }
+    if (num_seqs > 0 && lens == nullptr) return EDGE_ERR_NULL;
+    if (num_slots > 0 && (k_cache == nullptr || v_cache == nullptr)) return EDGE_ERR_NULL;
+    if (num_seqs > 0 && max_pages > 0 && block_table == nullptr) return EDGE_ERR_NULL;
+    if (q_starts == nullptr && tokens != num_seqs) return EDGE_ERR_SHAPE;
+    if (!(std::isfinite(scale) && scale > 0.0f) || (causal != 0 && causal != 1) || window < 0 ||
+        (window > 0 && causal == 0)) {
+        return EDGE_ERR_VALUE;
+    }
+    if ((st = check_scale(out_dt, inv_scale)) != EDGE_OK) return st;
+    const int64_t es = esize(dt);
+    int64_t q_b = 0, o_b = 0, c_b = 0, t_b = 0;
+    if (!checked_bytes(tokens, (int64_t)q_heads * head_dim, es, &q_b) ||
+        !checked_bytes(tokens, (int64_t)q_heads * head_dim, esize(out_dt), &o_b) ||
+        !checked_bytes(num_slots, (int64_t)kv_heads * head_dim, es, &c_b) ||
+        !checked_bytes(num_seqs, max_pages, 4, &t_b)) {
+        return EDGE_ERR_SHAPE;
+    }
+    if (head_dim > edge::kMaxAttnHeadDim || tokens > edge::kMaxAttnRows / q_heads ||
+        (int64_t)max_pages * page_size > edge::kMaxAttnRows ||
+        num_slots / page_size > edge::kMaxUnits) {
+        return EDGE_ERR_UNSUPPORTED;
+    }
+    if (!aligned(q, es) || !aligned(k_cache, es) || !aligned(v_cache, es) ||
+        !aligned(out, esize(out_dt)) || !aligned(lse, 4) || !aligned(block_table, 4) ||
+        !aligned(lens, 4) || !aligned(q_starts, 4) || !aligned(workspace, 16)) {
+        return EDGE_ERR_ALIGN;
+    }
+    const Span so = span(out, o_b), sl = span(lse, tokens * q_heads * 4);
+    const Span sw = span(workspace, workspace_bytes < 0 ? 0 : workspace_bytes);
+    const Span ro[] = {span(q, q_b), span(num_slots ? k_cache : nullptr, c_b),
+                       span(num_slots ? v_cache : nullptr, c_b), span(block_table, t_b),
+                       span(lens, (int64_t)num_seqs * 4),
+                       span(q_starts, ((int64_t)num_seqs + 1) * 4)};
+    if (overlap(so, sl) || overlap(so, sw) || overlap(sl, sw)) return EDGE_ERR_ALIAS;
+    for (const Span& r : ro) {
+        if (overlap(so, r) || overlap(sl, r) || overlap(sw, r)) return EDGE_ERR_ALIAS;
+    }
+    if (tokens == 0 || num_seqs == 0) return EDGE_OK;
+    if (workspace == nullptr) return EDGE_ERR_NULL;
+    if (workspace_bytes < edge::attn_workspace((int)dt, q_heads, kv_heads, head_dim)) {
+        return EDGE_ERR_SHAPE;
+    }
+    edge::AttnArgs a;
+    a.q = q;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.out = out;
+    a.lse = lse;
+    a.table = block_table;
+    a.lens = lens;
+    a.starts = q_starts;
+    a.workspace = workspace;
+    a.tokens = tokens;
+    a.q_heads = q_heads;
+    a.kv_heads = kv_heads;
+    a.head_dim = head_dim;
+    a.num_seqs = num_seqs;
+    a.max_pages = max_pages;
+    a.num_pages = (int)(num_slots / page_size);
+    a.page_size = page_size;
+    a.dt = (int)dt;
+    a.out_dt = (int)out_dt;
+    a.causal = causal;
+    a.window = window;
+    a.scale = scale;
+    a.inv_scale = inv_scale;
+    return finish(edge::launch_attn(a, static_cast<cudaStream_t>(stream)));
+}
+
 edge_status edge_copy(void* dst, const void* src, int64_t bytes, void* stream) {
     if (dst == nullptr || src == nullptr) return EDGE_ERR_NULL;
     if (bytes < 0) return EDGE_ERR_SHAPE;

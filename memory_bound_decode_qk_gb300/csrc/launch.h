@@ -89,6 +89,28 @@ struct QuantArgs {
 };
 cudaError_t launch_quant(const QuantArgs& a, cudaStream_t s);
 
+// Attention over a paged KV cache (paged_attn.cu).
+struct AttnArgs {
+    const void* q;
+    const void* k_cache;
+    const void* v_cache;
+    void* out;
+    float* lse;              // nullable
+    const int32_t* table;
+    const int32_t* lens;
+    const int32_t* starts;   // nullable: one token per sequence
+    void* workspace;
+    int64_t tokens;
+    int q_heads, kv_heads, head_dim;
+    int num_seqs, max_pages, num_pages, page_size;
+    int dt, out_dt, causal, window;
+    float scale, inv_scale;
+};
+constexpr int64_t kMaxAttnHeadDim = 256;
+constexpr int64_t kMaxAttnRows = int64_t(1) << 30;  // tokens * q_heads, max_pages * page_size
+int64_t attn_workspace(int dt, int q_heads, int kv_heads, int head_dim);
+cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s);
+
 // The yardstick copy (copy.cu): bytes from src to dst, validated.
 cudaError_t launch_copy(void* dst, const void* src, int64_t bytes, cudaStream_t s);
 

@@ -1,0 +1,362 @@
+// paged_attn.cu -- attention of a chunk of new tokens over a paged KV cache
+// (sm_103a): dispatch, the kernel for any type and head size, and the join of
+// split units.
+//
+// What it computes.  Sequence b has L_b keys in the cache and n_b new queries,
+// the last n_b of its positions: query i sits at L_b - n_b + i.  Key j lies in
+// slot table[b][j / page] * page + j % page of k_cache and v_cache.  For query
+// head h with key head h / G:
+//   s_j = scale q . k_j over the keys the query sees (j < L_b, a page inside
+//         the pool, and when causal j <= position and, with a window, fewer
+//         than `window` positions back)
+//   out = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m),   lse = m + ln sum
+// One pass over the keys with the running maximum m and sum (online softmax,
+// Milakov and Gimelshein 2018), both in fp32 and in base 2.  A query that
+// sees no key gives 0 and lse -inf.
+#include "paged_common.cuh"
+
+namespace edge {
+namespace {
+
+constexpr int kAnyM = 16;       // query rows of a unit
+constexpr int kAnyKT = 32;      // keys of a tile: one per lane
+constexpr int kAnyThreads = 128;
+
+template <int N>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+// floats per staged row: a multiple of 4 whose quarter is odd, so that 8
+// lanes reading 16 bytes of 8 rows touch all banks once
+__host__ __device__ constexpr int any_stride(int D) {
+    return (((D + 3) / 4) | 1) * 4;
+}
+
+__host__ __device__ constexpr int any_smem_floats(int D) {
+    return (kAnyM + 2 * kAnyKT) * any_stride(D) + kAnyM * kAnyKT;
+}
+
+// Any type, head size up to 32 NV and alignment.  Four warps; a tile's keys
+// and values are staged as fp32 in shared memory.  Scores: lane = key, a warp
+// does its four rows, so a key's 16 bytes serve four rows.  Values: lane =
+// channel, four rows per load.  A key of weight zero (masked, or underflowed)
+// is skipped, so what the cache holds there does not matter.
+template <typename T, int NV, bool VEC>
+__global__ void __launch_bounds__(kAnyThreads) attn_any_kernel(AttnP p) {
+    constexpr int M = kAnyM, KT = kAnyKT;
+    extern __shared__ __align__(16) float smem[];
+    __shared__ WalkSmem wsm;
+    __shared__ int64_t slot_of[KT];
+    const int D = p.D, ds = any_stride(D);
+    float* qs = smem;
+    float* ks = qs + M * ds;
+    float* vs = ks + KT * ds;
+    float* ps = vs + KT * ds;
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+
+    pdl_wait();
+    pdl_launch_dependents();
+    if (tid == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, -1);
+    // the padding channels stay zero
+    for (int i = tid; i < (M + 2 * KT) * ds; i += kAnyThreads) smem[i] = 0.0f;
+
+    Walk w;
+    if (!walk_begin<M, KT>(p, w, wsm, kAnyThreads)) return;
+    do {
+        const int rows = w.s.n * p.G;
+        const int r0 = w.rt * M;
+        __syncthreads();
+        for (int i = tid; i < M * D; i += kAnyThreads) {
+            const int r = i / D, d = i - r * D;
+            float x = 0.0f;
+            if (r0 + r < rows) {
+                x = to_f(reinterpret_cast<const T*>(p.q)[out_row(p, w.s, w.h, r0 + r) * D + d]);
+            }
+            qs[r * ds + d] = x;
+        }
+        float acc[4][NV], m[4], l[4];
+        int at[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            m[r] = -INFINITY;
+            l[r] = 0.0f;
+            at[r] = w.s.L - w.s.n + (int)fast_div((uint32_t)(r0 + wid * 4 + r), p.gdiv);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) acc[r][i] = 0.0f;
+        }
+        for (int kt = w.k0 + w.off; kt < w.k0 + w.off + w.cnt; ++kt) {
+            const int j0 = kt * KT;
+            __syncthreads();  // the tile before is consumed
+            if (tid < KT) slot_of[tid] = j0 + tid < w.s.L ? key_slot(p, w.b, j0 + tid) : -1;
+            __syncthreads();
+            if constexpr (VEC) {
+                constexpr int N = vec_elems<T>();
+                const int nv = D / N;
+                for (int i = tid; i < 2 * KT * nv; i += kAnyThreads) {
+                    const bool isv = i >= KT * nv;
+                    const int e = isv ? i - KT * nv : i;
+                    const int j = e / nv, c = e - j * nv;
+                    const int64_t slot = slot_of[j];
+                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                    if (slot >= 0) {
+                        x = __ldg(reinterpret_cast<const uint4*>(isv ? p.v : p.k) +
+                                  (slot * p.hk + w.h) * nv + c);
+                    }
+                    float f[N];
+                    unpack_vec<T, N>(x, f);
+                    float* dst = (isv ? vs : ks) + j * ds + c * N;
+#pragma unroll
+                    for (int t = 0; t < N; ++t) dst[t] = f[t];
+                }
+            } else {
+                for (int i = tid; i < KT * D; i += kAnyThreads) {
+                    const int j = i / D, d = i - j * D;
+                    const int64_t slot = slot_of[j];
+                    float a = 0.0f, b = 0.0f;
+                    if (slot >= 0) {
+                        const int64_t e = (slot * p.hk + w.h) * D + d;
+                        a = to_f(reinterpret_cast<const T*>(p.k)[e]);
+                        b = to_f(reinterpret_cast<const T*>(p.v)[e]);
+                    }
+                    ks[j * ds + d] = a;
+                    vs[j * ds + d] = b;
+                }
+            }
+            __syncthreads();
+            float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            const float4* kr = reinterpret_cast<const float4*>(ks + lane * ds);
+            for (int c = 0; c < (D + 3) / 4; ++c) {
+                const float4 kk = kr[c];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float4 qq = reinterpret_cast<const float4*>(qs + (wid * 4 + r) * ds)[c];
+                    s[r] = fmaf(qq.x, kk.x, s[r]);
+                    s[r] = fmaf(qq.y, kk.y, s[r]);
+                    s[r] = fmaf(qq.z, kk.z, s[r]);
+                    s[r] = fmaf(qq.w, kk.w, s[r]);
+                }
+            }
+            const bool in = slot_of[lane] >= 0;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float x = in && sees(p, at[r], j0 + lane) ? s[r] * p.scale_log2 : -INFINITY;
+                const float top = fmaxf(m[r], group_max<32>(x));
+                const float ref = top == -INFINITY ? 0.0f : top;
+                const float keep = ex2(m[r] - ref);
+                const float e = ex2(x - ref);
+                m[r] = top;
+                l[r] = l[r] * keep + group_sum<32>(e);
+#pragma unroll
+                for (int i = 0; i < NV; ++i) acc[r][i] *= keep;
+                ps[(wid * 4 + r) * KT + lane] = e;
+            }
+            __syncwarp();
+            for (int j = 0; j < KT; ++j) {
+                float vv[NV];
+#pragma unroll
+                for (int i = 0; i < NV; ++i) vv[i] = lane + 32 * i < D ? vs[j * ds + lane + 32 * i] : 0.0f;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float e = ps[(wid * 4 + r) * KT + j];
+                    if (e != 0.0f) {
+#pragma unroll
+                        for (int i = 0; i < NV; ++i) acc[r][i] = fmaf(e, vv[i], acc[r][i]);
+                    }
+                }
+            }
+        }
+        const int slot = walk_slot(w);
+        float* part = slot < 0 ? nullptr : part_of<M>(p, blockIdx.x, slot);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = wid * 4 + r;
+            if (r0 + row >= rows) continue;
+            if (part != nullptr) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    if (lane + 32 * i < D) part[row * D + lane + 32 * i] = acc[r][i];
+                }
+                if (lane == 0) {
+                    part[M * D + row] = m[r];
+                    part[M * D + M + row] = l[r];
+                }
+            } else {
+                const int64_t orow = out_row(p, w.s, w.h, r0 + row);
+                const float inv = l[r] == 0.0f ? 0.0f : 1.0f / l[r];
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    if (lane + 32 * i < D) store_one<T>(p, orow * D + lane + 32 * i, acc[r][i] * inv);
+                }
+                if (lane == 0 && p.lse != nullptr) p.lse[orow] = row_lse(m[r], l[r]);
+            }
+        }
+        if (slot == 1 && tid == 0) write_desc(p, w);
+    } while (walk_next<M, KT>(p, w));
+}
+
+// Joins the pieces of the unit that started in CTA blockIdx.x without ending
+// there: with M = max m_i, out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
+// One row at a time, a thread per channel.
+template <typename T, int M>
+__global__ void __launch_bounds__(128) attn_combine_kernel(AttnP p) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int c0 = blockIdx.x;
+    const int4 u = p.desc[c0];
+    if (u.w < 0) return;
+    const Seq s = load_seq(p, u.x);
+    const int rows = min(M, s.n * p.G - u.z * M);
+    const int64_t rec = M * (int64_t)p.D + 2 * M;
+    // pieces: slot 1 of c0, then slot 0 of c0 + 1 .. u.w
+    const float* base = p.part + ((int64_t)c0 * 2 + 1) * rec;
+    const int n = u.w - c0 + 1;
+    for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+        float top = -INFINITY;
+        for (int i = 0; i < n; ++i) {
+            const float* pc = base + (i == 0 ? 0 : (2 * i - 1) * rec);
+            top = fmaxf(top, pc[M * p.D + r]);
+        }
+        const float ref = top == -INFINITY ? 0.0f : top;
+        float l = 0.0f;
+        float acc[2] = {0.0f, 0.0f};
+        for (int i = 0; i < n; ++i) {
+            const float* pc = base + (i == 0 ? 0 : (2 * i - 1) * rec);
+            const float f = ex2(pc[M * p.D + r] - ref);
+            l = fmaf(f, pc[M * p.D + M + r], l);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int d = threadIdx.x + 128 * k;
+                if (d < p.D) acc[k] = fmaf(f, pc[(int64_t)r * p.D + d], acc[k]);
+            }
+        }
+        const int64_t orow = out_row(p, s, u.y, u.z * M + r);
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int d = threadIdx.x + 128 * k;
+            if (d < p.D) store_one<T>(p, orow * p.D + d, acc[k] * inv);
+        }
+        if (threadIdx.x == 0 && p.lse != nullptr) p.lse[orow] = row_lse(top, l);
+    }
+}
+
+void launch_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, cudaStream_t s) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 1 : 0;
+}
+
+template <typename T>
+cudaError_t launch_any(const AttnP& p, const AttnShape& sh, bool vec, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    launch_config(cfg, attr, s);
+    cfg.gridDim = dim3((unsigned)sh.ctas);
+    cfg.blockDim = dim3(kAnyThreads);
+    cfg.dynamicSmemBytes = (size_t)any_smem_floats(p.D) * 4;
+    void (*fn)(AttnP);
+    if (p.D <= 64) fn = vec ? attn_any_kernel<T, 2, true> : attn_any_kernel<T, 2, false>;
+    else if (p.D <= 128) fn = vec ? attn_any_kernel<T, 4, true> : attn_any_kernel<T, 4, false>;
+    else fn = vec ? attn_any_kernel<T, 8, true> : attn_any_kernel<T, 8, false>;
+    if (cfg.dynamicSmemBytes > 48 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)cfg.dynamicSmemBytes);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaLaunchKernelEx(&cfg, fn, p);
+}
+
+template <typename T>
+cudaError_t launch_combine_typed(const AttnP& p, const AttnShape& sh, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    launch_config(cfg, attr, s);
+    cfg.gridDim = dim3((unsigned)sh.ctas, 16);
+    cfg.blockDim = dim3(128);
+    return cudaLaunchKernelEx(&cfg, attn_combine_kernel<T, kAnyM>, p);
+}
+
+// The path and grid of a call: sizes and types only, so that the workspace
+// query and the launch agree.
+AttnShape any_shape(int head_dim) {
+    AttnShape sh;
+    sh.path = 0;
+    sh.M = kAnyM;
+    sh.KT = kAnyKT;
+    // two CTAs per SM fit at every head size (at most 88 KB each)
+    sh.ctas = 2 * sm_count();
+    (void)head_dim;
+    return sh;
+}
+
+int64_t shape_bytes(const AttnShape& sh, int head_dim) {
+    return (int64_t)sh.ctas * (16 + 2 * 4 * ((int64_t)sh.M * head_dim + 2 * sh.M));
+}
+
+}  // namespace
+
+cudaError_t launch_attn_combine(const AttnP& p, const AttnShape& sh, int dt, cudaStream_t s) {
+    switch (dt) {
+        case kF32: return launch_combine_typed<float>(p, sh, s);
+        case kF16: return launch_combine_typed<__half>(p, sh, s);
+        default: return launch_combine_typed<__nv_bfloat16>(p, sh, s);
+    }
+}
+
+int64_t attn_workspace(int dt, int q_heads, int kv_heads, int head_dim) {
+    (void)dt;
+    (void)q_heads;
+    (void)kv_heads;
+    return shape_bytes(any_shape(head_dim), head_dim);
+}
+
+cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s) {
+    AttnP p;
+    p.q = static_cast<const char*>(a.q);
+    p.k = static_cast<const char*>(a.k_cache);
+    p.v = static_cast<const char*>(a.v_cache);
+    p.out = static_cast<char*>(a.out);
+    p.lse = a.lse;
+    p.table = a.table;
+    p.lens = a.lens;
+    p.starts = a.starts;
+    p.num_seqs = a.num_seqs;
+    p.max_pages = a.max_pages;
+    p.num_pages = a.num_pages;
+    p.page_size = a.page_size;
+    p.tokens = (int)a.tokens;
+    p.hq = a.q_heads;
+    p.hk = a.kv_heads;
+    p.G = a.q_heads / a.kv_heads;
+    p.D = a.head_dim;
+    p.gdiv = make_fastdiv((uint32_t)p.G);
+    p.pdiv = make_fastdiv((uint32_t)a.page_size);
+    p.causal = a.causal;
+    p.window = a.causal ? a.window : 0;
+    p.out_fp8 = a.out_dt == kFP8;
+    p.max_len = a.max_pages * a.page_size;
+    p.min_per = 1;
+    p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.inv = a.inv_scale;
+    const int es = a.dt == kF32 ? 4 : 2;
+    auto aligned = [](const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) % 16) == 0; };
+    const bool vec = (a.head_dim * es) % 16 == 0 && aligned(a.k_cache) && aligned(a.v_cache);
+    const AttnShape sh = any_shape(a.head_dim);
+    p.desc = static_cast<int4*>(a.workspace);
+    p.part = reinterpret_cast<float*>(p.desc + sh.ctas);
+    cudaError_t e;
+    switch (a.dt) {
+        case kF32: e = launch_any<float>(p, sh, vec, s); break;
+        case kF16: e = launch_any<__half>(p, sh, vec, s); break;
+        default: e = launch_any<__nv_bfloat16>(p, sh, vec, s); break;
+    }
+    if (e != cudaSuccess) return e;
+    return launch_attn_combine(p, sh, a.dt, s);
+}
+
+}  // namespace edge

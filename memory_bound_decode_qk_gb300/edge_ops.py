@@ -27,6 +27,7 @@ STATUS = {
 EXPORTS = ("edge_rmsnorm", "edge_add_rmsnorm", "edge_glu_act", "edge_qk_norm_rope",
            "edge_qk_norm_rope_ex", "edge_rope", "edge_layernorm", "edge_quantize_fp8",
            "edge_qkv_rope_cache", "edge_copy",
+           "edge_paged_attention", "edge_paged_attention_workspace",
            "edge_status_str", "edge_last_cuda_error", "edge_version")
 QK_ROTATE_UNROUNDED = 1
 
@@ -80,6 +81,11 @@ def lib(build_if_missing: bool = False) -> ctypes.CDLL:
                  "edge_qk_norm_rope_ex", "edge_rope", "edge_layernorm", "edge_quantize_fp8",
                  "edge_qkv_rope_cache", "edge_copy"):
         getattr(L, name).restype = I
+    L.edge_paged_attention.argtypes = [P, I, P, P, P, P, I, I64, I32, I32, I32, I64, I32, P, I32,
+                                       I32, P, P, F, I, I32, F, P, I64, P]
+    L.edge_paged_attention.restype = I
+    L.edge_paged_attention_workspace.argtypes = [I, I32, I32, I32]
+    L.edge_paged_attention_workspace.restype = I64
     L.edge_status_str.argtypes = [I]
     L.edge_status_str.restype = ctypes.c_char_p
     L.edge_last_cuda_error.restype = I
@@ -289,3 +295,95 @@ def rope(q, k, positions, cos, sin, *, rotary_dim=None, layout=ROTATE_HALF, q_ou
                            Hk, D, rotary_dim, layout, _ptr(positions), _ptr(cos), _ptr(sin),
                            cache_len, inv_scale, _stream(stream)), "edge_rope")
     return q_out, k_out
+
+
+# ---------------------------------------------------------------- paged cache
+
+def _on(device, stream):
+    """The context in which a call allocates and launches: the tensors' device,
+    and `stream` as torch's current stream, so that memory taken for the call
+    belongs to the stream that uses it."""
+    if stream is None:
+        return torch.cuda.device(device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+def _plain(device, stream):
+    return stream is None and device.index == torch.cuda.current_device()
+
+
+def _want(t, name, dtype, shape, device):
+    """t is a contiguous tensor of this dtype, shape (None: any extent) and device."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not {device}")
+    if len(t.shape) != len(shape) or any(b is not None and a != b for a, b in zip(t.shape, shape)):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous (row-major)")
+
+
+def paged_attention_workspace(q, k_cache):
+    """A workspace for paged_attention calls with heads like q's ([T, Hq, D]) over
+    k_cache ([S, Hk, D]), of any batch and length.  Calls that may run at the
+    same time need one each."""
+    with torch.cuda.device(q.device):
+        n = lib().edge_paged_attention_workspace(_dt(q), q.shape[-2], k_cache.shape[-2],
+                                                 q.shape[-1])
+        if n < 0:
+            raise ValueError("paged_attention does not serve these heads")
+        return torch.empty(n, dtype=torch.uint8, device=q.device)
+
+
+def paged_attention(q, k_cache, v_cache, block_table, lens, *, page_size, q_starts=None,
+                    scale=None, causal=True, window=0, out=None, lse=None, fp8=False,
+                    inv_scale=1.0, workspace=None, stream=None):
+    """Attention of new tokens over a paged KV cache.  q: [T, Hq, D]; k_cache,
+    v_cache: [S, Hk, D] (slot = page * page_size + offset, as qkv_rope_cache
+    writes them); block_table: [B, P] int32; lens: [B] int32, the keys of each
+    sequence with its new tokens.  q_starts: [B + 1] int32, the rows of each
+    sequence in q; None for one token per sequence (T == B).  scale: 1 /
+    sqrt(D) when None.  lse: [T, Hq] fp32 to be filled with the log-sum-exp of
+    each row.  workspace: from paged_attention_workspace; one is taken from
+    torch for the call when None.  Returns out ([T, Hq, D])."""
+    T, Hq, D = q.shape
+    S, Hk, _ = k_cache.shape
+    B, pages = block_table.shape
+    dev = q.device
+    dt = _dt(q)
+    if dev.type != "cuda":
+        raise ValueError(f"q must be a CUDA tensor, not on {dev}")
+    _want(q, "q", q.dtype, (T, Hq, D), dev)
+    _want(k_cache, "k_cache", q.dtype, (S, Hk, D), dev)
+    _want(v_cache, "v_cache", q.dtype, (S, Hk, D), dev)
+    _want(block_table, "block_table", torch.int32, (B, pages), dev)
+    _want(lens, "lens", torch.int32, (B,), dev)
+    if q_starts is not None:
+        _want(q_starts, "q_starts", torch.int32, (B + 1,), dev)
+    if out is not None:
+        _want(out, "out", torch.uint8 if fp8 else q.dtype, (T, Hq, D), dev)
+    if lse is not None:
+        _want(lse, "lse", torch.float32, (T, Hq), dev)
+    if workspace is not None:
+        _want(workspace, "workspace", torch.uint8, (None,), dev)
+    if not _plain(dev, stream):
+        with _on(dev, stream):
+            return paged_attention(q, k_cache, v_cache, block_table, lens, page_size=page_size,
+                                   q_starts=q_starts, scale=scale, causal=causal, window=window,
+                                   out=out, lse=lse, fp8=fp8, inv_scale=inv_scale,
+                                   workspace=workspace)
+    if out is None:
+        out = _alloc(q, q.shape, fp8)
+    if workspace is None:
+        workspace = paged_attention_workspace(q, k_cache)
+    if scale is None:
+        scale = D ** -0.5
+    _check(lib().edge_paged_attention(
+        out.data_ptr(), _out_dt(fp8, dt), _ptr(lse), q.data_ptr(), k_cache.data_ptr(),
+        v_cache.data_ptr(), dt, T, Hq, Hk, D, S, page_size, block_table.data_ptr(), B, pages,
+        lens.data_ptr(), _ptr(q_starts), scale, 1 if causal else 0, window, inv_scale,
+        workspace.data_ptr(), workspace.numel(), _stream(None)), "edge_paged_attention")
+    return out

@@ -22,13 +22,6 @@ constexpr int kAnyM = 16;       // query rows of a unit
 constexpr int kAnyKT = 32;      // keys of a tile: one per lane
 constexpr int kAnyThreads = 128;
 
-template <int N>
-__device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-    for (int o = N / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
-}
-
 // floats per staged row: a multiple of 4 whose quarter is odd, so that 8
 // lanes reading 16 bytes of 8 rows touch all banks once
 __host__ __device__ constexpr int any_stride(int D) {
@@ -252,11 +245,7 @@ void launch_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, cudaStrea
 }
 
 template <typename T>
-cudaError_t launch_any(const AttnP& p, const AttnShape& sh, bool vec, cudaStream_t s) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    launch_config(cfg, attr, s);
-    cfg.gridDim = dim3((unsigned)sh.ctas);
+cudaError_t launch_any(const AttnP& p, bool vec, cudaLaunchConfig_t cfg) {
     cfg.blockDim = dim3(kAnyThreads);
     cfg.dynamicSmemBytes = (size_t)any_smem_floats(p.D) * 4;
     void (*fn)(AttnP);
@@ -272,27 +261,16 @@ cudaError_t launch_any(const AttnP& p, const AttnShape& sh, bool vec, cudaStream
 }
 
 template <typename T>
-cudaError_t launch_combine_typed(const AttnP& p, const AttnShape& sh, cudaStream_t s) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    launch_config(cfg, attr, s);
-    cfg.gridDim = dim3((unsigned)sh.ctas, 16);
+cudaError_t launch_combine(const AttnP& p, int M, cudaLaunchConfig_t cfg) {
+    cfg.gridDim.y = 16;
     cfg.blockDim = dim3(128);
-    return cudaLaunchKernelEx(&cfg, attn_combine_kernel<T, kAnyM>, p);
+    cfg.dynamicSmemBytes = 0;
+    if (M == 16) return cudaLaunchKernelEx(&cfg, attn_combine_kernel<T, 16>, p);
+    return cudaLaunchKernelEx(&cfg, attn_combine_kernel<T, 64>, p);
 }
 
-// The path and grid of a call: sizes and types only, so that the workspace
-// query and the launch agree.
-AttnShape any_shape(int head_dim) {
-    AttnShape sh;
-    sh.path = 0;
-    sh.M = kAnyM;
-    sh.KT = kAnyKT;
-    // two CTAs per SM fit at every head size (at most 88 KB each)
-    sh.ctas = 2 * sm_count();
-    (void)head_dim;
-    return sh;
-}
+// One CTA per SM and slot: two of them fit at every head size (at most 88 KB).
+AttnShape any_shape() { return AttnShape{kPathAny, kAnyM, 2 * sm_count()}; }
 
 int64_t shape_bytes(const AttnShape& sh, int head_dim) {
     return (int64_t)sh.ctas * (16 + 2 * 4 * ((int64_t)sh.M * head_dim + 2 * sh.M));
@@ -300,19 +278,17 @@ int64_t shape_bytes(const AttnShape& sh, int head_dim) {
 
 }  // namespace
 
-cudaError_t launch_attn_combine(const AttnP& p, const AttnShape& sh, int dt, cudaStream_t s) {
-    switch (dt) {
-        case kF32: return launch_combine_typed<float>(p, sh, s);
-        case kF16: return launch_combine_typed<__half>(p, sh, s);
-        default: return launch_combine_typed<__nv_bfloat16>(p, sh, s);
-    }
-}
-
 int64_t attn_workspace(int dt, int q_heads, int kv_heads, int head_dim) {
-    (void)dt;
     (void)q_heads;
     (void)kv_heads;
-    return shape_bytes(any_shape(head_dim), head_dim);
+    int64_t n = shape_bytes(any_shape(), head_dim);
+    if (dt != kF32 && head_dim % 8 == 0) {
+        for (AttnPath path : {kPathFew, kPathMore}) {
+            const int64_t b = shape_bytes(mma_shape(path, dt, head_dim), head_dim);
+            if (b > n) n = b;
+        }
+    }
+    return n;
 }
 
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s) {
@@ -346,17 +322,33 @@ cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s) {
     const int es = a.dt == kF32 ? 4 : 2;
     auto aligned = [](const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) % 16) == 0; };
     const bool vec = (a.head_dim * es) % 16 == 0 && aligned(a.k_cache) && aligned(a.v_cache);
-    const AttnShape sh = any_shape(a.head_dim);
+    AttnShape sh = any_shape();
+    if (a.dt != kF32 && vec && aligned(a.q)) {
+        // rows of a unit: packed (token, head of the group) rows of the
+        // average sequence
+        const int64_t rows = a.tokens * p.G / a.num_seqs;
+        sh = mma_shape(rows <= 16 ? kPathFew : kPathMore, a.dt, a.head_dim);
+    }
     p.desc = static_cast<int4*>(a.workspace);
     p.part = reinterpret_cast<float*>(p.desc + sh.ctas);
+
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 1 : 0;
+    cfg.gridDim = dim3((unsigned)sh.ctas);
     cudaError_t e;
-    switch (a.dt) {
-        case kF32: e = launch_any<float>(p, sh, vec, s); break;
-        case kF16: e = launch_any<__half>(p, sh, vec, s); break;
-        default: e = launch_any<__nv_bfloat16>(p, sh, vec, s); break;
-    }
+    if (sh.path != kPathAny) e = launch_attn_mma(p, sh, a.dt, cfg);
+    else if (a.dt == kF32) e = launch_any<float>(p, vec, cfg);
+    else if (a.dt == kF16) e = launch_any<__half>(p, vec, cfg);
+    else e = launch_any<__nv_bfloat16>(p, vec, cfg);
     if (e != cudaSuccess) return e;
-    return launch_attn_combine(p, sh, a.dt, s);
+    if (a.dt == kF32) return launch_combine<float>(p, sh.M, cfg);
+    if (a.dt == kF16) return launch_combine<__half>(p, sh.M, cfg);
+    return launch_combine<__nv_bfloat16>(p, sh.M, cfg);
 }
 
 }  // namespace edge

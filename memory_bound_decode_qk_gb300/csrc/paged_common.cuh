@@ -76,21 +76,39 @@ __device__ __forceinline__ bool sees(const AttnP& p, int at, int j) {
     return !p.causal || (j <= at && (p.window <= 0 || at - j < p.window));
 }
 
-// Key tiles [k0, k1) of row tile rt; at least one, so that rows that see
-// nothing are still written.
-template <int M, int KT>
-__device__ __forceinline__ void tile_range(const AttnP& p, const Seq& s, int rt, int& k0, int& k1) {
-    int lo = 0, hi = s.L;
+// Keys of row tile rt: [lo, hi) are seen by at least one of its rows (pages
+// outside the pool apart), [flo, fhi) by all of them.
+struct Keys {
+    int lo, hi, flo, fhi;
+};
+
+template <int M>
+__device__ __forceinline__ Keys tile_keys(const AttnP& p, const Seq& s, int rt) {
+    Keys k{0, s.L, 0, s.L};
     if (p.causal) {
         const int r0 = rt * M;
         const int r1 = min(r0 + M, s.n * p.G);
+        const int base = s.L - s.n;
         const int t0 = (int)fast_div((uint32_t)r0, p.gdiv);
-        const int t1 = (int)fast_div((uint32_t)(r1 - 1), p.gdiv) + 1;
-        hi = min(max(s.L - s.n + t1, 0), s.L);
-        if (p.window > 0) lo = max(s.L - s.n + t0 - p.window + 1, 0);
+        const int t1 = (int)fast_div((uint32_t)(r1 - 1), p.gdiv);
+        k.hi = max(base + t1 + 1, 0);
+        k.fhi = max(base + t0 + 1, 0);
+        if (p.window > 0) {
+            k.lo = max(base + t0 - p.window + 1, 0);
+            k.flo = max(base + t1 - p.window + 1, 0);
+        }
     }
-    k0 = lo / KT;
-    k1 = max((hi + KT - 1) / KT, k0 + 1);
+    return k;
+}
+
+// Key tiles [k0, k1) of row tile rt; at least one, so that rows that see
+// nothing are still written.
+template <int M, int KT>
+__device__ __forceinline__ Keys tile_range(const AttnP& p, const Seq& s, int rt, int& k0, int& k1) {
+    const Keys k = tile_keys<M>(p, s, rt);
+    k0 = k.lo / KT;
+    k1 = max((k.hi + KT - 1) / KT, k0 + 1);
+    return k;
 }
 
 template <int M, int KT>
@@ -115,6 +133,7 @@ struct Walk {
     Seq s;
     int k0, k1;    // the unit's key tiles
     int off, cnt;  // the part of them done here: [k0 + off, k0 + off + cnt)
+    Keys keys;
 };
 
 template <int M, int KT>
@@ -194,7 +213,7 @@ __device__ bool walk_begin(const AttnP& p, Walk& w, WalkSmem& sm, int threads) {
     rel -= w.h * per_head;
     w.rt = 0;
     for (;;) {
-        tile_range<M, KT>(p, w.s, w.rt, w.k0, w.k1);
+        w.keys = tile_range<M, KT>(p, w.s, w.rt, w.k0, w.k1);
         if (rel < w.k1 - w.k0) break;
         rel -= w.k1 - w.k0;
         ++w.rt;
@@ -218,7 +237,7 @@ __device__ bool walk_next(const AttnP& p, Walk& w) {
             } while (w.s.n == 0);
         }
     }
-    tile_range<M, KT>(p, w.s, w.rt, w.k0, w.k1);
+    w.keys = tile_range<M, KT>(p, w.s, w.rt, w.k0, w.k1);
     w.off = 0;
     walk_enter<M, KT>(p, w, w.after);
     return true;
@@ -251,6 +270,13 @@ __device__ __forceinline__ int64_t out_row(const AttnP& p, const Seq& s, int h, 
 
 __device__ __forceinline__ float ex2(float x) { return exp2f(x); }
 
+template <int N>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
 constexpr float kLn2 = 0.6931471805599453f;
 
 // Natural log of the row's sum of exponentials from its base-2 maximum and sum.
@@ -267,12 +293,18 @@ __device__ __forceinline__ void store_one(const AttnP& p, int64_t e, float y) {
     }
 }
 
-// Launchers of the tile kernels (each in its own file).  `ctas` is the grid.
+// A path of the operator: its rows per unit and its grid (CTAs that are resident
+// together, so that no piece waits for another's end).
+enum AttnPath { kPathAny = 0, kPathFew = 1, kPathMore = 2 };
 struct AttnShape {
-    int path;    // 0 any size or type, 1 few rows, 2 more rows, 3 many rows
-    int M, KT;
+    AttnPath path;
+    int M;
     int ctas;
 };
-cudaError_t launch_attn_combine(const AttnP& p, const AttnShape& sh, int dt, cudaStream_t s);
+
+// The 16-bit tile kernels (paged_attn_mma.cu): head sizes that are a multiple of
+// 8, 16-byte aligned tensors.
+AttnShape mma_shape(AttnPath path, int dt, int head_dim);
+cudaError_t launch_attn_mma(const AttnP& p, const AttnShape& sh, int dt, cudaLaunchConfig_t cfg);
 
 }  // namespace edge

@@ -21,6 +21,7 @@ namespace {
 constexpr int kAnyM = 16;       // query rows of a unit
 constexpr int kAnyKT = 32;      // keys of a tile: one per lane
 constexpr int kAnyThreads = 128;
+constexpr int kAnyUC = 1;
 
 // floats per staged row: a multiple of 4 whose quarter is odd, so that 8
 // lanes reading 16 bytes of 8 rows touch all banks once
@@ -41,7 +42,7 @@ template <typename T, int NV, bool VEC>
 __global__ void __launch_bounds__(kAnyThreads) attn_any_kernel(AttnP p) {
     constexpr int M = kAnyM, KT = kAnyKT;
     extern __shared__ __align__(16) float smem[];
-    __shared__ WalkSmem wsm;
+    __shared__ WalkSmem<1> wsm;
     __shared__ int64_t slot_of[KT];
     const int D = p.D, ds = any_stride(D);
     float* qs = smem;
@@ -57,7 +58,7 @@ __global__ void __launch_bounds__(kAnyThreads) attn_any_kernel(AttnP p) {
     for (int i = tid; i < (M + 2 * KT) * ds; i += kAnyThreads) smem[i] = 0.0f;
 
     Walk w;
-    if (!walk_begin<M, KT>(p, w, wsm, kAnyThreads)) return;
+    if (!walk_begin<M, KT, kAnyUC, 1>(p, w, wsm, kAnyThreads, 0)) return;
     do {
         const int rows = w.s.n * p.G;
         const int r0 = w.rt * M;
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(kAnyThreads) attn_any_kernel(AttnP p) {
             }
         }
         const int slot = walk_slot(w);
-        float* part = slot < 0 ? nullptr : part_of<M>(p, blockIdx.x, slot);
+        float* part = slot < 0 ? nullptr : part_of<M>(p, w.piece, slot);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int row = wid * 4 + r;
@@ -187,61 +188,70 @@ __global__ void __launch_bounds__(kAnyThreads) attn_any_kernel(AttnP p) {
             }
         }
         if (slot == 1 && tid == 0) write_desc(p, w);
-    } while (walk_next<M, KT>(p, w));
+    } while (walk_next<M, KT, kAnyUC>(p, w));
 }
 
-// Joins the pieces of the unit that started in CTA blockIdx.x without ending
-// there: with M = max m_i, out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
-// One row at a time, a thread per channel.
+// Joins the parts of the unit that started in piece blockIdx.x without ending
+// there: with M = max m_i, out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.  The
+// rows are spread over blockIdx.y; eight warps share a row's parts, a lane has
+// every 32nd channel, and the warps' sums are added in their order.
+constexpr int kJoinWarps = 8;
 template <typename T, int M>
-__global__ void __launch_bounds__(128) attn_combine_kernel(AttnP p) {
+__global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnP p) {
+    __shared__ float acc_of[kJoinWarps][256];
+    __shared__ float top_of[kJoinWarps], sum_of[kJoinWarps];
     pdl_wait();
     pdl_launch_dependents();
-    const int c0 = blockIdx.x;
+    const int c0 = blockIdx.x, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const int4 u = p.desc[c0];
     if (u.w < 0) return;
     const Seq s = load_seq(p, u.x);
     const int rows = min(M, s.n * p.G - u.z * M);
     const int64_t rec = M * (int64_t)p.D + 2 * M;
-    // pieces: slot 1 of c0, then slot 0 of c0 + 1 .. u.w
+    // parts: slot 1 of c0, then slot 0 of c0 + 1 .. u.w
     const float* base = p.part + ((int64_t)c0 * 2 + 1) * rec;
     const int n = u.w - c0 + 1;
     for (int r = blockIdx.y; r < rows; r += gridDim.y) {
         float top = -INFINITY;
-        for (int i = 0; i < n; ++i) {
-            const float* pc = base + (i == 0 ? 0 : (2 * i - 1) * rec);
-            top = fmaxf(top, pc[M * p.D + r]);
+        for (int i = wid * 32 + lane; i < n; i += 32 * kJoinWarps) {
+            top = fmaxf(top, base[(i == 0 ? 0 : (2 * i - 1) * rec) + M * p.D + r]);
         }
+        top = group_max<32>(top);
+        if (lane == 0) top_of[wid] = top;
+        __syncthreads();
+        for (int i = 0; i < kJoinWarps; ++i) top = fmaxf(top, top_of[i]);
         const float ref = top == -INFINITY ? 0.0f : top;
-        float l = 0.0f;
-        float acc[2] = {0.0f, 0.0f};
-        for (int i = 0; i < n; ++i) {
+        float l = 0.0f, acc[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] = 0.0f;
+#pragma unroll 2
+        for (int i = wid; i < n; i += kJoinWarps) {
             const float* pc = base + (i == 0 ? 0 : (2 * i - 1) * rec);
             const float f = ex2(pc[M * p.D + r] - ref);
             l = fmaf(f, pc[M * p.D + M + r], l);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int d = threadIdx.x + 128 * k;
+            for (int k = 0; k < 8; ++k) {
+                const int d = lane + 32 * k;
                 if (d < p.D) acc[k] = fmaf(f, pc[(int64_t)r * p.D + d], acc[k]);
             }
         }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc_of[wid][lane + 32 * k] = acc[k];
+        if (lane == 0) sum_of[wid] = l;
+        __syncthreads();
+        l = 0.0f;
+        for (int i = 0; i < kJoinWarps; ++i) l += sum_of[i];
         const int64_t orow = out_row(p, s, u.y, u.z * M + r);
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int d = threadIdx.x + 128 * k;
-            if (d < p.D) store_one<T>(p, orow * p.D + d, acc[k] * inv);
+        const int d = threadIdx.x;
+        if (d < p.D) {
+            float y = 0.0f;
+            for (int i = 0; i < kJoinWarps; ++i) y += acc_of[i][d];
+            store_one<T>(p, orow * p.D + d, y * inv);
         }
-        if (threadIdx.x == 0 && p.lse != nullptr) p.lse[orow] = row_lse(top, l);
+        if (d == 0 && p.lse != nullptr) p.lse[orow] = row_lse(top, l);
+        __syncthreads();  // the shared sums are read before the next row's
     }
-}
-
-void launch_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, cudaStream_t s) {
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = pdl_enabled() ? 1 : 0;
 }
 
 template <typename T>
@@ -261,19 +271,20 @@ cudaError_t launch_any(const AttnP& p, bool vec, cudaLaunchConfig_t cfg) {
 }
 
 template <typename T>
-cudaError_t launch_combine(const AttnP& p, int M, cudaLaunchConfig_t cfg) {
-    cfg.gridDim.y = 16;
-    cfg.blockDim = dim3(128);
+cudaError_t launch_join(const AttnP& p, const AttnShape& sh, cudaLaunchConfig_t cfg) {
+    const int rows = sh.M < p.tokens * (int64_t)p.G ? sh.M : (int)(p.tokens * (int64_t)p.G);
+    cfg.gridDim = dim3((unsigned)(sh.ctas * sh.per_cta), rows < 16 ? rows : 16);
+    cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.dynamicSmemBytes = 0;
-    if (M == 16) return cudaLaunchKernelEx(&cfg, attn_combine_kernel<T, 16>, p);
-    return cudaLaunchKernelEx(&cfg, attn_combine_kernel<T, 64>, p);
+    if (sh.M == 16) return cudaLaunchKernelEx(&cfg, attn_join_kernel<T, 16>, p);
+    return cudaLaunchKernelEx(&cfg, attn_join_kernel<T, 64>, p);
 }
 
-// One CTA per SM and slot: two of them fit at every head size (at most 88 KB).
-AttnShape any_shape() { return AttnShape{kPathAny, kAnyM, 2 * sm_count()}; }
+// Two CTAs per SM fit at every head size (at most 88 KB each).
+AttnShape any_shape() { return AttnShape{kPathAny, kAnyM, 2 * sm_count(), 1}; }
 
 int64_t shape_bytes(const AttnShape& sh, int head_dim) {
-    return (int64_t)sh.ctas * (16 + 2 * 4 * ((int64_t)sh.M * head_dim + 2 * sh.M));
+    return (int64_t)sh.ctas * sh.per_cta * (16 + 2 * 4 * ((int64_t)sh.M * head_dim + 2 * sh.M));
 }
 
 }  // namespace
@@ -316,7 +327,6 @@ cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s) {
     p.window = a.causal ? a.window : 0;
     p.out_fp8 = a.out_dt == kFP8;
     p.max_len = a.max_pages * a.page_size;
-    p.min_per = 1;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.inv = a.inv_scale;
     const int es = a.dt == kF32 ? 4 : 2;
@@ -329,8 +339,9 @@ cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s) {
         const int64_t rows = a.tokens * p.G / a.num_seqs;
         sh = mma_shape(rows <= 16 ? kPathFew : kPathMore, a.dt, a.head_dim);
     }
+    p.min_per = sh.path == kPathFew ? 4 : 1;
     p.desc = static_cast<int4*>(a.workspace);
-    p.part = reinterpret_cast<float*>(p.desc + sh.ctas);
+    p.part = reinterpret_cast<float*>(p.desc + sh.ctas * sh.per_cta);
 
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -346,9 +357,9 @@ cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s) {
     else if (a.dt == kF16) e = launch_any<__half>(p, vec, cfg);
     else e = launch_any<__nv_bfloat16>(p, vec, cfg);
     if (e != cudaSuccess) return e;
-    if (a.dt == kF32) return launch_combine<float>(p, sh.M, cfg);
-    if (a.dt == kF16) return launch_combine<__half>(p, sh.M, cfg);
-    return launch_combine<__nv_bfloat16>(p, sh.M, cfg);
+    if (a.dt == kF32) return launch_join<float>(p, sh, cfg);
+    if (a.dt == kF16) return launch_join<__half>(p, sh, cfg);
+    return launch_join<__nv_bfloat16>(p, sh, cfg);
 }
 
 }  // namespace edge

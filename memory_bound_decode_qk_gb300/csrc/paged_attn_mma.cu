@@ -7,10 +7,12 @@
 // are the smallest tile they have, and a decode step seldom fills even those,
 // so the wide tcgen05 tiles would have nothing to gain here.
 //
-// attn_few_kernel (16 rows): the four warps of a CTA share the rows and split a
-// tile's keys, each with its own ring of cp.async stages, so nothing but the
-// end of a unit waits for another warp.  The loads run ahead over the ends of
-// units: the walk of the loads is a copy of the walk of the products.
+// attn_few_kernel (16 rows): a worker is one warp, with a piece of the line and a
+// ring of cp.async stages of its own, so no warp ever waits for another.  The
+// loads run ahead over the ends of units: the walk of the loads is a copy of
+// the walk of the products.  (Four warps that split each tile of one piece and
+// joined at the ends of units reached 2.7 TB/s on a ragged batch; this form
+// has no such joins.)
 // attn_more_kernel (64 rows): a warp has 16 rows each and the CTA shares the
 // tiles, so that a key is read once for 64 rows.
 //
@@ -202,7 +204,7 @@ __device__ __forceinline__ void write_tile(const AttnP& p, const Walk& w, const 
                                            const float (&ref)[2], const float (&sum)[2], int row0,
                                            int nrows, int lane) {
     const int slot = walk_slot(w);
-    float* part = slot < 0 ? nullptr : part_of<M>(p, blockIdx.x, slot);
+    float* part = slot < 0 ? nullptr : part_of<M>(p, w.piece, slot);
     const int q = (lane & 3) * 2;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -232,7 +234,6 @@ __device__ __forceinline__ void write_tile(const AttnP& p, const Walk& w, const 
             if (q == 0 && p.lse != nullptr) p.lse[orow] = row_lse(ref[r], sum[r]);
         }
     }
-    if (slot == 1 && threadIdx.x == 0) write_desc(p, w);
 }
 
 // ---------------------------------------------------------------- few rows
@@ -240,33 +241,35 @@ __device__ __forceinline__ void write_tile(const AttnP& p, const Walk& w, const 
 constexpr int kFewWarps = 4;
 constexpr int kFewKeys = 16;  // keys of a warp's stage
 constexpr int kFewStages = 3;
+constexpr int kFewUC = 2;
 
+// Wide heads keep the queries in shared memory: beside 16 rows of output
+// accumulators the registers do not hold them.
 template <int DP>
 constexpr size_t few_smem() {
-    return (size_t)kFewWarps * kFewStages * 2 * kFewKeys * DP * 2 + (size_t)16 * DP * 4 +
-           kFewWarps * 16 * kFewKeys * 4;
+    return (size_t)kFewWarps * (kFewStages * 2 * kFewKeys * DP * 2 + (DP > 128 ? 16 * DP * 2 : 0));
 }
 
 template <typename T, int DP>
 __global__ void __launch_bounds__(kFewWarps * 32, DP <= 128 ? 2 : 1) attn_few_kernel(AttnP p) {
-    constexpr int M = 16, KW = kFewKeys, KT = kFewWarps * KW, ST = kFewStages;
-    constexpr int KS = DP / 16, NO = DP / 8, NT = KW / 8;
-    constexpr int kTile = KW * DP * 2;  // bytes of a warp's K (or V) stage
+    constexpr int M = 16, KT = kFewKeys, ST = kFewStages, UC = kFewUC;
+    constexpr int KS = DP / 16, NO = DP / 8, NT = KT / 8;
+    constexpr bool kQS = DP > 128;
+    constexpr int kTile = KT * DP * 2;  // bytes of a K (or V) stage
     extern __shared__ __align__(128) char smem[];
-    __shared__ WalkSmem wsm;
+    __shared__ WalkSmem<kFewWarps> wsm;
     __shared__ uint32_t dead_of[kFewWarps][ST];
-    __shared__ float mx[kFewWarps][16], sm[kFewWarps][16];
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-    char* mine = smem + wid * ST * 2 * kTile;
-    float* joined = reinterpret_cast<float*>(smem + kFewWarps * ST * 2 * kTile);  // [16][DP]
-    float* ps = joined + 16 * DP + wid * 16 * KW;
+    char* ring = smem + wid * ST * 2 * kTile;
+    char* qt = smem + kFewWarps * ST * 2 * kTile + wid * 16 * DP * 2;
 
     pdl_wait();
     pdl_launch_dependents();
-    if (tid == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, -1);
+    if (tid < kFewWarps) p.desc[blockIdx.x + gridDim.x * tid] = make_int4(0, 0, 0, -1);
+    __syncthreads();
 
     Walk w;
-    if (!walk_begin<M, KT>(p, w, wsm, kFewWarps * 32)) return;
+    if (!walk_begin<M, KT, UC, kFewWarps>(p, w, wsm, kFewWarps * 32, wid)) return;
 
     // the loads' own walk: `off` is the element offset of this lane's key in
     // the next stage to load (-1: a key no row sees), looked up one stage ahead
@@ -275,9 +278,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, DP <= 128 ? 2 : 1) attn_few_ke
     bool live = true;
     int64_t off = -1;
     auto look = [&] {
-        const int j = (lw.k0 + lw.off + lt) * KT + wid * KW + lane;
+        const int j = (lw.k0 + lw.off + lt) * KT + lane;
         off = -1;
-        if (lane < KW && j >= lw.keys.lo && j < lw.keys.hi) {
+        if (lane < KT && j >= lw.keys.lo && j < lw.keys.hi) {
             const int64_t slot = key_slot(p, lw.b, j);
             if (slot >= 0) off = (slot * p.hk + lw.h) * p.D;
         }
@@ -287,9 +290,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, DP <= 128 ? 2 : 1) attn_few_ke
         if (live) {
             const uint32_t dead = __ballot_sync(0xffffffffu, off < 0);
             if (lane == 0) dead_of[wid][st] = dead;
-            const uint32_t kb = smem_addr(mine + st * 2 * kTile), vb = kb + kTile;
+            const uint32_t kb = smem_addr(ring + st * 2 * kTile), vb = kb + kTile;
 #pragma unroll
-            for (int i = 0; i < KW * (DP / 8) / 32; ++i) {
+            for (int i = 0; i < KT * (DP / 8) / 32; ++i) {
                 const int e = lane + 32 * i;
                 const int r = e / (DP / 8), c = e % (DP / 8);
                 const int64_t o = __shfl_sync(0xffffffffu, off, r);
@@ -301,7 +304,16 @@ __global__ void __launch_bounds__(kFewWarps * 32, DP <= 128 ? 2 : 1) attn_few_ke
             }
             if (++lt == lw.cnt) {
                 lt = 0;
-                live = walk_next<M, KT>(p, lw);
+                live = walk_next<M, KT, UC>(p, lw);
+                if (live) {
+                    // the next unit's queries into L1, a line per lane
+                    const int rows = min(lw.s.n * p.G - lw.rt * M, M);
+                    const int lines = (p.D * 2 + 127) / 128;
+                    for (int i = lane; i < rows * lines; i += 32) {
+                        const int r = i / lines;
+                        prefetch_l1_line(p.q + out_row(p, lw.s, lw.h, lw.rt * M + r) * p.D * 2 + (i - r * lines) * 128);
+                    }
+                }
             }
             if (live) look();
         }
@@ -312,9 +324,20 @@ __global__ void __launch_bounds__(kFewWarps * 32, DP <= 128 ? 2 : 1) attn_few_ke
     int stage = 0;
     do {
         const int rows = w.s.n * p.G - w.rt * M;  // rows of the unit (may exceed 16)
-        // queries straight into the fragments of the first product
-        uint32_t qf[KS][4];
-        {
+        uint32_t qf[kQS ? 1 : KS][4];
+        if constexpr (kQS) {
+            __syncwarp();
+            for (int i = lane; i < 16 * (DP / 8); i += 32) {
+                const int r = i / (DP / 8), c = i % (DP / 8);
+                uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                if (r < rows && c * 8 < p.D) {
+                    x = __ldg(reinterpret_cast<const uint4*>(p.q + (out_row(p, w.s, w.h, w.rt * M + r) * p.D + c * 8) * 2));
+                }
+                *reinterpret_cast<uint4*>(qt + chunk_at<DP>(r, c)) = x;
+            }
+            __syncwarp();
+        } else {
+            // queries straight into the fragments of the first product
             const int g = lane >> 2, q = (lane & 3) * 2;
             const T* qp[2];
 #pragma unroll
@@ -351,11 +374,11 @@ __global__ void __launch_bounds__(kFewWarps * 32, DP <= 128 ? 2 : 1) attn_few_ke
             cp_async_wait<ST - 2>();
             __syncwarp();
             issue(stage == 0 ? ST - 1 : stage - 1);
-            const char* kt = mine + stage * 2 * kTile;
+            char* kt = ring + stage * 2 * kTile;
             const char* vt = kt + kTile;
-            const uint32_t ka = smem_addr(kt), va = smem_addr(vt);
-            const uint32_t dead = dead_of[wid][stage];
-            const int j0 = (w.k0 + w.off + t) * KT + wid * KW;
+            const uint32_t ka = smem_addr(kt), va = smem_addr(vt), qa = smem_addr(qt);
+            const uint32_t dead = dead_of[wid][stage] & ((1u << KT) - 1u);
+            const int j0 = (w.k0 + w.off + t) * KT;
             stage = stage + 1 == ST ? 0 : stage + 1;
 
             float s[NT][4];
@@ -366,29 +389,36 @@ __global__ void __launch_bounds__(kFewWarps * 32, DP <= 128 ? 2 : 1) attn_few_ke
             }
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
+                uint32_t a[4];
+                if constexpr (kQS) {
+                    ldsm4(qa + chunk_at<DP>(lane & 15, 2 * k + (lane >> 4)), a);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) a[i] = qf[k][i];
+                }
                 // keys 0-7 and 8-15 by channel halves of the step
                 uint32_t b[4];
                 const int r = (lane & 7) + ((lane >> 4) << 3);
                 ldsm4(ka + chunk_at<DP>(r, 2 * k + ((lane >> 3) & 1)), b);
-                mma16816<T>(s[0], qf[k], b[0], b[1]);
-                mma16816<T>(s[1], qf[k], b[2], b[3]);
+                mma16816<T>(s[0], a, b[0], b[1]);
+                mma16816<T>(s[1], a, b[2], b[3]);
             }
-            const bool part = j0 < w.keys.flo || j0 + KW > w.keys.fhi;
-            const uint32_t mask = dead & 0xffffu;
+            const bool part = j0 < w.keys.flo || j0 + KT > w.keys.fhi;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     s[n][i] *= p.scale_log2;
-                    if (part || mask) {
+                    if (part || dead) {
                         const int c = n * 8 + (lane & 3) * 2 + (i & 1);
-                        if (((mask >> c) & 1u) || !sees(p, at[i >> 1], j0 + c)) s[n][i] = -INFINITY;
+                        if (((dead >> c) & 1u) || !sees(p, at[i >> 1], j0 + c)) s[n][i] = -INFINITY;
                     }
                 }
             }
             soft_tile<NT, NO>(s, o, st);
+            // several tokens: values that only some rows see
             bool odd = false;
-            if (part && w.keys.lo + 1 < w.keys.hi && w.s.n > 1) {
+            if (part && w.s.n > 1) {
                 for (int i = lane; i < kTile / 16; i += 32) {
                     const uint4 x = reinterpret_cast<const uint4*>(vt)[i];
                     odd |= unbounded<T>(x.x) || unbounded<T>(x.y) || unbounded<T>(x.z) || unbounded<T>(x.w);
@@ -396,7 +426,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, DP <= 128 ? 2 : 1) attn_few_ke
                 odd = __any_sync(0xffffffffu, odd);
             }
             if (odd) {
-                careful_values<T, DP, KW, NT, NO>(s, o, vt, ps, lane);
+                careful_values<T, DP, KT, NT, NO>(s, o, vt, reinterpret_cast<float*>(kt), lane);  // the keys are done with
                 continue;
             }
             const uint32_t a[4] = {pack2<T>(s[0][0], s[0][1]), pack2<T>(s[0][2], s[0][3]),
@@ -409,55 +439,14 @@ __global__ void __launch_bounds__(kFewWarps * 32, DP <= 128 ? 2 : 1) attn_few_ke
                 mma16816<T>(o[n + 1], a, b[2], b[3]);
             }
         }
-        // join the warps: a common reference, then the sums one warp at a time
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             st.sum[r] += __shfl_xor_sync(0xffffffffu, st.sum[r], 1);
             st.sum[r] += __shfl_xor_sync(0xffffffffu, st.sum[r], 2);
-            if ((lane & 3) == 0) {
-                mx[wid][(lane >> 2) + 8 * r] = st.ref[r];
-                sm[wid][(lane >> 2) + 8 * r] = st.sum[r];
-            }
         }
-        __syncthreads();
-        float ref[2], sum[2], f[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int row = (lane >> 2) + 8 * r;
-            ref[r] = -INFINITY;
-            for (int i = 0; i < kFewWarps; ++i) ref[r] = fmaxf(ref[r], mx[i][row]);
-            const float base = ref[r] == -INFINITY ? 0.0f : ref[r];
-            sum[r] = 0.0f;
-            for (int i = 0; i < kFewWarps; ++i) sum[r] += ex2(mx[i][row] - base) * sm[i][row];
-            f[r] = ex2(st.ref[r] - base);
-        }
-        for (int turn = 0; turn < kFewWarps; ++turn) {
-            if (turn == wid) {
-#pragma unroll
-                for (int n = 0; n < NO; ++n) {
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        float2* cell = reinterpret_cast<float2*>(joined + ((lane >> 2) + 8 * r) * DP + n * 8 + (lane & 3) * 2);
-                        float2 v = make_float2(o[n][2 * r] * f[r], o[n][2 * r + 1] * f[r]);
-                        if (turn > 0) {
-                            const float2 c = *cell;
-                            v.x += c.x;
-                            v.y += c.y;
-                        }
-                        if (turn == kFewWarps - 1) {
-                            o[n][2 * r] = v.x;
-                            o[n][2 * r + 1] = v.y;
-                        } else {
-                            *cell = v;
-                        }
-                    }
-                }
-            }
-            __syncthreads();
-        }
-        if (wid == kFewWarps - 1) write_tile<T, M, NO>(p, w, o, ref, sum, 0, rows < M ? rows : M, lane);
-        if (walk_slot(w) == 1 && tid == 0) write_desc(p, w);
-    } while (walk_next<M, KT>(p, w));
+        write_tile<T, M, NO>(p, w, o, st.ref, st.sum, 0, rows < M ? rows : M, lane);
+        if (lane == 0 && walk_slot(w) == 1) write_desc(p, w);
+    } while (walk_next<M, KT, UC>(p, w));
     cp_async_wait<0>();
 }
 
@@ -466,6 +455,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, DP <= 128 ? 2 : 1) attn_few_ke
 constexpr int kMoreKeys = 64;
 
 constexpr int kMoreStages = 2;
+constexpr int kMoreUC = 1;
 
 template <int DP>
 constexpr size_t more_smem() {
@@ -478,7 +468,7 @@ __global__ void __launch_bounds__(128, DP <= 128 ? 2 : 1) attn_more_kernel(AttnP
     constexpr int KS = DP / 16, NO = DP / 8, NT = KT / 8;
     constexpr int kTile = KT * DP * 2;
     extern __shared__ __align__(128) char smem[];
-    __shared__ WalkSmem wsm;
+    __shared__ WalkSmem<1> wsm;
     __shared__ uint32_t dead_of[ST][KT / 32];
     __shared__ int64_t off_of[KT];
     __shared__ float ps[4][16 * 16];
@@ -491,7 +481,7 @@ __global__ void __launch_bounds__(128, DP <= 128 ? 2 : 1) attn_more_kernel(AttnP
     if (tid == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, -1);
 
     Walk w;
-    if (!walk_begin<M, KT>(p, w, wsm, 128)) return;
+    if (!walk_begin<M, KT, kMoreUC, 1>(p, w, wsm, 128, 0)) return;
     do {
         const int rows = w.s.n * p.G - w.rt * M;
         __syncthreads();  // the unit before is done with the queries and the ring
@@ -630,7 +620,8 @@ __global__ void __launch_bounds__(128, DP <= 128 ? 2 : 1) attn_more_kernel(AttnP
             st.sum[r] += __shfl_xor_sync(0xffffffffu, st.sum[r], 2);
         }
         write_tile<T, M, NO>(p, w, o, st.ref, st.sum, wid * 16, rows < M ? rows : M, lane);
-    } while (walk_next<M, KT>(p, w));
+        if (tid == 0 && walk_slot(w) == 1) write_desc(p, w);
+    } while (walk_next<M, KT, kMoreUC>(p, w));
     cp_async_wait<0>();
 }
 
@@ -661,7 +652,8 @@ cudaError_t launch_typed(const AttnP& p, const AttnShape& sh, cudaLaunchConfig_t
 AttnShape mma_shape(AttnPath path, int dt, int head_dim) {
     (void)dt;
     const int per_sm = padded(head_dim) <= 128 ? 2 : 1;
-    return AttnShape{path, path == kPathFew ? 16 : 64, per_sm * sm_count()};
+    const bool few = path == kPathFew;
+    return AttnShape{path, few ? 16 : 64, per_sm * sm_count(), few ? kFewWarps : 1};
 }
 
 cudaError_t launch_attn_mma(const AttnP& p, const AttnShape& sh, int dt, cudaLaunchConfig_t cfg) {

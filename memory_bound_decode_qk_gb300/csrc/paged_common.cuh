@@ -3,15 +3,17 @@
 //
 // Schedule.  A unit is M packed query rows of one sequence and one key head
 // (rows are (token, query head of the group), token-major), and its work is a
-// run of key tiles of KT keys.  The tiles of all units form one line, and every
-// CTA takes an equal piece of it, wherever that starts and ends, so a batch of
-// ragged lengths or one long sequence fills the GPU alike.  The lengths live on
-// the device, so each CTA finds its piece itself: a block-wide sum of the
-// sequences' tiles and a scan up to its own start.  A unit that lies in one
-// CTA is written directly.  The pieces of a unit that spans several CTAs go to
-// the workspace as (row maximum, row sum, unnormalized output) and a second
-// kernel joins them.  At most one unit starts in a CTA without ending there
-// (partial slot 1), and at most one ends there that started earlier (slot 0).
+// run of key tiles of KT keys.  The units stand in one line, each as long as
+// its tiles and a constant for its start and end (UC tiles' worth, measured),
+// and every worker (a CTA, or a warp) takes an equal piece of it, wherever that
+// starts and ends, so a batch of ragged lengths or one long sequence fills the
+// GPU alike.  The lengths live on the device, so each CTA finds its pieces
+// itself: a block-wide sum over the sequences and a scan up to its own starts.
+// A unit that lies in one piece is written directly.  The parts of a unit that
+// spans several pieces go to the workspace as (row maximum, row sum,
+// unnormalized output) and a second kernel joins them.  At most one unit starts
+// in a piece without ending there (partial slot 1), and at most one ends there
+// that started earlier (slot 0).
 #pragma once
 
 #include "edge_common.cuh"
@@ -30,14 +32,14 @@ struct AttnP {
     const int32_t* table;
     const int32_t* lens;
     const int32_t* starts;  // nullable: one token per sequence
-    float* part;        // [ctas][2][M * D + 2 M] fp32
-    int4* desc;         // [ctas]: unit of slot 1 (b, h, rt) and its last CTA, or w < 0
+    float* part;        // [pieces][2][M * D + 2 M] fp32
+    int4* desc;         // [pieces]: unit of slot 1 (b, h, rt) and its last piece, or w < 0
     int num_seqs, max_pages, num_pages, page_size;
     int tokens, hq, hk, G, D;
     FastDiv gdiv, pdiv;  // by G and by page_size
     int causal, window, out_fp8;
     int max_len;        // max_pages * page_size
-    int min_per;        // fewest key tiles a CTA takes
+    int min_per;        // shortest piece, in tiles
     float scale_log2;   // scale * log2(e): scores are kept in base 2
     float inv;
 };
@@ -111,24 +113,26 @@ __device__ __forceinline__ Keys tile_range(const AttnP& p, const Seq& s, int rt,
     return k;
 }
 
-template <int M, int KT>
-__device__ __forceinline__ int64_t seq_tiles(const AttnP& p, const Seq& s) {
+// Length of sequence b's units of one key head in the line.
+template <int M, int KT, int UC>
+__device__ __forceinline__ int64_t seq_length(const AttnP& p, const Seq& s) {
     int64_t c = 0;
     const int nrt = (s.n * p.G + M - 1) / M;
     for (int rt = 0; rt < nrt; ++rt) {
         int k0, k1;
         tile_range<M, KT>(p, s, rt, k0, k1);
-        c += k1 - k0;
+        c += UC + k1 - k0;
     }
     return c;
 }
 
-// This CTA's walk over its piece of the line.  Every thread holds the same
-// copy.
+// A worker's walk over its piece of the line.  Every thread of the worker holds
+// the same copy.
 struct Walk {
-    int64_t left;  // tiles of the piece still to do, this unit's included
+    int64_t left;  // length of the piece behind this unit
     int64_t after; // line position at which this unit ends
-    int64_t per;   // tiles per CTA
+    int64_t per;   // length of a piece
+    int piece;
     int b, h, rt;
     Seq s;
     int k0, k1;    // the unit's key tiles
@@ -136,42 +140,54 @@ struct Walk {
     Keys keys;
 };
 
-template <int M, int KT>
-__device__ __forceinline__ void walk_enter(const AttnP& p, Walk& w, int64_t pos) {
-    const int len = w.k1 - w.k0;
-    w.cnt = (int)(w.left < (int64_t)(len - w.off) ? w.left : (int64_t)(len - w.off));
-    w.after = pos + (len - w.off);
+// Takes the unit (b, h, rt), of which the line position `at` lies `rel` behind
+// the start, as far as the piece reaches.  False if that is no tile of it.
+template <int M, int KT, int UC>
+__device__ __forceinline__ bool walk_enter(const AttnP& p, Walk& w, int64_t at, int64_t rel) {
+    w.keys = tile_range<M, KT>(p, w.s, w.rt, w.k0, w.k1);
+    const int64_t len = UC + w.k1 - w.k0;
+    const int64_t share = w.left < len - rel ? w.left : len - rel;
+    w.off = (int)(rel > UC ? rel - UC : 0);
+    const int64_t end = rel + share - UC;
+    w.cnt = end > w.off ? (int)(end - w.off) : 0;
+    w.left -= share;
+    w.after = at + len - rel;
+    return w.cnt > 0;
 }
 
+template <int PP>
 struct WalkSmem {
     int64_t warp[32];
-    int64_t rel;
-    int b;
+    int64_t rel[PP];
+    int b[PP];
 };
 
-// Finds this CTA's piece.  Every thread of the block calls it; false if the
-// piece is empty.  `threads` is the block size, a multiple of 32.
-template <int M, int KT>
-__device__ bool walk_begin(const AttnP& p, Walk& w, WalkSmem& sm, int threads) {
+// Finds the pieces blockIdx.x + gridDim.x i, i < PP, of this CTA; the calling
+// thread's worker takes the one of i = `mine`.  Every thread of the block calls
+// it; false if the worker's piece is empty.  `threads` is the block size, a
+// multiple of 32.
+template <int M, int KT, int UC, int PP>
+__device__ bool walk_begin(const AttnP& p, Walk& w, WalkSmem<PP>& sm, int threads, int mine) {
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, nw = threads >> 5;
-    int64_t first = 0, mine = 0;
+    int64_t first = 0, own = 0;
     for (int b = tid; b < p.num_seqs; b += threads) {
-        const int64_t c = seq_tiles<M, KT>(p, load_seq(p, b));
+        const int64_t c = seq_length<M, KT, UC>(p, load_seq(p, b));
         if (b == tid) first = c;
-        mine += c;
+        own += c;
     }
-    int64_t tot = group_sum<32>(mine);
+    int64_t tot = group_sum<32>(own);
     if (lane == 0) sm.warp[wid] = tot;
+    if (tid < PP) sm.b[tid] = -1;
     __syncthreads();
     tot = 0;
     for (int i = 0; i < nw; ++i) tot += sm.warp[i];
     const int64_t total = tot * p.hk;
-    int64_t per = (total + gridDim.x - 1) / gridDim.x;
+    const int pieces = gridDim.x * PP;
+    int64_t per = (total + pieces - 1) / pieces;
     if (per < p.min_per) per = p.min_per;
-    const int64_t start = per * blockIdx.x;
-    if (start >= total) return false;
-    w.per = per;
-    w.left = total - start < per ? total - start : per;
+    const int64_t low = per * blockIdx.x;  // the first of the CTA's pieces
+    if (low >= total) return false;
+    const int64_t high = per * ((int64_t)blockIdx.x + (int64_t)gridDim.x * (PP - 1));
     int64_t base = 0;
     for (int b0 = 0; b0 < p.num_seqs; b0 += threads) {
         const int b = b0 + tid;
@@ -179,7 +195,7 @@ __device__ bool walk_begin(const AttnP& p, Walk& w, WalkSmem& sm, int threads) {
         if (b0 == 0) {
             c = first;
         } else if (b < p.num_seqs) {
-            c = seq_tiles<M, KT>(p, load_seq(p, b));
+            c = seq_length<M, KT, UC>(p, load_seq(p, b));
         }
         int64_t inc = c;
 #pragma unroll
@@ -189,7 +205,6 @@ __device__ bool walk_begin(const AttnP& p, Walk& w, WalkSmem& sm, int threads) {
         }
         __syncthreads();  // sm.warp's readers of the round before are done
         if (lane == 31) sm.warp[wid] = inc;
-        if (tid == 0) sm.b = -1;
         __syncthreads();
         int64_t before = base, all = 0;
         for (int i = 0; i < nw; ++i) {
@@ -197,36 +212,44 @@ __device__ bool walk_begin(const AttnP& p, Walk& w, WalkSmem& sm, int threads) {
             all += sm.warp[i];
         }
         const int64_t hi = (before + inc) * p.hk, lo = (before + inc - c) * p.hk;
-        if (lo <= start && start < hi) {
-            sm.b = b;
-            sm.rel = start - lo;
+#pragma unroll
+        for (int i = 0; i < PP; ++i) {
+            const int64_t start = low + per * gridDim.x * i;
+            if (lo <= start && start < hi) {
+                sm.b[i] = b;
+                sm.rel[i] = start - lo;
+            }
         }
-        __syncthreads();
-        if (sm.b >= 0) break;
         base += all;
+        if (base * p.hk > high) break;
     }
-    w.b = sm.b;
-    int64_t rel = sm.rel;
+    __syncthreads();
+    w.b = sm.b[mine];
+    if (w.b < 0) return false;
+    w.piece = blockIdx.x + gridDim.x * mine;
+    const int64_t start = per * w.piece;
+    w.per = per;
+    w.left = total - start < per ? total - start : per;
+    int64_t rel = sm.rel[mine];
     w.s = load_seq(p, w.b);
-    const int64_t per_head = seq_tiles<M, KT>(p, w.s);
+    const int64_t per_head = seq_length<M, KT, UC>(p, w.s);
     w.h = (int)(rel / per_head);
     rel -= w.h * per_head;
     w.rt = 0;
     for (;;) {
-        w.keys = tile_range<M, KT>(p, w.s, w.rt, w.k0, w.k1);
-        if (rel < w.k1 - w.k0) break;
-        rel -= w.k1 - w.k0;
+        int k0, k1;
+        tile_range<M, KT>(p, w.s, w.rt, k0, k1);
+        const int len = UC + k1 - k0;
+        if (rel < len) break;
+        rel -= len;
         ++w.rt;
     }
-    w.off = (int)rel;
-    walk_enter<M, KT>(p, w, start);
-    return true;
+    return walk_enter<M, KT, UC>(p, w, start, rel);
 }
 
 // The next unit; false at the end of the piece.
-template <int M, int KT>
+template <int M, int KT, int UC>
 __device__ bool walk_next(const AttnP& p, Walk& w) {
-    w.left -= w.cnt;
     if (w.left <= 0) return false;
     if ((++w.rt) * M >= w.s.n * p.G) {
         w.rt = 0;
@@ -237,29 +260,26 @@ __device__ bool walk_next(const AttnP& p, Walk& w) {
             } while (w.s.n == 0);
         }
     }
-    w.keys = tile_range<M, KT>(p, w.s, w.rt, w.k0, w.k1);
-    w.off = 0;
-    walk_enter<M, KT>(p, w, w.after);
-    return true;
+    return walk_enter<M, KT, UC>(p, w, w.after, 0);
 }
 
-// Where this CTA's part of the unit goes: -1 the output itself, else the
+// Where the worker's part of the unit goes: -1 the output itself, else the
 // partial slot.
 __device__ __forceinline__ int walk_slot(const Walk& w) {
     if (w.cnt == w.k1 - w.k0) return -1;
     return w.off == 0 ? 1 : 0;
 }
 
-// The partial record of (cta, slot): M * D outputs, M maxima, M sums.
+// The partial record of (piece, slot): M * D outputs, M maxima, M sums.
 template <int M>
-__device__ __forceinline__ float* part_of(const AttnP& p, int cta, int slot) {
-    return p.part + ((int64_t)cta * 2 + slot) * (M * (int64_t)p.D + 2 * M);
+__device__ __forceinline__ float* part_of(const AttnP& p, int piece, int slot) {
+    return p.part + ((int64_t)piece * 2 + slot) * (M * (int64_t)p.D + 2 * M);
 }
 
-// Names the unit of slot 1 and the last CTA that holds a piece of it (called
+// Names the unit of slot 1 and the last piece that holds a part of it (called
 // by one thread).
 __device__ __forceinline__ void write_desc(const AttnP& p, const Walk& w) {
-    p.desc[blockIdx.x] = make_int4(w.b, w.h, w.rt, (int)((w.after - 1) / w.per));
+    p.desc[w.piece] = make_int4(w.b, w.h, w.rt, (int)((w.after - 1) / w.per));
 }
 
 // Row r (of the sequence's packed rows) -> element offset of its output row.
@@ -293,13 +313,14 @@ __device__ __forceinline__ void store_one(const AttnP& p, int64_t e, float y) {
     }
 }
 
-// A path of the operator: its rows per unit and its grid (CTAs that are resident
-// together, so that no piece waits for another's end).
+// A path of the operator: its rows per unit, its grid (CTAs that are resident
+// together) and the pieces each CTA takes.
 enum AttnPath { kPathAny = 0, kPathFew = 1, kPathMore = 2 };
 struct AttnShape {
     AttnPath path;
     int M;
     int ctas;
+    int per_cta;
 };
 
 // The 16-bit tile kernels (paged_attn_mma.cu): head sizes that are a multiple of

@@ -227,7 +227,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnP p) {
 #pragma unroll 2
         for (int i = wid; i < n; i += kJoinWarps) {
             const float* pc = base + (i == 0 ? 0 : (2 * i - 1) * rec);
+            // a part that saw nothing wrote no outputs
             const float f = ex2(pc[M * p.D + r] - ref);
+            if (f == 0.0f) continue;
             l = fmaf(f, pc[M * p.D + M + r], l);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -277,7 +279,8 @@ cudaError_t launch_join(const AttnP& p, const AttnShape& sh, cudaLaunchConfig_t 
     cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.dynamicSmemBytes = 0;
     if (sh.M == 16) return cudaLaunchKernelEx(&cfg, attn_join_kernel<T, 16>, p);
-    return cudaLaunchKernelEx(&cfg, attn_join_kernel<T, 64>, p);
+    if (sh.M == 64) return cudaLaunchKernelEx(&cfg, attn_join_kernel<T, 64>, p);
+    return cudaLaunchKernelEx(&cfg, attn_join_kernel<T, 256>, p);
 }
 
 // Two CTAs per SM fit at every head size (at most 88 KB each).
@@ -298,6 +301,8 @@ int64_t attn_workspace(int dt, int q_heads, int kv_heads, int head_dim) {
             const int64_t b = shape_bytes(mma_shape(path, dt, head_dim), head_dim);
             if (b > n) n = b;
         }
+        const int64_t b = shape_bytes(tc_shape(), head_dim);
+        if (head_dim <= 128 && b > n) n = b;
     }
     return n;
 }
@@ -337,7 +342,8 @@ cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s) {
         // rows of a unit: packed (token, head of the group) rows of the
         // average sequence
         const int64_t rows = a.tokens * p.G / a.num_seqs;
-        sh = mma_shape(rows <= 16 ? kPathFew : kPathMore, a.dt, a.head_dim);
+        if (rows > 64 && tc_suits(p)) sh = tc_shape();
+        else sh = mma_shape(rows <= 16 ? kPathFew : kPathMore, a.dt, a.head_dim);
     }
     p.min_per = sh.path == kPathFew ? 4 : 1;
     p.desc = static_cast<int4*>(a.workspace);
@@ -352,7 +358,8 @@ cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s) {
     cfg.numAttrs = pdl_enabled() ? 1 : 0;
     cfg.gridDim = dim3((unsigned)sh.ctas);
     cudaError_t e;
-    if (sh.path != kPathAny) e = launch_attn_mma(p, sh, a.dt, cfg);
+    if (sh.path == kPathMany) e = launch_attn_tc(p, a.dt, cfg);
+    else if (sh.path != kPathAny) e = launch_attn_mma(p, sh, a.dt, cfg);
     else if (a.dt == kF32) e = launch_any<float>(p, vec, cfg);
     else if (a.dt == kF16) e = launch_any<__half>(p, vec, cfg);
     else e = launch_any<__nv_bfloat16>(p, vec, cfg);

@@ -1,0 +1,688 @@
+// paged_attn_tc.cu -- paged attention of 16-bit chunks with many query rows per
+// key head, on the 5th-generation tensor cores (sm_103a).
+//
+// A unit is 256 packed query rows of one key head, as two tiles of 128, so that
+// a key tile of 128 keys is fetched once for 256 rows.  Work per key tile and
+// query tile: S = Q K^T and O += P V, 4 * 128 * 128 * D flops, against 128 * 128
+// exponentials, so the kernel is bound by the matrix pipe if the softmax of one
+// tile runs under the products of the other.  Roles of the 12 warps:
+//   warp 0        copies key and value tiles by TMA into a ring in shared memory
+//   warp 1        issues tcgen05.mma (one thread); accumulators S and O in TMEM
+//   warp 2        value tiles at the edges of what the rows see (below)
+//   warps 4-7     softmax of tile 0, a thread per row;  warps 8-11: of tile 1
+// P goes back to TMEM over S as 16-bit values and is the A operand of the
+// second product.  The order of the products is PV0 S0' PV1 S1', so while a
+// tile's softmax runs the pipe works for the other one.
+// TMEM (512 columns): S0 | S1 | O0 | O1, 128 columns each (fp32).
+//
+// Pages.  The cache is a 3-d tensor (channel, head, slot) to TMA; a page (or 128
+// rows of it) is one box per 64 channels, stored with the 128-byte swizzle.  A
+// page outside the pool or outside the keys that the unit sees is copied from
+// behind the tensor's end, which fills zeros.  A page that is seen in part
+// brings rows that no query may touch, and rows that only some see: warp 2
+// zeroes the first before the tile is used, and looks for infinities and NaN
+// in the second, since 0 * NaN is NaN in a matrix product.  If it finds any, the
+// unit's values are summed again row by row with masked keys skipped.
+//
+// Every wait has a limit of two seconds.  A wait that runs out (which correct
+// operation never does) ends all later waits of the CTA at once and makes its
+// rows NaN.
+#include <cuda.h>
+
+#include "paged_common.cuh"
+
+namespace edge {
+namespace {
+
+constexpr int kTile = 128;  // query rows of a tile, and keys of a tile
+constexpr int kThreads = 384;
+constexpr int kTcUC = 2;
+constexpr uint64_t kWaitLimit = 2000000000ull;  // nanoseconds
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
+
+// ---------------------------------------------------------------- barriers
+
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ uint64_t now_ns() {
+    uint64_t t;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+    return t;
+}
+// Waits for the phase of `parity`; gives up after the limit, or at once if the
+// CTA has failed.
+__device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* failed) {
+    if (bar_try(bar, parity)) return;
+    const uint64_t t0 = now_ns();
+    for (;;) {
+        for (int i = 0; i < 16; ++i) {
+            if (bar_try(bar, parity)) return;
+        }
+        if (*failed) return;
+        if (now_ns() - t0 > kWaitLimit) break;
+    }
+    *failed = 1u;
+}
+
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// ---------------------------------------------------------------- tcgen05
+
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// Arrives on the barrier once every tcgen05 operation issued before is complete.
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// d[128, N] (+)= A B, both operands in shared memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// The same with A in TMEM.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+// 32 columns of this warp's 32 lanes.
+__device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+        : "memory");
+}
+
+// Shared-memory operand descriptor with the 128-byte swizzle: address, leading
+// and stride byte offsets in 16-byte units, version 1 (bit 46), swizzle code 2
+// (bits 61-63).  Operands whose rows run along the summed dimension (Q, K): 8
+// rows of 128 bytes are 1024 bytes (stride offset), the leading offset is
+// unused.  Operands that run along the other one (V): 64 channels of 8 keys are
+// 1024 bytes (stride offset to the next 8 keys), and the leading offset leads to
+// the next 64 channels.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t leading) {
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(leading >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// Instruction descriptor: fp32 accumulator, A and B of type T, M = 128, N = n;
+// bmn: B runs along n.
+template <typename T>
+constexpr __host__ __device__ uint32_t instr_desc(int n, int bmn) {
+    const uint32_t f = std::is_same<T, __half>::value ? 0u : 1u;
+    return (1u << 4) | (f << 7) | (f << 10) | ((uint32_t)bmn << 16) | ((uint32_t)(n / 8) << 17) | ((uint32_t)(kTile / 16) << 24);
+}
+
+// Byte offset of channel chunk c (16 bytes) of row r in a tile of 128 rows,
+// stored as panels of 64 channels with the 128-byte swizzle.
+__device__ __forceinline__ uint32_t panel_at(int r, int c) {
+    return (uint32_t)((c >> 3) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    if constexpr (std::is_same<T, __half>::value) {
+        __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<uint32_t*>(&h);
+    } else {
+        __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<uint32_t*>(&h);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ bool unbounded(uint32_t w) {
+    constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7C007C00u : 0x7F807F80u;
+    return __vcmpeq2(w & e, e) != 0;
+}
+
+// The lowest n bits (n clamped to 0 .. 32).
+__device__ __forceinline__ uint32_t bits_below(int n) {
+    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
+// ---------------------------------------------------------------- the kernel
+
+template <int DP>
+struct Tc {
+    static constexpr int kStages = DP == 64 ? 8 : 5;
+    static constexpr int kPanels = DP / 64;
+    static constexpr int kBytes = kTile * DP * 2;  // one tile of Q, K or V
+    static constexpr int kSmem = (2 + kStages) * kBytes + 1024;
+};
+
+struct TcSmem {
+    uint64_t full[8], empty[8], edge[8];
+    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+    uint32_t tmem;
+    uint32_t failed;
+    uint32_t careful;  // a bit per unit (its number mod 32): values to be summed row by row
+};
+
+// The tiles [a, b) of the unit's part (relative to its first tile) of which query
+// tile i sees anything.
+__device__ __forceinline__ void tile_span(const AttnP& p, const Walk& w, int i, int& a, int& b) {
+    const int t0 = w.k0 + w.off;
+    const Keys k = tile_keys<kTile>(p, w.s, w.rt * 2 + i);
+    a = max(k.lo / kTile - t0, 0);
+    b = min((k.hi + kTile - 1) / kTile - t0, w.cnt);
+    if ((w.rt * 2 + i) * kTile >= w.s.n * p.G || b < a) b = a;
+}
+
+// Whether value tile kt holds keys that not every row of the unit sees.
+__device__ __forceinline__ bool is_edge(const Walk& w, int kt) {
+    return kt * kTile < w.keys.flo || (kt + 1) * kTile > w.keys.fhi;
+}
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+    using C = Tc<DP>;
+    constexpr int M = 2 * kTile, KT = kTile, ST = C::kStages;
+    extern __shared__ char raw[];
+    __shared__ WalkSmem<1> wsm;
+    __shared__ TcSmem sh;
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    // the swizzle works on address bits: tiles start on 1024 bytes
+    const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
+    char* tiles = raw + (base - smem_addr(raw));
+    const uint32_t ring = base + 2 * C::kBytes;
+
+    pdl_wait();
+    pdl_launch_dependents();
+    if (tid == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, -1);
+    Walk w;
+    if (!walk_begin<M, KT, kTcUC, 1>(p, w, wsm, kThreads, 0)) return;
+
+    if (wid == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (tid == 0) {
+        for (int i = 0; i < ST; ++i) {
+            bar_init(smem_addr(&sh.full[i]), 1);
+            bar_init(smem_addr(&sh.empty[i]), 1);
+            bar_init(smem_addr(&sh.edge[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(smem_addr(&sh.q_full[i]), kTile);
+            bar_init(smem_addr(&sh.s_full[i]), 1);
+            bar_init(smem_addr(&sh.p_full[i]), kTile);
+            bar_init(smem_addr(&sh.o_full[i]), 1);
+        }
+        sh.failed = 0;
+        sh.careful = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async_smem();
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = sh.tmem;
+    volatile uint32_t* failed = &sh.failed;
+    // registers: 128 threads at 88 and 256 at 208 are the launch's 384 at 168
+    if (wid < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (wid == 0) {
+        // ---- copies: K0 V0 K1 V1 ... of every unit
+        const int ps = p.page_size;
+        const int rows = ps < kTile ? ps : kTile;  // rows of a box
+        const int np = kTile / rows;               // boxes per panel
+        const int oob = p.num_pages * ps;          // a slot behind the tensor
+        uint32_t e = 0;
+        do {
+            for (int t = 0; t < w.cnt; ++t) {
+                const int kt = w.k0 + w.off + t;
+                // lane l < np looks up page l of the tile
+                int slot = oob;
+                if (lane < np) {
+                    const int j = kt * KT + lane * rows;
+                    if (j + rows > w.keys.lo && j < w.keys.hi) {
+                        const int64_t x = key_slot(p, w.b, j);
+                        if (x >= 0) slot = (int)x;
+                    }
+                }
+#pragma unroll
+                for (int isv = 0; isv < 2; ++isv, ++e) {
+                    const uint32_t st = e % ST;
+                    const uint32_t dst = ring + st * C::kBytes;
+                    bar_wait(smem_addr(&sh.empty[st]), ((e / ST) & 1) ^ 1, failed);
+                    const uint32_t bar = smem_addr(isv && is_edge(w, kt) ? &sh.edge[st] : &sh.full[st]);
+                    if (lane == 0) bar_expect(bar, C::kBytes);
+                    __syncwarp();
+                    for (int i0 = 0; i0 < np * C::kPanels; i0 += 32) {
+                        const int page = (i0 + lane) % np, panel = (i0 + lane) / np;
+                        const int z = __shfl_sync(0xffffffffu, slot, page);
+                        if (panel < C::kPanels) {
+                            tma_load(dst + panel * (kTile * 128) + page * rows * 128, isv ? &vmap : &kmap, panel * 64, w.h, z, bar);
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+        } while (walk_next<M, KT, kTcUC>(p, w));
+    } else if (wid == 1) {
+        // ---- products
+        if (lane == 0) {
+            constexpr uint32_t is = instr_desc<T>(KT, 0), io = instr_desc<T>(DP, 1);
+            uint32_t e = 0, unit[2] = {0, 0}, step[2] = {0, 0};
+            auto scores = [&](int i, uint32_t kst) {
+                const uint32_t a = base + i * C::kBytes, b = ring + kst * C::kBytes;
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k) {
+                    const uint32_t o = (k >> 2) * (kTile * 128) + (k & 3) * 32;
+                    mma_ss(tmem + i * 128, smem_desc(a + o, 16), smem_desc(b + o, 16), is, k > 0);
+                }
+                tc_commit(smem_addr(&sh.s_full[i]));
+            };
+            do {
+                int a[2], b[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) tile_span(p, w, i, a[i], b[i]);
+                for (int t = -1; t < w.cnt; ++t) {
+                    const uint32_t vst = e % ST, vph = (e / ST) & 1;      // V of t
+                    const uint32_t e1 = e + (t < 0 ? 0 : 1);
+                    const uint32_t kst = e1 % ST, kph = (e1 / ST) & 1;    // K of t + 1
+                    if (t >= 0) bar_wait(smem_addr(&sh.full[vst]), vph, failed);
+                    if (t + 1 < w.cnt) bar_wait(smem_addr(&sh.full[kst]), kph, failed);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (t >= a[i] && t < b[i]) {
+                            bar_wait(smem_addr(&sh.p_full[i]), step[i] & 1, failed);
+                            ++step[i];
+                            tc_after();
+#pragma unroll
+                            for (int k = 0; k < KT / 16; ++k) {
+                                mma_ts(tmem + 256 + i * 128, tmem + i * 128 + k * 8,
+                                       smem_desc(ring + vst * C::kBytes + k * 16 * 128, kTile * 128), io, t > a[i] || k > 0);
+                            }
+                            if (t == b[i] - 1) tc_commit(smem_addr(&sh.o_full[i]));
+                        }
+                        if (t + 1 >= a[i] && t + 1 < b[i]) {
+                            if (t + 1 == a[i]) {
+                                bar_wait(smem_addr(&sh.q_full[i]), unit[i] & 1, failed);
+                                ++unit[i];
+                                tc_after();
+                            }
+                            scores(i, kst);
+                        }
+                    }
+                    if (t >= 0) tc_commit(smem_addr(&sh.empty[vst]));
+                    if (t + 1 < w.cnt) tc_commit(smem_addr(&sh.empty[kst]));
+                    e += t < 0 ? 1 : 2;
+                }
+                --e;  // the last step has no next key tile
+            } while (walk_next<M, KT, kTcUC>(p, w));
+        }
+        __syncwarp();
+    } else if (wid == 2) {
+        // ---- value tiles at an edge: rows that no query sees become zero;
+        // infinities and NaN in rows that some see mark the unit
+        uint32_t e = 0, phase = 0, unit = 0;
+        do {
+            for (int t = 0; t < w.cnt; ++t) {
+                const int kt = w.k0 + w.off + t;
+                const uint32_t st = (e + 1) % ST;
+                e += 2;
+                if (!is_edge(w, kt)) continue;
+                bar_wait(smem_addr(&sh.edge[st]), (phase >> st) & 1, failed);
+                phase ^= 1u << st;
+                char* v = tiles + 2 * C::kBytes + st * C::kBytes;
+                bool odd = false;
+                for (int i = lane; i < kTile * (DP / 8); i += 32) {
+                    const int r = i / (DP / 8), c = i % (DP / 8);
+                    const int j = kt * KT + r;
+                    uint4* x = reinterpret_cast<uint4*>(v + panel_at(r, c));
+                    if (j < w.keys.lo || j >= w.keys.hi) {
+                        *x = make_uint4(0u, 0u, 0u, 0u);
+                    } else if (j < w.keys.flo || j >= w.keys.fhi) {
+                        const uint4 y = *x;
+                        odd |= unbounded<T>(y.x) || unbounded<T>(y.y) || unbounded<T>(y.z) || unbounded<T>(y.w);
+                    }
+                }
+                if (__any_sync(0xffffffffu, odd) && lane == 0) atomicOr(&sh.careful, 1u << (unit & 31));
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) bar_arrive(smem_addr(&sh.full[st]));
+            }
+            ++unit;
+        } while (walk_next<M, KT, kTcUC>(p, w));
+    }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        // ---- softmax of query tile i, a thread per row
+        const int i = (wid - 4) >> 2;
+        const int row = tid & 127;
+        const uint32_t lanes = (uint32_t)(wid & 3) << 21;  // 32 lanes of TMEM per warp
+        const uint32_t ts = tmem + i * 128 + lanes, to = tmem + 256 + i * 128 + lanes;
+        char* qt = tiles + i * C::kBytes;
+        uint32_t step = 0, done = 0, unit = 0;
+        do {
+            int a, b;
+            tile_span(p, w, i, a, b);
+            const int r0 = w.rt * M + i * kTile;
+            const int rows = min(w.s.n * p.G - r0, kTile);  // may be <= 0
+            float ref = -INFINITY, sum = 0.0f;
+            const int at = w.s.L - w.s.n + (int)fast_div((uint32_t)(r0 + row), p.gdiv);
+            // keys [from, upto) are this row's
+            const int upto = p.causal ? min(at + 1, w.s.L) : w.s.L;
+            const int from = p.causal && p.window > 0 ? at - p.window + 1 : 0;
+            if (a < b) {
+                for (int x = row; x < kTile * (DP / 8); x += kTile) {
+                    const int r = x / (DP / 8), c = x % (DP / 8);
+                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                    if (r < rows && c * 8 < p.D) {
+                        v = __ldg(reinterpret_cast<const uint4*>(p.q + (out_row(p, w.s, w.h, r0 + r) * p.D + c * 8) * 2));
+                    }
+                    *reinterpret_cast<uint4*>(qt + panel_at(r, c)) = v;
+                }
+                fence_async_smem();
+                tc_before();
+                bar_arrive(smem_addr(&sh.q_full[i]));
+            }
+            const Keys keys = tile_keys<kTile>(p, w.s, w.rt * 2 + i);
+            const int box = p.page_size < kTile ? p.page_size : kTile;
+            const int box_shift = 31 - __clz(box);
+            for (int t = a; t < b; ++t) {
+                const int j0 = (w.k0 + w.off + t) * KT;
+                // pages outside the pool, one lane each
+                bool gone = false;
+                if (lane * box < kTile) {
+                    const int j = j0 + lane * box;
+                    gone = j < w.s.L && key_slot(p, w.b, j) < 0;
+                }
+                const uint32_t lost = __ballot_sync(0xffffffffu, gone);
+                bar_wait(smem_addr(&sh.s_full[i]), step & 1, failed);
+                ++step;
+                tc_after();
+                float s[KT];
+#pragma unroll
+                for (int c = 0; c < KT / 32; ++c) tc_ld32(ts + c * 32, reinterpret_cast<uint32_t*>(s) + c * 32);
+                tc_wait_ld();
+                if (lost || j0 < keys.flo || j0 + KT > keys.fhi) {
+                    const int lo = from - j0, hi = upto - j0;
+#pragma unroll
+                    for (int c = 0; c < KT / 32; ++c) {
+                        uint32_t seen = bits_below(hi - c * 32) & ~bits_below(lo - c * 32);
+                        if (lost) {
+                            for (int k = 0; k < 32; k += 8) {  // a page is 8 keys at least
+                                if ((lost >> ((c * 32 + k) >> box_shift)) & 1u) seen &= ~(0xffu << k);
+                            }
+                        }
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            if (!((seen >> k) & 1u)) s[c * 32 + k] = -INFINITY;
+                        }
+                    }
+                }
+                float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                for (int c = 4; c < KT; c += 4) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) top[k] = fmaxf(top[k], s[c + k]);
+                }
+                const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
+                if (t == a) {
+                    ref = high;
+                } else if (__any_sync(0xffffffffu, high > ref + 8.0f)) {
+                    // lazily: the reference moves only when the weights would
+                    // pass 2^8; the products into O before are complete
+                    // (commit of S is behind them)
+                    const float next = fmaxf(ref, high);
+                    const float keep = next == -INFINITY ? 1.0f : ex2(ref - next);
+                    ref = next;
+                    sum *= keep;
+#pragma unroll 1
+                    for (int c = 0; c < DP / 16; ++c) {
+                        uint32_t o[16];
+                        tc_ld16(to + c * 16, o);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
+                        tc_st16(to + c * 16, o);
+                    }
+                    tc_wait_st();
+                }
+                const float sub = ref == -INFINITY ? 0.0f : -ref;
+                const float2 f2 = splat2(p.scale_log2), r2 = splat2(sub);
+                float2 acc[2] = {splat2(0.0f), splat2(0.0f)};
+#pragma unroll
+                for (int c = 0; c < KT / 32; ++c) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        float2 x = __ffma2_rn(make_float2(s[c * 32 + 2 * k], s[c * 32 + 2 * k + 1]), f2, r2);
+                        x.x = ex2(x.x);
+                        x.y = ex2(x.y);
+                        acc[k & 1] = __fadd2_rn(acc[k & 1], x);
+                        pk[k] = pack2<T>(x.x, x.y);
+                    }
+                    tc_st16(ts + c * 16, pk);
+                }
+                sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+                tc_wait_st();
+                tc_before();
+                bar_arrive(smem_addr(&sh.p_full[i]));
+            }
+            // ---- the unit's end
+            if (a < b) {
+                bar_wait(smem_addr(&sh.o_full[i]), done & 1, failed);
+                ++done;
+                tc_after();
+            }
+            if (rows > 0) {
+                const bool mine = row < rows;
+                const bool again = a < b && ((*(volatile uint32_t*)&sh.careful >> (unit & 31)) & 1u) != 0;
+                const int slot = walk_slot(w);
+                const float nan = *failed ? NAN : 0.0f;
+                float* part = slot < 0 ? nullptr : part_of<M>(p, w.piece, slot);
+                const int64_t orow = mine ? out_row(p, w.s, w.h, r0 + row) : 0;
+                const float scale = (part != nullptr ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum) + nan;
+#pragma unroll 1
+                for (int c = 0; c < DP / 32; ++c) {
+                    uint32_t o[32];
+                    if (a < b) {
+                        tc_ld32(to + c * 32, o);
+                        tc_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = 0u;
+                    }
+                    if (again) {
+                        // key by key, weights of zero skipped
+                        float y[32];
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) y[k] = 0.0f;
+                        const int j1 = min((w.k0 + w.off + b) * KT, upto);
+                        for (int j = max((w.k0 + w.off + a) * KT, from); mine && j < j1; ++j) {
+                            const int64_t ks = key_slot(p, w.b, j);
+                            if (ks < 0) continue;
+                            const T* kr = reinterpret_cast<const T*>(p.k) + (ks * p.hk + w.h) * p.D;
+                            const T* vr = reinterpret_cast<const T*>(p.v) + (ks * p.hk + w.h) * p.D;
+                            float x = 0.0f;
+                            for (int d = 0; d < p.D; ++d) {
+                                x = fmaf(to_f(*reinterpret_cast<const T*>(qt + panel_at(row, d >> 3) + (d & 7) * 2)), to_f(kr[d]), x);
+                            }
+                            x = ex2(fmaf(x, p.scale_log2, ref == -INFINITY ? 0.0f : -ref));
+                            x = round_to<T>(x);
+                            if (x == 0.0f) continue;
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) {
+                                if (c * 32 + k < p.D) y[k] = fmaf(x, to_f(vr[c * 32 + k]), y[k]);
+                            }
+                        }
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(y[k]);
+                        __syncwarp();
+                    }
+                    if (mine) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 8) {
+                            if (c * 32 + k >= p.D) continue;
+                            float y[8];
+#pragma unroll
+                            for (int z = 0; z < 8; ++z) y[z] = __uint_as_float(o[k + z]) * scale;
+                            if (part != nullptr) {
+                                float4* dst = reinterpret_cast<float4*>(part + (int64_t)(i * kTile + row) * p.D + c * 32 + k);
+                                dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+                                dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+                            } else if (p.out_fp8) {
+                                *reinterpret_cast<uint2*>(p.out + orow * p.D + c * 32 + k) = quantize_vec<8>(y, p.inv);
+                            } else {
+                                *reinterpret_cast<uint4*>(p.out + (orow * p.D + c * 32 + k) * 2) = pack_vec<T, 8>(y);
+                            }
+                        }
+                    }
+                }
+                if (mine && part != nullptr) {
+                    part[(int64_t)M * p.D + (i * kTile + row)] = ref;
+                    part[(int64_t)M * p.D + M + (i * kTile + row)] = sum + nan;
+                } else if (mine && p.lse != nullptr) {
+                    p.lse[orow] = row_lse(ref, sum) + nan;
+                }
+                if (slot == 1 && row == 0 && i == 0) write_desc(p, w);
+                tc_before();
+            }
+            // both softmax groups are done with the unit's mark; it is cleared
+            // for the unit after the next
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (tid == 128) atomicAnd(&sh.careful, ~(1u << (unit & 31)));
+            ++unit;
+        } while (walk_next<M, KT, kTcUC>(p, w));
+    }
+    tc_before();
+    __syncthreads();
+    if (*failed) {
+        // copies that nobody waited for end before the shared memory is given up
+        for (const uint64_t t0 = now_ns(); now_ns() - t0 < 1000000ull;) {
+        }
+        __syncthreads();
+    }
+    if (wid == 1) {
+        tc_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+// ---------------------------------------------------------------- launch
+
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                            const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                            CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                            CUtensorMapFloatOOBfill);
+
+Encode encoder() {
+    static const Encode fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            (void)cudaGetLastError();
+            f = nullptr;
+        }
+        return reinterpret_cast<Encode>(f);
+    }();
+    return fn;
+}
+
+bool cache_map(CUtensorMap* map, const AttnP& p, const char* base, int dt) {
+    const cuuint64_t dims[3] = {(cuuint64_t)p.D, (cuuint64_t)p.hk, (cuuint64_t)p.num_pages * p.page_size};
+    const cuuint64_t strides[2] = {(cuuint64_t)p.D * 2, (cuuint64_t)p.hk * p.D * 2};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)(p.page_size < kTile ? p.page_size : kTile)};
+    const cuuint32_t ones[3] = {1, 1, 1};
+    return encoder()(map, dt == kF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                     const_cast<char*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int DP>
+cudaError_t launch_typed(const AttnP& p, const CUtensorMap& km, const CUtensorMap& vm, cudaLaunchConfig_t cfg) {
+    cudaError_t e = cudaFuncSetAttribute((const void*)attn_tc_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         Tc<DP>::kSmem);
+    if (e != cudaSuccess) return e;
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Tc<DP>::kSmem;
+    return cudaLaunchKernelEx(&cfg, attn_tc_kernel<T, DP>, p, km, vm);
+}
+
+}  // namespace
+
+AttnShape tc_shape() { return AttnShape{kPathMany, 2 * kTile, sm_count(), 1}; }
+
+// 16-byte aligned 16-bit tensors of heads of 64 to 128 channels (a multiple of
+// 8); pages of 8, 16, 32, 64 or a multiple of 128 tokens, so that a tile is made
+// of whole boxes of at least one swizzle atom.
+bool tc_suits(const AttnP& p) {
+    const bool page = p.page_size % kTile == 0 || (p.page_size >= 8 && p.page_size < kTile && kTile % p.page_size == 0);
+    return page && p.D >= 64 && p.D <= 128 && p.num_pages > 0 &&
+           (int64_t)p.num_pages * p.page_size <= (int64_t)INT32_MAX - kTile && encoder() != nullptr;
+}
+
+cudaError_t launch_attn_tc(const AttnP& p, int dt, cudaLaunchConfig_t cfg) {
+    CUtensorMap km, vm;
+    if (!cache_map(&km, p, p.k, dt) || !cache_map(&vm, p, p.v, dt)) return cudaErrorInvalidValue;
+    if (dt == kF16) {
+        return p.D <= 64 ? launch_typed<__half, 64>(p, km, vm, cfg) : launch_typed<__half, 128>(p, km, vm, cfg);
+    }
+    return p.D <= 64 ? launch_typed<__nv_bfloat16, 64>(p, km, vm, cfg)
+                     : launch_typed<__nv_bfloat16, 128>(p, km, vm, cfg);
+}
+
+}  // namespace edge

@@ -288,7 +288,13 @@ __device__ __forceinline__ int64_t out_row(const AttnP& p, const Seq& s, int h, 
     return ((int64_t)(s.q0 + tok) * p.hq + h * p.G + (r - tok * p.G));
 }
 
-__device__ __forceinline__ float ex2(float x) { return exp2f(x); }
+// 2^x by the hardware's approximation (relative error about 2^-22, results
+// below the normal range flushed to zero).
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 template <int N>
 __device__ __forceinline__ float group_max(float v) {
@@ -315,7 +321,7 @@ __device__ __forceinline__ void store_one(const AttnP& p, int64_t e, float y) {
 
 // A path of the operator: its rows per unit, its grid (CTAs that are resident
 // together) and the pieces each CTA takes.
-enum AttnPath { kPathAny = 0, kPathFew = 1, kPathMore = 2 };
+enum AttnPath { kPathAny = 0, kPathFew = 1, kPathMore = 2, kPathMany = 3 };
 struct AttnShape {
     AttnPath path;
     int M;
@@ -327,5 +333,11 @@ struct AttnShape {
 // 8, 16-byte aligned tensors.
 AttnShape mma_shape(AttnPath path, int dt, int head_dim);
 cudaError_t launch_attn_mma(const AttnP& p, const AttnShape& sh, int dt, cudaLaunchConfig_t cfg);
+
+// The tcgen05 kernel (paged_attn_tc.cu), where tc_suits says that it serves the
+// head and page size.
+AttnShape tc_shape();
+bool tc_suits(const AttnP& p);
+cudaError_t launch_attn_tc(const AttnP& p, int dt, cudaLaunchConfig_t cfg);
 
 }  // namespace edge

@@ -355,3 +355,106 @@ def test_binding_checks_its_tensors():
                        (dict(scale=0.0), edge_ops.EdgeError), (dict(window=-1), edge_ops.EdgeError)]:
         with pytest.raises(error):
             go(**bad)
+
+
+# chunks of many rows per key head
+
+WIDE = [(8, 2, 128), (3, 3, 128), (6, 1, 64), (12, 2, 80), (24, 2, 104), (40, 1, 128), (4, 2, 256), (16, 1, 192)]
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("hq,hk,D", WIDE)
+@pytest.mark.parametrize("page", [8, 32, 128, 384])
+def test_wide_chunks(dt, hq, hk, D, page):
+    # units that end inside, at and behind a tile of 128 rows or keys; whole prompts and late chunks
+    verify(make(dt, hq, hk, D, page, [(300, 300), (1100, 130), (129, 1), (128, 128), (70, 0), (0, 3), (513, 257)], seed=page + D),
+           tail=3)
+
+
+@gpu
+@pytest.mark.parametrize("hq,hk,D", [(8, 2, 128), (4, 4, 64), (4, 2, 256)])
+@pytest.mark.parametrize("window", [1, 64, 127, 128, 129, 300])
+def test_wide_chunks_window(hq, hk, D, window):
+    verify(make("bf16", hq, hk, D, 16, [(600, 400), (260, 260), (900, 100)], seed=window), window=window)
+
+
+@gpu
+@pytest.mark.parametrize("hq,hk,D", [(8, 2, 128), (4, 4, 64), (4, 2, 256)])
+def test_wide_chunks_cross_and_bad_pages(hq, hk, D):
+    c = make("f16", hq, hk, D, 16, [(333, 200), (40, 300), (0, 200), (1000, 90)], seed=21)
+    verify(c, causal=False, fp8=True, inv=50.0)
+    pages = c["k"].shape[0] // 16
+    c["table"][0, 3] = -1
+    c["table"][0, 20] = pages
+    c["table"][1, :] = pages + 7
+    c["table"][3, 8:40] = -5
+    verify(c, causal=False)
+    verify(c)
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("hq,hk,D", [(8, 2, 128), (4, 4, 64), (4, 2, 256)])
+def test_wide_values_behind_the_mask(dt, hq, hk, D):
+    # NaN and infinite values that only later queries see, in several units and tiles
+    c = make(dt, hq, hk, D, 16, [(700, 600), (400, 300)], seed=22)
+    for b, j, bad in ((0, 350, math.nan), (0, 690, math.inf), (1, 399, -math.inf)):
+        slot = int(c["table"][b, j // 16]) * 16 + j % 16
+        c["v"][slot] = bad
+    out, lse = run(c)
+    torch.cuda.synchronize()
+    ref, tol, rl, lt = paged_ref.attention(c["q"], c["k"], c["v"].nan_to_num(0, 0, 0), c["table"], c["lens"],
+                                           c["starts"], 16, D ** -0.5)
+    clean = torch.ones(900, dtype=torch.bool)
+    clean[250:600] = False
+    clean[899] = False
+    ref[~clean], tol[~clean] = math.nan, math.nan
+    paged_ref.check_rows(out, ref, tol, c["q"].dtype)
+    assert torch.isnan(out[250:600]).any(-1).all() and not torch.isfinite(out[899]).any()
+    assert ((lse.cpu().double() - rl).abs() <= lt).all()
+
+
+@gpu
+def test_wide_chunk_splits_and_repeats():
+    # one sequence over the whole GPU: units in several pieces; the same bits each time
+    c = make("bf16", 8, 2, 128, 16, [(9000, 300), (33, 33)], seed=23, sharp=3.0)
+    first, lse = verify(c)
+    again, lse2 = run(c)
+    assert torch.equal(first, again) and torch.equal(lse, lse2)
+
+
+@gpu
+def test_wide_growing_scores():
+    c = make("bf16", 4, 1, 128, 16, [(900, 300)], seed=24)
+    for j in range(900):
+        c["k"][int(c["table"][0, j // 16]) * 16 + j % 16] = j / 16
+    c["q"] = torch.full_like(c["q"], 0.5)
+    verify(c)
+
+
+@gpu
+def test_wide_chunk_on_another_stream_and_in_a_graph():
+    c = make("bf16", 8, 2, 128, 16, [(700, 200), (300, 300)], seed=25)
+    want, _ = verify(c)
+    d = {n: x.cuda() for n, x in c.items() if n != "page"}
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    args = (d["q"], d["k"], d["v"], d["table"], d["lens"])
+    got = edge_ops.paged_attention(*args, page_size=16, q_starts=d["starts"], stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+    # two graphs with a workspace each, replayed together
+    outs, graphs = [torch.zeros_like(d["q"]) for _ in range(2)], []
+    works = [edge_ops.paged_attention_workspace(d["q"], d["k"]) for _ in range(2)]
+    for out, ws in zip(outs, works):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            edge_ops.paged_attention(*args, page_size=16, q_starts=d["starts"], out=out, workspace=ws)
+        graphs.append(graph)
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            graphs[0].replay()
+        graphs[1].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want) and torch.equal(outs[1], want)

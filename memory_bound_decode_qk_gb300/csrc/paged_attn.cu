@@ -280,6 +280,7 @@ cudaError_t launch_join(const AttnP& p, const AttnShape& sh, cudaLaunchConfig_t 
     cfg.dynamicSmemBytes = 0;
     if (sh.M == 16) return cudaLaunchKernelEx(&cfg, attn_join_kernel<T, 16>, p);
     if (sh.M == 64) return cudaLaunchKernelEx(&cfg, attn_join_kernel<T, 64>, p);
+    if (sh.M == 128) return cudaLaunchKernelEx(&cfg, attn_join_kernel<T, 128>, p);
     return cudaLaunchKernelEx(&cfg, attn_join_kernel<T, 256>, p);
 }
 
@@ -301,8 +302,8 @@ int64_t attn_workspace(int dt, int q_heads, int kv_heads, int head_dim) {
             const int64_t b = shape_bytes(mma_shape(path, dt, head_dim), head_dim);
             if (b > n) n = b;
         }
-        const int64_t b = shape_bytes(tc_shape(), head_dim);
-        if (head_dim <= 128 && b > n) n = b;
+        const int64_t b = shape_bytes(tc_shape(head_dim), head_dim);
+        if (b > n) n = b;
     }
     return n;
 }
@@ -342,7 +343,7 @@ cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s) {
         // rows of a unit: packed (token, head of the group) rows of the
         // average sequence
         const int64_t rows = a.tokens * p.G / a.num_seqs;
-        if (rows > 64 && tc_suits(p)) sh = tc_shape();
+        if (rows > 64 && tc_suits(p)) sh = tc_shape(a.head_dim);
         else sh = mma_shape(rows <= 16 ? kPathFew : kPathMore, a.dt, a.head_dim);
     }
     p.min_per = sh.path == kPathFew ? 4 : 1;

@@ -1,19 +1,24 @@
 // paged_attn_tc.cu -- paged attention of 16-bit chunks with many query rows per
 // key head, on the 5th-generation tensor cores (sm_103a).
 //
-// A unit is 256 packed query rows of one key head, as two tiles of 128, so that
-// a key tile of 128 keys is fetched once for 256 rows.  Work per key tile and
-// query tile: S = Q K^T and O += P V, 4 * 128 * 128 * D flops, against 128 * 128
+// Work per key tile (128 keys) and query tile (128 packed rows of one key head):
+// S = Q K^T and O += P V, 4 * 128 * 128 * D flops, against 128 * 128
 // exponentials, so the kernel is bound by the matrix pipe if the softmax of one
-// tile runs under the products of the other.  Roles of the 12 warps:
-//   warp 0        copies key and value tiles by TMA into a ring in shared memory
-//   warp 1        issues tcgen05.mma (one thread); accumulators S and O in TMEM
-//   warp 2        value tiles at the edges of what the rows see (below)
-//   warps 4-7     softmax of tile 0, a thread per row;  warps 8-11: of tile 1
+// tile runs under the products of another.  Two forms, by what TMEM's 512
+// columns hold:
+//   heads to 128 channels: a unit is two query tiles, S0 | S1 | O0 | O1.  A key
+//     tile is fetched once for 256 rows, and the products alternate,
+//     PV0 S0' PV1 S1': while a tile's softmax runs the pipe works for the other.
+//   heads to 256 channels: a unit is one query tile, S | S' | O (256 columns).
+//     The scores of the next key tile are computed ahead, S' PV S'' PV', so the
+//     softmax of one key tile runs under the products of its neighbours.
+// Roles of the warps:
+//   warp 0        copies keys and values by TMA into a ring in shared memory
+//   warp 1        issues tcgen05.mma (one thread)
+//   warp 2        values at the edges of what the rows see (below)
+//   warps 4-7     softmax, a thread per row;  warps 8-11: of the second tile
 // P goes back to TMEM over S as 16-bit values and is the A operand of the
-// second product.  The order of the products is PV0 S0' PV1 S1', so while a
-// tile's softmax runs the pipe works for the other one.
-// TMEM (512 columns): S0 | S1 | O0 | O1, 128 columns each (fp32).
+// second product.
 //
 // Pages.  The cache is a 3-d tensor (channel, head, slot) to TMA; a page (or 128
 // rows of it) is one box per 64 channels, stored with the 128-byte swizzle.  A
@@ -35,7 +40,6 @@ namespace edge {
 namespace {
 
 constexpr int kTile = 128;  // query rows of a tile, and keys of a tile
-constexpr int kThreads = 384;
 constexpr int kTcUC = 2;
 constexpr uint64_t kWaitLimit = 2000000000ull;  // nanoseconds
 
@@ -169,10 +173,11 @@ constexpr __host__ __device__ uint32_t instr_desc(int n, int bmn) {
     return (1u << 4) | (f << 7) | (f << 10) | ((uint32_t)bmn << 16) | ((uint32_t)(n / 8) << 17) | ((uint32_t)(kTile / 16) << 24);
 }
 
-// Byte offset of channel chunk c (16 bytes) of row r in a tile of 128 rows,
-// stored as panels of 64 channels with the 128-byte swizzle.
+// Byte offset of channel chunk c (16 bytes) of row r in a tile of R rows, stored
+// as panels of 64 channels with the 128-byte swizzle.
+template <int R>
 __device__ __forceinline__ uint32_t panel_at(int r, int c) {
-    return (uint32_t)((c >> 3) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+    return (uint32_t)((c >> 3) * (R * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
 template <typename T>
@@ -201,10 +206,16 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
 
 template <int DP>
 struct Tc {
-    static constexpr int kStages = DP == 64 ? 8 : 5;
+    static constexpr int kNQ = DP <= 128 ? 2 : 1;       // query tiles of a unit
+    static constexpr int kM = kNQ * kTile;
+    static constexpr int kKeys = DP <= 128 ? 128 : 64;  // keys of a ring entry
+    static constexpr int kParts = kTile / kKeys;        // entries of a key tile
+    static constexpr int kStages = DP == 64 ? 8 : DP == 192 ? 7 : 5;
     static constexpr int kPanels = DP / 64;
-    static constexpr int kBytes = kTile * DP * 2;  // one tile of Q, K or V
-    static constexpr int kSmem = (2 + kStages) * kBytes + 1024;
+    static constexpr int kQ = kTile * DP * 2;           // bytes of a query tile
+    static constexpr int kBytes = kKeys * DP * 2;       // bytes of an entry
+    static constexpr int kSmem = kNQ * kQ + kStages * kBytes + 1024;
+    static constexpr int kThreads = 128 + 128 * kNQ;
 };
 
 struct TcSmem {
@@ -217,24 +228,33 @@ struct TcSmem {
 
 // The tiles [a, b) of the unit's part (relative to its first tile) of which query
 // tile i sees anything.
+template <int NQ>
 __device__ __forceinline__ void tile_span(const AttnP& p, const Walk& w, int i, int& a, int& b) {
     const int t0 = w.k0 + w.off;
-    const Keys k = tile_keys<kTile>(p, w.s, w.rt * 2 + i);
+    const Keys k = tile_keys<kTile>(p, w.s, w.rt * NQ + i);
     a = max(k.lo / kTile - t0, 0);
     b = min((k.hi + kTile - 1) / kTile - t0, w.cnt);
-    if ((w.rt * 2 + i) * kTile >= w.s.n * p.G || b < a) b = a;
+    if ((w.rt * NQ + i) * kTile >= w.s.n * p.G || b < a) b = a;
 }
 
-// Whether value tile kt holds keys that not every row of the unit sees.
-__device__ __forceinline__ bool is_edge(const Walk& w, int kt) {
-    return kt * kTile < w.keys.flo || (kt + 1) * kTile > w.keys.fhi;
+// Whether the n keys from j on hold some that not every row of the unit sees.
+__device__ __forceinline__ bool is_edge(const Walk& w, int j, int n) {
+    return j < w.keys.flo || j + n > w.keys.fhi;
+}
+
+// The ring positions (in key tiles, from the unit's first) of the keys and the
+// values of tile t of cnt: the order in which the products take them, K0 V0 K1
+// V1 .. with two query tiles, K0 K1 V0 K2 V1 .. with one.
+template <int NQ>
+__device__ __forceinline__ uint32_t value_place(int t, int cnt) {
+    return NQ == 2 || t + 1 == cnt ? 2 * t + 1 : 2 * t + 2;
 }
 
 template <typename T, int DP>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
 attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
     using C = Tc<DP>;
-    constexpr int M = 2 * kTile, KT = kTile, ST = C::kStages;
+    constexpr int NQ = C::kNQ, M = C::kM, KT = kTile, KE = C::kKeys, ST = C::kStages;
     extern __shared__ char raw[];
     __shared__ WalkSmem<1> wsm;
     __shared__ TcSmem sh;
@@ -242,13 +262,13 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
     // the swizzle works on address bits: tiles start on 1024 bytes
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
     char* tiles = raw + (base - smem_addr(raw));
-    const uint32_t ring = base + 2 * C::kBytes;
+    const uint32_t ring = base + NQ * C::kQ;
 
     pdl_wait();
     pdl_launch_dependents();
     if (tid == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, -1);
     Walk w;
-    if (!walk_begin<M, KT, kTcUC, 1>(p, w, wsm, kThreads, 0)) return;
+    if (!walk_begin<M, KT, kTcUC, 1>(p, w, wsm, C::kThreads, 0)) return;
 
     if (wid == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem)) : "memory");
@@ -276,146 +296,206 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
     tc_after();
     const uint32_t tmem = sh.tmem;
     volatile uint32_t* failed = &sh.failed;
-    // registers: 128 threads at 88 and 256 at 208 are the launch's 384 at 168
+    // registers with two softmax groups: 128 threads at 88 and 256 at 208 are
+    // the launch's 384 at 168
     if (wid < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (wid == 0) {
-        // ---- copies: K0 V0 K1 V1 ... of every unit
-        const int ps = p.page_size;
-        const int rows = ps < kTile ? ps : kTile;  // rows of a box
-        const int np = kTile / rows;               // boxes per panel
-        const int oob = p.num_pages * ps;          // a slot behind the tensor
-        uint32_t e = 0;
-        do {
-            for (int t = 0; t < w.cnt; ++t) {
-                const int kt = w.k0 + w.off + t;
-                // lane l < np looks up page l of the tile
-                int slot = oob;
-                if (lane < np) {
-                    const int j = kt * KT + lane * rows;
-                    if (j + rows > w.keys.lo && j < w.keys.hi) {
-                        const int64_t x = key_slot(p, w.b, j);
-                        if (x >= 0) slot = (int)x;
-                    }
-                }
+        if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (wid == 0) {
+            // ---- copies
+            const int rows = p.page_size < KE ? p.page_size : KE;  // rows of a box
+            const int np = KE / rows;                              // boxes per panel
+            const int oob = p.num_pages * p.page_size;             // a slot behind the tensor
+            uint32_t e = 0;
+            auto copy = [&](int t, bool isv) {
 #pragma unroll
-                for (int isv = 0; isv < 2; ++isv, ++e) {
+                for (int h = 0; h < C::kParts; ++h, ++e) {
+                    const int j0 = (w.k0 + w.off + t) * KT + h * KE;
+                    // lane l < np looks up page l
+                    int slot = oob;
+                    if (lane < np) {
+                        const int j = j0 + lane * rows;
+                        if (j + rows > w.keys.lo && j < w.keys.hi) {
+                            const int64_t x = key_slot(p, w.b, j);
+                            if (x >= 0) slot = (int)x;
+                        }
+                    }
                     const uint32_t st = e % ST;
                     const uint32_t dst = ring + st * C::kBytes;
                     bar_wait(smem_addr(&sh.empty[st]), ((e / ST) & 1) ^ 1, failed);
-                    const uint32_t bar = smem_addr(isv && is_edge(w, kt) ? &sh.edge[st] : &sh.full[st]);
+                    const uint32_t bar = smem_addr(isv && is_edge(w, j0, KE) ? &sh.edge[st] : &sh.full[st]);
                     if (lane == 0) bar_expect(bar, C::kBytes);
                     __syncwarp();
                     for (int i0 = 0; i0 < np * C::kPanels; i0 += 32) {
                         const int page = (i0 + lane) % np, panel = (i0 + lane) / np;
                         const int z = __shfl_sync(0xffffffffu, slot, page);
                         if (panel < C::kPanels) {
-                            tma_load(dst + panel * (kTile * 128) + page * rows * 128, isv ? &vmap : &kmap, panel * 64, w.h, z, bar);
+                            tma_load(dst + panel * (KE * 128) + page * rows * 128, isv ? &vmap : &kmap, panel * 64, w.h, z, bar);
                         }
                     }
                     __syncwarp();
                 }
-            }
-        } while (walk_next<M, KT, kTcUC>(p, w));
-    } else if (wid == 1) {
-        // ---- products
-        if (lane == 0) {
-            constexpr uint32_t is = instr_desc<T>(KT, 0), io = instr_desc<T>(DP, 1);
-            uint32_t e = 0, unit[2] = {0, 0}, step[2] = {0, 0};
-            auto scores = [&](int i, uint32_t kst) {
-                const uint32_t a = base + i * C::kBytes, b = ring + kst * C::kBytes;
-#pragma unroll
-                for (int k = 0; k < DP / 16; ++k) {
-                    const uint32_t o = (k >> 2) * (kTile * 128) + (k & 3) * 32;
-                    mma_ss(tmem + i * 128, smem_desc(a + o, 16), smem_desc(b + o, 16), is, k > 0);
-                }
-                tc_commit(smem_addr(&sh.s_full[i]));
             };
             do {
-                int a[2], b[2];
+                if constexpr (NQ == 1) copy(0, false);
+                for (int t = 0; t < w.cnt; ++t) {
+                    if constexpr (NQ == 2) {
+                        copy(t, false);
+                    } else if (t + 1 < w.cnt) {
+                        copy(t + 1, false);
+                    }
+                    copy(t, true);
+                }
+            } while (walk_next<M, KT, kTcUC>(p, w));
+        } else if (wid == 1) {
+            // ---- products
+            if (lane == 0) {
+                constexpr uint32_t is = instr_desc<T>(KE, 0), io = instr_desc<T>(DP, 1);
+                // S (at column ts of TMEM) of query tile i and the keys of entries e ..
+                auto scores = [&](uint32_t ts, int i, uint32_t e) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) tile_span(p, w, i, a[i], b[i]);
-                for (int t = -1; t < w.cnt; ++t) {
-                    const uint32_t vst = e % ST, vph = (e / ST) & 1;      // V of t
-                    const uint32_t e1 = e + (t < 0 ? 0 : 1);
-                    const uint32_t kst = e1 % ST, kph = (e1 / ST) & 1;    // K of t + 1
-                    if (t >= 0) bar_wait(smem_addr(&sh.full[vst]), vph, failed);
-                    if (t + 1 < w.cnt) bar_wait(smem_addr(&sh.full[kst]), kph, failed);
+                    for (int h = 0; h < C::kParts; ++h) {
+                        const uint32_t a = base + i * C::kQ, b = ring + ((e + h) % ST) * C::kBytes;
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (t >= a[i] && t < b[i]) {
-                            bar_wait(smem_addr(&sh.p_full[i]), step[i] & 1, failed);
-                            ++step[i];
-                            tc_after();
-#pragma unroll
-                            for (int k = 0; k < KT / 16; ++k) {
-                                mma_ts(tmem + 256 + i * 128, tmem + i * 128 + k * 8,
-                                       smem_desc(ring + vst * C::kBytes + k * 16 * 128, kTile * 128), io, t > a[i] || k > 0);
-                            }
-                            if (t == b[i] - 1) tc_commit(smem_addr(&sh.o_full[i]));
-                        }
-                        if (t + 1 >= a[i] && t + 1 < b[i]) {
-                            if (t + 1 == a[i]) {
-                                bar_wait(smem_addr(&sh.q_full[i]), unit[i] & 1, failed);
-                                ++unit[i];
-                                tc_after();
-                            }
-                            scores(i, kst);
+                        for (int k = 0; k < DP / 16; ++k) {
+                            mma_ss(tmem + ts + h * KE, smem_desc(a + (k >> 2) * (kTile * 128) + (k & 3) * 32, 16),
+                                   smem_desc(b + (k >> 2) * (KE * 128) + (k & 3) * 32, 16), is, k > 0);
                         }
                     }
-                    if (t >= 0) tc_commit(smem_addr(&sh.empty[vst]));
-                    if (t + 1 < w.cnt) tc_commit(smem_addr(&sh.empty[kst]));
-                    e += t < 0 ? 1 : 2;
+                };
+                // O (at column to) += P (over S) times the values of entries e ..
+                auto values = [&](uint32_t to, uint32_t ts, uint32_t e, bool add) {
+#pragma unroll
+                    for (int h = 0; h < C::kParts; ++h) {
+                        const uint32_t b = ring + ((e + h) % ST) * C::kBytes;
+#pragma unroll
+                        for (int k = 0; k < KE / 16; ++k) {
+                            mma_ts(tmem + to, tmem + ts + h * (KE / 2) + k * 8, smem_desc(b + k * 16 * 128, KE * 128), io,
+                                   add || h > 0 || k > 0);
+                        }
+                    }
+                };
+                auto wait_full = [&](uint32_t e) {
+#pragma unroll
+                    for (int h = 0; h < C::kParts; ++h) bar_wait(smem_addr(&sh.full[(e + h) % ST]), ((e + h) / ST) & 1, failed);
+                };
+                auto give_back = [&](uint32_t e) {
+#pragma unroll
+                    for (int h = 0; h < C::kParts; ++h) tc_commit(smem_addr(&sh.empty[(e + h) % ST]));
+                };
+                uint32_t e = 0, unit[2] = {0, 0}, step[2] = {0, 0};
+                do {
+                    int a[NQ], b[NQ];
+#pragma unroll
+                    for (int i = 0; i < NQ; ++i) tile_span<NQ>(p, w, i, a[i], b[i]);
+                    for (int t = -1; t < w.cnt; ++t) {
+                        const bool next = t + 1 < w.cnt;
+                        const uint32_t ek = e + C::kParts * (NQ == 2 || t < 0 ? 2 * (t + 1) : 2 * t + 1);
+                        const uint32_t ev = e + C::kParts * value_place<NQ>(t, w.cnt);
+                        if constexpr (NQ == 2) {
+                            if (t >= 0) wait_full(ev);
+                            if (next) wait_full(ek);
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                if (t >= a[i] && t < b[i]) {
+                                    bar_wait(smem_addr(&sh.p_full[i]), step[i] & 1, failed);
+                                    ++step[i];
+                                    tc_after();
+                                    values(256 + i * 128, i * 128, ev, t > a[i]);
+                                    if (t == b[i] - 1) tc_commit(smem_addr(&sh.o_full[i]));
+                                }
+                                if (t + 1 >= a[i] && t + 1 < b[i]) {
+                                    if (t + 1 == a[i]) {
+                                        bar_wait(smem_addr(&sh.q_full[i]), unit[i] & 1, failed);
+                                        ++unit[i];
+                                        tc_after();
+                                    }
+                                    scores(i * 128, i, ek);
+                                    tc_commit(smem_addr(&sh.s_full[i]));
+                                }
+                            }
+                            if (t >= 0) give_back(ev);
+                            if (next) give_back(ek);
+                        } else {
+                            // unit[1] counts the score tiles, step[0] the value tiles
+                            if (next) {
+                                wait_full(ek);
+                                if (t + 1 < b[0]) {
+                                    if (t < 0) {
+                                        bar_wait(smem_addr(&sh.q_full[0]), unit[0] & 1, failed);
+                                        ++unit[0];
+                                        tc_after();
+                                    }
+                                    scores((unit[1] & 1) * 128, 0, ek);
+                                    tc_commit(smem_addr(&sh.s_full[unit[1] & 1]));
+                                    ++unit[1];
+                                }
+                                give_back(ek);
+                            }
+                            if (t >= 0) {
+                                wait_full(ev);
+                                if (t < b[0]) {
+                                    const uint32_t u = step[0]++;
+                                    bar_wait(smem_addr(&sh.p_full[u & 1]), (u >> 1) & 1, failed);
+                                    tc_after();
+                                    values(256, (u & 1) * 128, ev, t > 0);
+                                    tc_commit(smem_addr(&sh.o_full[0]));
+                                }
+                                give_back(ev);
+                            }
+                        }
+                    }
+                    e += 2 * C::kParts * w.cnt;
+                } while (walk_next<M, KT, kTcUC>(p, w));
+            }
+            __syncwarp();
+        } else if (wid == 2) {
+            // ---- values at an edge: rows that no query sees become zero;
+            // infinities and NaN in rows that some see mark the unit
+            uint32_t e = 0, phase = 0, unit = 0;
+            do {
+                for (int t = 0; t < w.cnt; ++t) {
+#pragma unroll 1
+                    for (int h = 0; h < C::kParts; ++h) {
+                        const int j0 = (w.k0 + w.off + t) * KT + h * KE;
+                        if (!is_edge(w, j0, KE)) continue;
+                        const uint32_t st = (e + C::kParts * value_place<NQ>(t, w.cnt) + h) % ST;
+                        bar_wait(smem_addr(&sh.edge[st]), (phase >> st) & 1, failed);
+                        phase ^= 1u << st;
+                        char* v = tiles + NQ * C::kQ + st * C::kBytes;
+                        bool odd = false;
+                        for (int i = lane; i < KE * (DP / 8); i += 32) {
+                            const int r = i / (DP / 8), c = i % (DP / 8);
+                            const int j = j0 + r;
+                            uint4* x = reinterpret_cast<uint4*>(v + panel_at<KE>(r, c));
+                            if (j < w.keys.lo || j >= w.keys.hi) {
+                                *x = make_uint4(0u, 0u, 0u, 0u);
+                            } else if (j < w.keys.flo || j >= w.keys.fhi) {
+                                const uint4 y = *x;
+                                odd |= unbounded<T>(y.x) || unbounded<T>(y.y) || unbounded<T>(y.z) || unbounded<T>(y.w);
+                            }
+                        }
+                        if (__any_sync(0xffffffffu, odd) && lane == 0) atomicOr(&sh.careful, 1u << (unit & 31));
+                        fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(smem_addr(&sh.full[st]));
+                    }
                 }
-                --e;  // the last step has no next key tile
+                e += 2 * C::kParts * w.cnt;
+                ++unit;
             } while (walk_next<M, KT, kTcUC>(p, w));
         }
-        __syncwarp();
-    } else if (wid == 2) {
-        // ---- value tiles at an edge: rows that no query sees become zero;
-        // infinities and NaN in rows that some see mark the unit
-        uint32_t e = 0, phase = 0, unit = 0;
-        do {
-            for (int t = 0; t < w.cnt; ++t) {
-                const int kt = w.k0 + w.off + t;
-                const uint32_t st = (e + 1) % ST;
-                e += 2;
-                if (!is_edge(w, kt)) continue;
-                bar_wait(smem_addr(&sh.edge[st]), (phase >> st) & 1, failed);
-                phase ^= 1u << st;
-                char* v = tiles + 2 * C::kBytes + st * C::kBytes;
-                bool odd = false;
-                for (int i = lane; i < kTile * (DP / 8); i += 32) {
-                    const int r = i / (DP / 8), c = i % (DP / 8);
-                    const int j = kt * KT + r;
-                    uint4* x = reinterpret_cast<uint4*>(v + panel_at(r, c));
-                    if (j < w.keys.lo || j >= w.keys.hi) {
-                        *x = make_uint4(0u, 0u, 0u, 0u);
-                    } else if (j < w.keys.flo || j >= w.keys.fhi) {
-                        const uint4 y = *x;
-                        odd |= unbounded<T>(y.x) || unbounded<T>(y.y) || unbounded<T>(y.z) || unbounded<T>(y.w);
-                    }
-                }
-                if (__any_sync(0xffffffffu, odd) && lane == 0) atomicOr(&sh.careful, 1u << (unit & 31));
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) bar_arrive(smem_addr(&sh.full[st]));
-            }
-            ++unit;
-        } while (walk_next<M, KT, kTcUC>(p, w));
-    }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        if constexpr (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ---- softmax of query tile i, a thread per row
         const int i = (wid - 4) >> 2;
         const int row = tid & 127;
         const uint32_t lanes = (uint32_t)(wid & 3) << 21;  // 32 lanes of TMEM per warp
-        const uint32_t ts = tmem + i * 128 + lanes, to = tmem + 256 + i * 128 + lanes;
-        char* qt = tiles + i * C::kBytes;
+        const uint32_t to = tmem + 256 + i * 128 + lanes;
+        char* qt = tiles + i * C::kQ;
         uint32_t step = 0, done = 0, unit = 0;
         do {
             int a, b;
-            tile_span(p, w, i, a, b);
+            tile_span<NQ>(p, w, i, a, b);
             const int r0 = w.rt * M + i * kTile;
             const int rows = min(w.s.n * p.G - r0, kTile);  // may be <= 0
             float ref = -INFINITY, sum = 0.0f;
@@ -430,13 +510,13 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                     if (r < rows && c * 8 < p.D) {
                         v = __ldg(reinterpret_cast<const uint4*>(p.q + (out_row(p, w.s, w.h, r0 + r) * p.D + c * 8) * 2));
                     }
-                    *reinterpret_cast<uint4*>(qt + panel_at(r, c)) = v;
+                    *reinterpret_cast<uint4*>(qt + panel_at<kTile>(r, c)) = v;
                 }
                 fence_async_smem();
                 tc_before();
                 bar_arrive(smem_addr(&sh.q_full[i]));
             }
-            const Keys keys = tile_keys<kTile>(p, w.s, w.rt * 2 + i);
+            const Keys keys = tile_keys<kTile>(p, w.s, w.rt * NQ + i);
             const int box = p.page_size < kTile ? p.page_size : kTile;
             const int box_shift = 31 - __clz(box);
             for (int t = a; t < b; ++t) {
@@ -448,8 +528,10 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                     gone = j < w.s.L && key_slot(p, w.b, j) < 0;
                 }
                 const uint32_t lost = __ballot_sync(0xffffffffu, gone);
-                bar_wait(smem_addr(&sh.s_full[i]), step & 1, failed);
-                ++step;
+                // two query tiles: each its own S; one: the two S in turn
+                const uint32_t buf = NQ == 2 ? i : step & 1;
+                const uint32_t ts = tmem + buf * 128 + lanes;
+                bar_wait(smem_addr(&sh.s_full[buf]), (NQ == 2 ? step : step >> 1) & 1, failed);
                 tc_after();
                 float s[KT];
 #pragma unroll
@@ -482,8 +564,12 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                     ref = high;
                 } else if (__any_sync(0xffffffffu, high > ref + 8.0f)) {
                     // lazily: the reference moves only when the weights would
-                    // pass 2^8; the products into O before are complete
-                    // (commit of S is behind them)
+                    // pass 2^8.  The products into O before must be complete:
+                    // with two query tiles the commit of S is behind them
+                    if constexpr (NQ == 1) {
+                        bar_wait(smem_addr(&sh.o_full[0]), (step - 1) & 1, failed);
+                        tc_after();
+                    }
                     const float next = fmaxf(ref, high);
                     const float keep = next == -INFINITY ? 1.0f : ex2(ref - next);
                     ref = next;
@@ -518,11 +604,15 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                 sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
                 tc_wait_st();
                 tc_before();
-                bar_arrive(smem_addr(&sh.p_full[i]));
+                // every phase of o_full is waited for, so that a parity names
+                // one phase only
+                if (NQ == 1 && t > a) bar_wait(smem_addr(&sh.o_full[0]), (step - 1) & 1, failed);
+                bar_arrive(smem_addr(&sh.p_full[buf]));
+                ++step;
             }
             // ---- the unit's end
             if (a < b) {
-                bar_wait(smem_addr(&sh.o_full[i]), done & 1, failed);
+                bar_wait(smem_addr(&sh.o_full[i]), (NQ == 2 ? done : step - 1) & 1, failed);
                 ++done;
                 tc_after();
             }
@@ -557,7 +647,7 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                             const T* vr = reinterpret_cast<const T*>(p.v) + (ks * p.hk + w.h) * p.D;
                             float x = 0.0f;
                             for (int d = 0; d < p.D; ++d) {
-                                x = fmaf(to_f(*reinterpret_cast<const T*>(qt + panel_at(row, d >> 3) + (d & 7) * 2)), to_f(kr[d]), x);
+                                x = fmaf(to_f(*reinterpret_cast<const T*>(qt + panel_at<kTile>(row, d >> 3) + (d & 7) * 2)), to_f(kr[d]), x);
                             }
                             x = ex2(fmaf(x, p.scale_log2, ref == -INFINITY ? 0.0f : -ref));
                             x = round_to<T>(x);
@@ -599,9 +689,8 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                 if (slot == 1 && row == 0 && i == 0) write_desc(p, w);
                 tc_before();
             }
-            // both softmax groups are done with the unit's mark; it is cleared
-            // for the unit after the next
-            asm volatile("bar.sync 1, 256;" ::: "memory");
+            // the softmax warps are done with the unit's mark
+            asm volatile("bar.sync 1, %0;" ::"n"(C::kThreads - 128) : "memory");
             if (tid == 128) atomicAnd(&sh.careful, ~(1u << (unit & 31)));
             ++unit;
         } while (walk_next<M, KT, kTcUC>(p, w));
@@ -644,7 +733,8 @@ Encode encoder() {
 bool cache_map(CUtensorMap* map, const AttnP& p, const char* base, int dt) {
     const cuuint64_t dims[3] = {(cuuint64_t)p.D, (cuuint64_t)p.hk, (cuuint64_t)p.num_pages * p.page_size};
     const cuuint64_t strides[2] = {(cuuint64_t)p.D * 2, (cuuint64_t)p.hk * p.D * 2};
-    const cuuint32_t box[3] = {64, 1, (cuuint32_t)(p.page_size < kTile ? p.page_size : kTile)};
+    const int keys = p.D <= 128 ? Tc<128>::kKeys : Tc<256>::kKeys;
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)(p.page_size < keys ? p.page_size : keys)};
     const cuuint32_t ones[3] = {1, 1, 1};
     return encoder()(map, dt == kF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                      const_cast<char*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -657,32 +747,36 @@ cudaError_t launch_typed(const AttnP& p, const CUtensorMap& km, const CUtensorMa
     cudaError_t e = cudaFuncSetAttribute((const void*)attn_tc_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          Tc<DP>::kSmem);
     if (e != cudaSuccess) return e;
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(Tc<DP>::kThreads);
     cfg.dynamicSmemBytes = Tc<DP>::kSmem;
     return cudaLaunchKernelEx(&cfg, attn_tc_kernel<T, DP>, p, km, vm);
 }
 
 }  // namespace
 
-AttnShape tc_shape() { return AttnShape{kPathMany, 2 * kTile, sm_count(), 1}; }
+AttnShape tc_shape(int head_dim) { return AttnShape{kPathMany, head_dim <= 128 ? Tc<128>::kM : Tc<256>::kM, sm_count(), 1}; }
 
-// 16-byte aligned 16-bit tensors of heads of 64 to 128 channels (a multiple of
-// 8); pages of 8, 16, 32, 64 or a multiple of 128 tokens, so that a tile is made
-// of whole boxes of at least one swizzle atom.
+// 16-byte aligned 16-bit tensors of heads of at least 64 channels (a multiple of
+// 8); pages of 8, 16, 32, 64 or a multiple of 128 tokens, so that a ring entry
+// is made of whole boxes of at least one swizzle atom.
 bool tc_suits(const AttnP& p) {
     const bool page = p.page_size % kTile == 0 || (p.page_size >= 8 && p.page_size < kTile && kTile % p.page_size == 0);
-    return page && p.D >= 64 && p.D <= 128 && p.num_pages > 0 &&
+    return page && p.D >= 64 && p.num_pages > 0 &&
            (int64_t)p.num_pages * p.page_size <= (int64_t)INT32_MAX - kTile && encoder() != nullptr;
+}
+
+template <typename T>
+cudaError_t launch_by_size(const AttnP& p, const CUtensorMap& km, const CUtensorMap& vm, cudaLaunchConfig_t cfg) {
+    if (p.D <= 64) return launch_typed<T, 64>(p, km, vm, cfg);
+    if (p.D <= 128) return launch_typed<T, 128>(p, km, vm, cfg);
+    if (p.D <= 192) return launch_typed<T, 192>(p, km, vm, cfg);
+    return launch_typed<T, 256>(p, km, vm, cfg);
 }
 
 cudaError_t launch_attn_tc(const AttnP& p, int dt, cudaLaunchConfig_t cfg) {
     CUtensorMap km, vm;
     if (!cache_map(&km, p, p.k, dt) || !cache_map(&vm, p, p.v, dt)) return cudaErrorInvalidValue;
-    if (dt == kF16) {
-        return p.D <= 64 ? launch_typed<__half, 64>(p, km, vm, cfg) : launch_typed<__half, 128>(p, km, vm, cfg);
-    }
-    return p.D <= 64 ? launch_typed<__nv_bfloat16, 64>(p, km, vm, cfg)
-                     : launch_typed<__nv_bfloat16, 128>(p, km, vm, cfg);
+    return dt == kF16 ? launch_by_size<__half>(p, km, vm, cfg) : launch_by_size<__nv_bfloat16>(p, km, vm, cfg);
 }
 
 }  // namespace edge

@@ -336,7 +336,7 @@ cudaError_t launch_attn_mma(const AttnP& p, const AttnShape& sh, int dt, cudaLau
 
 // The tcgen05 kernel (paged_attn_tc.cu), where tc_suits says that it serves the
 // head and page size.
-AttnShape tc_shape();
+AttnShape tc_shape(int head_dim);
 bool tc_suits(const AttnP& p);
 cudaError_t launch_attn_tc(const AttnP& p, int dt, cudaLaunchConfig_t cfg);
 

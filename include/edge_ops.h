@@ -275,6 +275,56 @@ edge_status edge_rope(void* q_out, void* k_out, edge_dtype out_dt, const void* q
                       const int64_t* positions, const float* cos, const float* sin,
                       int64_t cache_len, float inv_scale, void* stream);
 
+/* How the pairs of a rotary embedding with several axes belong to the axes. */
+typedef enum {
+    EDGE_AXES_BLOCKS = 0, /* sections[0] pairs of axis 0, then those of axis 1, ... */
+    EDGE_AXES_CYCLED = 1  /* dealt in turn: pair j to axis j mod axes while that axis has
+                           * pairs left (j / axes < sections[j mod axes]), else to axis 0 */
+} edge_axis_order;
+
+/*
+ * Rotary positions with several axes (time, height and width of images and
+ * video; text tokens carry the same position on every axis).  The forms of
+ * edge_qk_norm_rope_ex, edge_rope and edge_qkv_rope_cache in which pair j of
+ * the rotary channels turns by cos/sin row positions[axis(j)][t], column j.
+ *
+ * positions: [axes, tokens] int64, device.  A token with any of its positions
+ *            negative or >= cache_len does not rotate, and no cache row is read
+ *            for it.
+ * axes:      1 to 4.
+ * sections:  [axes] pairs of each axis, HOST memory, read during the call;
+ *            together rotary_dim / 2.  EDGE_AXES_CYCLED needs every pair of the
+ *            axes behind the first to exist: (sections[a] - 1) * axes + a <
+ *            rotary_dim / 2.
+ * Otherwise the arguments, results and errors of the forms with one position;
+ * equal positions on every axis give the same values.  EDGE_ERR_NULL: sections
+ * NULL.  EDGE_ERR_SHAPE: axes or sections that do not fit.  EDGE_ERR_VALUE: an
+ * unknown order.
+ */
+edge_status edge_qk_norm_rope_axes(void* q_out, void* k_out, edge_dtype out_dt, const void* q,
+                                   const void* k, const void* wq, const void* wk, edge_dtype dt,
+                                   int64_t tokens, int32_t q_heads, int32_t k_heads,
+                                   int32_t head_dim, int32_t rotary_dim, edge_rope_layout layout,
+                                   const int64_t* positions, int32_t axes, const int32_t* sections,
+                                   edge_axis_order order, const float* cos, const float* sin,
+                                   int64_t cache_len, float eps, int weight_offset,
+                                   float inv_scale, uint32_t flags, void* stream);
+edge_status edge_rope_axes(void* q_out, void* k_out, edge_dtype out_dt, const void* q,
+                           const void* k, edge_dtype dt, int64_t tokens, int32_t q_heads,
+                           int32_t k_heads, int32_t head_dim, int32_t rotary_dim,
+                           edge_rope_layout layout, const int64_t* positions, int32_t axes,
+                           const int32_t* sections, edge_axis_order order, const float* cos,
+                           const float* sin, int64_t cache_len, float inv_scale, void* stream);
+edge_status edge_qkv_rope_cache_axes(void* q_out, void* k_cache, void* v_cache, const void* qkv,
+                                     const void* wq, const void* wk, edge_dtype dt, int64_t tokens,
+                                     int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                     int32_t rotary_dim, edge_rope_layout layout,
+                                     const int64_t* positions, int32_t axes,
+                                     const int32_t* sections, edge_axis_order order,
+                                     const float* cos, const float* sin, int64_t cache_len,
+                                     const int64_t* slots, int64_t num_slots, float eps,
+                                     int weight_offset, int normalize, void* stream);
+
 /*
  * Attention of a chunk of new tokens over a paged KV cache (the reader of the
  * cache that edge_qkv_rope_cache writes).  A chunk of one token per sequence is

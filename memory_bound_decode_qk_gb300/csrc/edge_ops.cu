@@ -181,12 +181,37 @@ edge_status rows_entry(void* out, edge_dtype out_dt, const void* x, void* residu
 
 namespace {
 
+const edge::Axes kOneAxis = {0, 0, {0, 0, 0, 0}};
+
+// The sections of a rotary embedding with several axes.
+edge_status read_axes(int32_t axes, const int32_t* sections, edge_axis_order order,
+                      int32_t rotary_dim, edge::Axes* out) {
+    if (sections == nullptr) return EDGE_ERR_NULL;
+    if (axes < 1 || axes > 4) return EDGE_ERR_SHAPE;
+    if (order != EDGE_AXES_BLOCKS && order != EDGE_AXES_CYCLED) return EDGE_ERR_VALUE;
+    *out = edge::Axes{axes, order == EDGE_AXES_CYCLED, {0, 0, 0, 0}};
+    const int64_t half = rotary_dim / 2;
+    int64_t sum = 0;
+    for (int a = 0; a < axes; ++a) {
+        if (sections[a] < 0) return EDGE_ERR_SHAPE;
+        // dealt in turn, the last pair of every axis but the first is named
+        if (out->cycled && a > 0 && sections[a] > 0 &&
+            ((int64_t)sections[a] - 1) * axes + a >= half) {
+            return EDGE_ERR_SHAPE;
+        }
+        out->count[a] = sections[a];
+        sum += sections[a];
+    }
+    return sum == half ? EDGE_OK : EDGE_ERR_SHAPE;
+}
+
 static edge_status qk_entry(void* q_out, void* k_out, edge_dtype out_dt, const void* q,
                             const void* k, const void* wq, const void* wk, edge_dtype dt,
                             int64_t tokens, int32_t q_heads, int32_t k_heads, int32_t head_dim,
                             int32_t rotary_dim, edge_rope_layout layout, const int64_t* positions,
                             const float* cos, const float* sin, int64_t cache_len, float eps,
-                            int weight_offset, float inv_scale, int mode, void* stream) {
+                            int weight_offset, float inv_scale, int mode, const edge::Axes& axes,
+                            void* stream) {
     edge_status st = check_out_dt(out_dt, dt);
     if (st != EDGE_OK) return st;
     if (q == nullptr || q_out == nullptr) return EDGE_ERR_NULL;
@@ -199,6 +224,7 @@ static edge_status qk_entry(void* q_out, void* k_out, edge_dtype out_dt, const v
     if (!finite_nonneg(eps) || (weight_offset != 0 && weight_offset != 1)) return EDGE_ERR_VALUE;
     if ((st = check_scale(out_dt, inv_scale)) != EDGE_OK) return st;
     const bool may_rotate = rotary_dim > 0 && cache_len > 0;
+    const int64_t per_token = axes.n > 0 ? axes.n : 1;
     if (may_rotate && (positions == nullptr || cos == nullptr || sin == nullptr)) {
         return EDGE_ERR_NULL;
     }
@@ -222,7 +248,7 @@ static edge_status qk_entry(void* q_out, void* k_out, edge_dtype out_dt, const v
     const Span sq = span(q, qb), sk = span(k_heads ? k : nullptr, kb);
     const Span sqo = span(q_out, qob), sko = span(k_heads ? k_out : nullptr, kob);
     const Span ro[] = {span(wq, head_dim * es), span(wk, head_dim * es),
-                       span(may_rotate ? positions : nullptr, tokens * 8),
+                       span(may_rotate ? positions : nullptr, per_token * tokens * 8),
                        span(may_rotate ? cos : nullptr, cb), span(may_rotate ? sin : nullptr, cb)};
     if (bad_alias(sqo, sq, same_dt) || bad_alias(sko, sk, same_dt) || overlap(sqo, sk) ||
         overlap(sko, sq) || overlap(sqo, sko)) {
@@ -256,34 +282,18 @@ static edge_status qk_entry(void* q_out, void* k_out, edge_dtype out_dt, const v
     a.inv_scale = inv_scale;
     a.weight_offset = weight_offset;
     a.mode = mode;
+    a.axes = axes;
     return finish(edge::launch_qk(a, static_cast<cudaStream_t>(stream)));
 }
 
-}  // namespace
-
-extern "C" {
-
-edge_status edge_rmsnorm(void* out, edge_dtype out_dt, const void* x, const void* w, edge_dtype dt,
-                         int64_t rows, int64_t hidden, float eps, int weight_offset,
-                         float inv_scale, void* stream) {
-    return rows_entry(out, out_dt, x, nullptr, false, w, dt, rows, hidden, eps, weight_offset,
-                      inv_scale, stream);
-}
-
-edge_status edge_add_rmsnorm(void* out, edge_dtype out_dt, const void* x, void* residual,
-                             const void* w, edge_dtype dt, int64_t rows, int64_t hidden, float eps,
-                             int weight_offset, float inv_scale, void* stream) {
-    return rows_entry(out, out_dt, x, residual, true, w, dt, rows, hidden, eps, weight_offset,
-                      inv_scale, stream);
-}
-
-edge_status edge_qkv_rope_cache(void* q_out, void* k_cache, void* v_cache, const void* qkv,
-                                const void* wq, const void* wk, edge_dtype dt, int64_t tokens,
-                                int32_t q_heads, int32_t kv_heads, int32_t head_dim,
-                                int32_t rotary_dim, edge_rope_layout layout,
-                                const int64_t* positions, const float* cos, const float* sin,
-                                int64_t cache_len, const int64_t* slots, int64_t num_slots,
-                                float eps, int weight_offset, int normalize, void* stream) {
+static edge_status qkv_entry(void* q_out, void* k_cache, void* v_cache, const void* qkv,
+                             const void* wq, const void* wk, edge_dtype dt, int64_t tokens,
+                             int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                             int32_t rotary_dim, edge_rope_layout layout,
+                             const int64_t* positions, const float* cos, const float* sin,
+                             int64_t cache_len, const int64_t* slots, int64_t num_slots,
+                             float eps, int weight_offset, int normalize, const edge::Axes& axes,
+                             void* stream) {
     if (!act_dtype(dt)) return EDGE_ERR_DTYPE;
     if (qkv == nullptr || q_out == nullptr) return EDGE_ERR_NULL;
     const bool writes_cache = kv_heads > 0 && num_slots > 0;
@@ -304,6 +314,7 @@ edge_status edge_qkv_rope_cache(void* q_out, void* k_cache, void* v_cache, const
     if (may_rotate && (positions == nullptr || cos == nullptr || sin == nullptr)) {
         return EDGE_ERR_NULL;
     }
+    const int64_t per_token = axes.n > 0 ? axes.n : 1;
     const int64_t es = esize(dt);
     const int64_t heads_row = (int64_t)q_heads + 2 * (int64_t)kv_heads;
     int64_t in_b = 0, q_b = 0, c_b = 0, cs_b = 0;
@@ -324,7 +335,7 @@ edge_status edge_qkv_rope_cache(void* q_out, void* k_cache, void* v_cache, const
     const Span sk = span(writes_cache ? k_cache : nullptr, c_b);
     const Span sv = span(writes_cache ? v_cache : nullptr, c_b);
     const Span ro[] = {span(qkv, in_b), span(wq, head_dim * es), span(wk, head_dim * es),
-                       span(may_rotate ? positions : nullptr, tokens * 8),
+                       span(may_rotate ? positions : nullptr, per_token * tokens * 8),
                        span(may_rotate ? cos : nullptr, cs_b), span(may_rotate ? sin : nullptr, cs_b),
                        span(writes_cache ? slots : nullptr, tokens * 8)};
     if (overlap(sq, sk) || overlap(sq, sv) || overlap(sk, sv)) return EDGE_ERR_ALIAS;
@@ -355,10 +366,58 @@ edge_status edge_qkv_rope_cache(void* q_out, void* k_cache, void* v_cache, const
     a.normalize = normalize;
     a.weight_offset = weight_offset;
     a.eps = eps;
+    a.axes = axes;
     bool handled = false;
     cudaError_t e = edge::launch_qkv_cache(a, static_cast<cudaStream_t>(stream), &handled);
     if (e == cudaSuccess && !handled) return EDGE_ERR_UNSUPPORTED;
     return finish(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+edge_status edge_rmsnorm(void* out, edge_dtype out_dt, const void* x, const void* w, edge_dtype dt,
+                         int64_t rows, int64_t hidden, float eps, int weight_offset,
+                         float inv_scale, void* stream) {
+    return rows_entry(out, out_dt, x, nullptr, false, w, dt, rows, hidden, eps, weight_offset,
+                      inv_scale, stream);
+}
+
+edge_status edge_add_rmsnorm(void* out, edge_dtype out_dt, const void* x, void* residual,
+                             const void* w, edge_dtype dt, int64_t rows, int64_t hidden, float eps,
+                             int weight_offset, float inv_scale, void* stream) {
+    return rows_entry(out, out_dt, x, residual, true, w, dt, rows, hidden, eps, weight_offset,
+                      inv_scale, stream);
+}
+
+edge_status edge_qkv_rope_cache(void* q_out, void* k_cache, void* v_cache, const void* qkv,
+                                const void* wq, const void* wk, edge_dtype dt, int64_t tokens,
+                                int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                int32_t rotary_dim, edge_rope_layout layout,
+                                const int64_t* positions, const float* cos, const float* sin,
+                                int64_t cache_len, const int64_t* slots, int64_t num_slots,
+                                float eps, int weight_offset, int normalize, void* stream) {
+    return qkv_entry(q_out, k_cache, v_cache, qkv, wq, wk, dt, tokens, q_heads, kv_heads, head_dim,
+                     rotary_dim, layout, positions, cos, sin, cache_len, slots, num_slots, eps,
+                     weight_offset, normalize, kOneAxis, stream);
+}
+
+edge_status edge_qkv_rope_cache_axes(void* q_out, void* k_cache, void* v_cache, const void* qkv,
+                                     const void* wq, const void* wk, edge_dtype dt, int64_t tokens,
+                                     int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                     int32_t rotary_dim, edge_rope_layout layout,
+                                     const int64_t* positions, int32_t axes,
+                                     const int32_t* sections, edge_axis_order order,
+                                     const float* cos, const float* sin, int64_t cache_len,
+                                     const int64_t* slots, int64_t num_slots, float eps,
+                                     int weight_offset, int normalize, void* stream) {
+    edge::Axes ax;
+    const edge_status st = read_axes(axes, sections, order, rotary_dim, &ax);
+    if (st != EDGE_OK) return st;
+    return qkv_entry(q_out, k_cache, v_cache, qkv, wq, wk, dt, tokens, q_heads, kv_heads, head_dim,
+                     rotary_dim, layout, positions, cos, sin, cache_len, slots, num_slots, eps,
+                     weight_offset, normalize, ax, stream);
 }
 
 edge_status edge_layernorm(void* out, edge_dtype out_dt, const void* x, const void* gamma,
@@ -463,7 +522,7 @@ edge_status edge_qk_norm_rope(void* q_out, void* k_out, edge_dtype out_dt, const
                               void* stream) {
     return qk_entry(q_out, k_out, out_dt, q, k, wq, wk, dt, tokens, q_heads, k_heads, head_dim,
                     rotary_dim, layout, positions, cos, sin, cache_len, eps, weight_offset,
-                    inv_scale, 1 /* normalize */, stream);
+                    inv_scale, 1 /* normalize */, kOneAxis, stream);
 }
 
 edge_status edge_qk_norm_rope_ex(void* q_out, void* k_out, edge_dtype out_dt, const void* q,
@@ -477,7 +536,39 @@ edge_status edge_qk_norm_rope_ex(void* q_out, void* k_out, edge_dtype out_dt, co
     const int mode = 1 | ((flags & EDGE_QK_ROTATE_UNROUNDED) ? 2 : 0);
     return qk_entry(q_out, k_out, out_dt, q, k, wq, wk, dt, tokens, q_heads, k_heads, head_dim,
                     rotary_dim, layout, positions, cos, sin, cache_len, eps, weight_offset,
-                    inv_scale, mode, stream);
+                    inv_scale, mode, kOneAxis, stream);
+}
+
+edge_status edge_qk_norm_rope_axes(void* q_out, void* k_out, edge_dtype out_dt, const void* q,
+                                   const void* k, const void* wq, const void* wk, edge_dtype dt,
+                                   int64_t tokens, int32_t q_heads, int32_t k_heads,
+                                   int32_t head_dim, int32_t rotary_dim, edge_rope_layout layout,
+                                   const int64_t* positions, int32_t axes, const int32_t* sections,
+                                   edge_axis_order order, const float* cos, const float* sin,
+                                   int64_t cache_len, float eps, int weight_offset,
+                                   float inv_scale, uint32_t flags, void* stream) {
+    if ((flags & ~(uint32_t)EDGE_QK_ROTATE_UNROUNDED) != 0) return EDGE_ERR_VALUE;
+    edge::Axes ax;
+    const edge_status st = read_axes(axes, sections, order, rotary_dim, &ax);
+    if (st != EDGE_OK) return st;
+    const int mode = 1 | ((flags & EDGE_QK_ROTATE_UNROUNDED) ? 2 : 0);
+    return qk_entry(q_out, k_out, out_dt, q, k, wq, wk, dt, tokens, q_heads, k_heads, head_dim,
+                    rotary_dim, layout, positions, cos, sin, cache_len, eps, weight_offset,
+                    inv_scale, mode, ax, stream);
+}
+
+edge_status edge_rope_axes(void* q_out, void* k_out, edge_dtype out_dt, const void* q,
+                           const void* k, edge_dtype dt, int64_t tokens, int32_t q_heads,
+                           int32_t k_heads, int32_t head_dim, int32_t rotary_dim,
+                           edge_rope_layout layout, const int64_t* positions, int32_t axes,
+                           const int32_t* sections, edge_axis_order order, const float* cos,
+                           const float* sin, int64_t cache_len, float inv_scale, void* stream) {
+    edge::Axes ax;
+    const edge_status st = read_axes(axes, sections, order, rotary_dim, &ax);
+    if (st != EDGE_OK) return st;
+    return qk_entry(q_out, k_out, out_dt, q, k, nullptr, nullptr, dt, tokens, q_heads, k_heads,
+                    head_dim, rotary_dim, layout, positions, cos, sin, cache_len, 0.0f, 0,
+                    inv_scale, 0 /* rotate only */, ax, stream);
 }
 
 edge_status edge_rope(void* q_out, void* k_out, edge_dtype out_dt, const void* q, const void* k,
@@ -487,7 +578,7 @@ edge_status edge_rope(void* q_out, void* k_out, edge_dtype out_dt, const void* q
                       int64_t cache_len, float inv_scale, void* stream) {
     return qk_entry(q_out, k_out, out_dt, q, k, nullptr, nullptr, dt, tokens, q_heads, k_heads,
                     head_dim, rotary_dim, layout, positions, cos, sin, cache_len, 0.0f, 0,
-                    inv_scale, 0 /* rotate only */, stream);
+                    inv_scale, 0 /* rotate only */, kOneAxis, stream);
 }
 
 int64_t edge_paged_attention_workspace(edge_dtype dt, int32_t q_heads, int32_t kv_heads,

@@ -10,6 +10,14 @@ namespace edge {
 
 enum Dt { kF32 = 0, kF16 = 1, kBF16 = 2, kFP8 = 3 };
 
+// Rotary positions with several axes: pair j of the rotary channels turns by
+// the position of its axis.  n = 0: one position per token.
+struct Axes {
+    int n;          // axes, 0 or 1 .. 4
+    int cycled;     // pairs dealt in turn instead of in blocks
+    int count[4];   // pairs of each axis
+};
+
 struct QKArgs {
     const void* q;
     const void* k;
@@ -27,6 +35,7 @@ struct QKArgs {
     float eps, inv_scale;
     int weight_offset;
     int mode;                // kModeNorm (1) | kModeUnrounded (2), qk_common.cuh
+    Axes axes;
 };
 
 struct RowsArgs {
@@ -76,6 +85,7 @@ struct QKVArgs {
     int q_heads, kv_heads, head_dim, rotary_dim, layout, dt;
     int normalize, weight_offset;
     float eps;
+    Axes axes;
 };
 // *handled is false when the geometry or alignment has no vector path.
 cudaError_t launch_qkv_cache(const QKVArgs& a, cudaStream_t s, bool* handled);

@@ -38,7 +38,56 @@ struct QKP {
     int in_bytes, out_bytes;  // element sizes of input and output
     float eps, delta, inv, invD;  // invD = 1 / head_dim (fp32)
     int mode;                     // kModeNorm | kModeUnrounded
+    // several axes (the AXES kernels): positions of axis a at pos + a * tokens
+    int axes, cycled;
+    int axis_end[4];              // blocks: first pair behind axis a; cycled: pairs of axis a
 };
+
+__host__ inline void set_axes(QKP& p, const Axes& ax) {
+    p.axes = ax.n;
+    p.cycled = ax.cycled;
+    int end = 0;
+    for (int a = 0; a < 4; ++a) {
+        end += a < ax.n ? ax.count[a] : 0;
+        p.axis_end[a] = ax.cycled ? (a < ax.n ? ax.count[a] : 0) : end;
+    }
+}
+
+// Positions of one token on every axis, and whether all of them are in the
+// cache (a token with one outside does not rotate and reads no cache row).
+struct AxisPos {
+    int64_t at[4];
+    bool in;
+};
+
+__device__ __forceinline__ AxisPos load_axis_pos(const QKP& p, int64_t t) {
+    AxisPos r;
+    r.in = true;
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+        r.at[a] = a < p.axes ? __ldg(p.pos + a * p.tokens + t) : 0;
+        r.in = r.in && r.at[a] >= 0 && r.at[a] < p.cache_len;
+    }
+    return r;
+}
+
+// Axis of pair j.  Blocks: the sections one after the other.  Cycled: axis j mod
+// n while that axis has pairs left, else axis 0.
+__device__ __forceinline__ int pair_axis(const QKP& p, int j) {
+    if (p.cycled) {
+        const int turn = p.axes == 3 ? j / 3 : p.axes == 2 ? j >> 1 : p.axes == 4 ? j >> 2 : j;
+        const int a = j - turn * p.axes;
+        const int have = a == 0 ? 0 : a == 1 ? p.axis_end[1] : a == 2 ? p.axis_end[2] : p.axis_end[3];
+        return turn < have ? a : 0;
+    }
+    return (j >= p.axis_end[0]) + (j >= p.axis_end[1]) + (j >= p.axis_end[2]);
+}
+
+__device__ __forceinline__ int64_t axis_row(const QKP& p, const AxisPos& x, int j) {
+    const int a = pair_axis(p, j);
+    const int64_t at = a == 0 ? x.at[0] : a == 1 ? x.at[1] : a == 2 ? x.at[2] : x.at[3];
+    return at * p.half + j;
+}
 
 struct Unit {
     const char* src;
@@ -145,6 +194,37 @@ __device__ __forceinline__ void load_cache(const QKP& p, int64_t pos, int sub, i
             float4 cc = __ldg(c4 + v), sv = __ldg(s4 + v);
             cr.c[4 * v] = cc.x; cr.c[4 * v + 1] = cc.y; cr.c[4 * v + 2] = cc.z; cr.c[4 * v + 3] = cc.w;
             cr.s[4 * v] = sv.x; cr.s[4 * v + 1] = sv.y; cr.s[4 * v + 2] = sv.z; cr.s[4 * v + 3] = sv.w;
+        }
+    }
+}
+
+// load_cache for several axes: four pairs at a time, as one vector where they
+// have one axis, else pair by pair (L1 hits: the heads of a token share the
+// rows).
+template <typename T, int LAYOUT>
+__device__ __forceinline__ void load_cache_axes(const QKP& p, const AxisPos& x, int sub, int role,
+                                                CacheRegs<T, LAYOUT>& cr) {
+    constexpr int N = vec_elems<T>();
+    constexpr int n = CacheRegs<T, LAYOUT>::kCount;
+    constexpr int G = n < 4 ? n : 4;
+    const int e0 = sub * N;
+    const int j0 = LAYOUT == kInterleaved ? e0 / 2 : (role == 1 ? e0 : e0 - p.half);
+#pragma unroll
+    for (int g = 0; g < n; g += G) {
+        const int j = j0 + g;
+        if (G == 4 && !p.cycled && pair_axis(p, j) == pair_axis(p, j + 3)) {
+            const int64_t e = axis_row(p, x, j);
+            const float4 c4 = __ldg(reinterpret_cast<const float4*>(p.cs + e));
+            const float4 s4 = __ldg(reinterpret_cast<const float4*>(p.sn + e));
+            cr.c[g] = c4.x; cr.c[g + 1] = c4.y; cr.c[g + 2 < n ? g + 2 : 0] = c4.z; cr.c[g + 3 < n ? g + 3 : 0] = c4.w;
+            cr.s[g] = s4.x; cr.s[g + 1] = s4.y; cr.s[g + 2 < n ? g + 2 : 0] = s4.z; cr.s[g + 3 < n ? g + 3 : 0] = s4.w;
+        } else {
+#pragma unroll
+            for (int k = 0; k < G; ++k) {
+                const int64_t e = axis_row(p, x, j + k);
+                cr.c[g + k] = __ldg(p.cs + e);
+                cr.s[g + k] = __ldg(p.sn + e);
+            }
         }
     }
 }
@@ -363,7 +443,7 @@ __device__ __forceinline__ float ld_elem(const char* base, int i) {
 // in the unrounded mode.  The first p.rot channels rotate when token t's
 // position is inside the cache.  Every output is rounded once to T (or takes
 // the FP8 epilogue).
-template <typename T, bool FP8>
+template <typename T, bool FP8, bool AXES = false>
 __device__ void generic_head(const QKP& p, const char* src, char* dst, const char* w, int64_t t,
                              bool norm, float* hm, int lane, int layout) {
     float ss = 0.0f;
@@ -384,8 +464,17 @@ __device__ void generic_head(const QKP& p, const char* src, char* dst, const cha
     }
     __syncwarp();
     int64_t pos = -1;
-    if (p.rot > 0) pos = p.pos[t];
-    const bool rot = pos >= 0 && pos < p.cache_len;
+    bool rot = false;
+    AxisPos ap;
+    if constexpr (AXES) {
+        if (p.rot > 0) {
+            ap = load_axis_pos(p, t);
+            rot = ap.in;
+        }
+    } else {
+        if (p.rot > 0) pos = p.pos[t];
+        rot = pos >= 0 && pos < p.cache_len;
+    }
     for (int e = lane; e < p.D; e += 32) {
         float y = round_to<T>(hm[e]);
         if (rot && e < p.rot) {
@@ -400,8 +489,10 @@ __device__ void generic_head(const QKP& p, const char* src, char* dst, const cha
                 j = first ? e : e - p.half;
                 partner = first ? e + p.half : e - p.half;
             }
-            const float c = p.cs[pos * p.half + j];
-            const float sn = p.sn[pos * p.half + j];
+            int64_t at = pos * p.half + j;
+            if constexpr (AXES) at = axis_row(p, ap, j);
+            const float c = p.cs[at];
+            const float sn = p.sn[at];
             const float own = hm[e], other = hm[partner];
             y = first ? __fmaf_rn(own, c, -__fmul_rn(other, sn))
                       : __fmaf_rn(own, c, __fmul_rn(other, sn));

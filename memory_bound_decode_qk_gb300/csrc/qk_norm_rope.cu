@@ -43,7 +43,8 @@ namespace {
 // address hint for the row, to save that second round trip, was 0.03 to
 // 0.26 us slower per launch from T = 1 to 128, and so was a grid-stride loop
 // over the heads.)
-template <typename T, bool FP8, int LPH, int LAYOUT>
+// AXES: several positions per token; each lane picks its pairs' cache rows.
+template <typename T, bool FP8, int LPH, int LAYOUT, bool AXES = false>
 __global__ void __launch_bounds__(256) qk_vec_kernel(QKP p) {
     constexpr int N = vec_elems<T>();
     constexpr int HPW = 32 / LPH;
@@ -64,16 +65,28 @@ __global__ void __launch_bounds__(256) qk_vec_kernel(QKP p) {
     const int lane_role = p.rot > 0 ? rotary_role<T, LAYOUT>(p, sub) : 0;
     uint4 raw = make_uint4(0u, 0u, 0u, 0u);
     int64_t pos = -1;
+    AxisPos ap;
+    ap.in = false;
     if (active) {
         raw = __ldcs(reinterpret_cast<const uint4*>(un.src) + sub);
-        if (p.rot > 0) pos = __ldg(p.pos + un.t);
+        if constexpr (AXES) {
+            if (p.rot > 0) ap = load_axis_pos(p, un.t);
+        } else {
+            if (p.rot > 0) pos = __ldg(p.pos + un.t);
+        }
     }
     float w[N];
     weights_plus_delta<T>(p, un.w, sub, w);
-    const bool rot = active && pos >= 0 && pos < p.cache_len;
+    const bool rot = AXES ? ap.in : active && pos >= 0 && pos < p.cache_len;
     const int role = rot ? lane_role : 0;
     CacheRegs<T, LAYOUT> cr;
-    if (role != 0) load_cache<T, LAYOUT>(p, pos, sub, role, cr);
+    if (role != 0) {
+        if constexpr (AXES) {
+            load_cache_axes<T, LAYOUT>(p, ap, sub, role, cr);
+        } else {
+            load_cache<T, LAYOUT>(p, pos, sub, role, cr);
+        }
+    }
     qk_core<T, FP8, LPH, LAYOUT>(p, un.dst, active, lane, sub, raw, w, role, cr);
 }
 
@@ -123,7 +136,7 @@ __global__ void __launch_bounds__(256) qk_vec2_kernel(QKP p) {
 
 // ---------------------------------------------------------------- generic path
 
-template <typename T, bool FP8>
+template <typename T, bool FP8, bool AXES = false>
 __global__ void __launch_bounds__(128) qk_generic_kernel(QKP p, int layout) {
     extern __shared__ float smem[];
     const int lane = threadIdx.x & 31;
@@ -137,8 +150,8 @@ __global__ void __launch_bounds__(128) qk_generic_kernel(QKP p, int layout) {
 
     for (uint32_t u = warp; u < p.units; u += nwarps) {
         const Unit un = locate(p, u);
-        generic_head<T, FP8>(p, un.src, un.dst, un.w, un.t, (p.mode & kModeNorm) != 0, hm, lane,
-                             layout);
+        generic_head<T, FP8, AXES>(p, un.src, un.dst, un.w, un.t, (p.mode & kModeNorm) != 0, hm,
+                                   lane, layout);
     }
 }
 
@@ -147,7 +160,11 @@ __global__ void __launch_bounds__(128) qk_generic_kernel(QKP p, int layout) {
 using QKFn = void (*)(QKP);
 
 template <typename T, bool FP8, int LPH>
-QKFn vec_fn(int layout) {
+QKFn vec_fn(int layout, bool axes) {
+    if (axes) {
+        return layout == kInterleaved ? qk_vec_kernel<T, FP8, LPH, kInterleaved, true>
+                                      : qk_vec_kernel<T, FP8, LPH, kRotateHalf, true>;
+    }
     return layout == kInterleaved ? qk_vec_kernel<T, FP8, LPH, kInterleaved>
                                   : qk_vec_kernel<T, FP8, LPH, kRotateHalf>;
 }
@@ -156,6 +173,7 @@ template <typename T, bool FP8>
 cudaError_t launch_typed(const QKArgs& a, QKP& p, cudaStream_t s) {
     constexpr int N = vec_elems<T>();
     const int D = a.head_dim;
+    const bool axes = a.axes.n > 0 && a.rotary_dim > 0;
     const int nvec = (D * (int)sizeof(T)) % 16 == 0 ? D * (int)sizeof(T) / 16 : 0;
     auto aligned = [](const void* ptr, uintptr_t n) {
         return ptr == nullptr || (reinterpret_cast<uintptr_t>(ptr) % n) == 0;
@@ -185,12 +203,12 @@ cudaError_t launch_typed(const QKArgs& a, QKP& p, cudaStream_t s) {
         const int hpw = 32 / lph;
         QKFn vfn = nullptr;
         switch (lph) {
-            case 1: vfn = vec_fn<T, FP8, 1>(a.layout); break;
-            case 2: vfn = vec_fn<T, FP8, 2>(a.layout); break;
-            case 4: vfn = vec_fn<T, FP8, 4>(a.layout); break;
-            case 8: vfn = vec_fn<T, FP8, 8>(a.layout); break;
-            case 16: vfn = vec_fn<T, FP8, 16>(a.layout); break;
-            default: vfn = vec_fn<T, FP8, 32>(a.layout); break;
+            case 1: vfn = vec_fn<T, FP8, 1>(a.layout, axes); break;
+            case 2: vfn = vec_fn<T, FP8, 2>(a.layout, axes); break;
+            case 4: vfn = vec_fn<T, FP8, 4>(a.layout, axes); break;
+            case 8: vfn = vec_fn<T, FP8, 8>(a.layout, axes); break;
+            case 16: vfn = vec_fn<T, FP8, 16>(a.layout, axes); break;
+            default: vfn = vec_fn<T, FP8, 32>(a.layout, axes); break;
         }
         // decode-width path: one head per lane group, a one-shot grid (on
         // GB300 many short CTAs that each issue one round of loads keep more
@@ -215,10 +233,10 @@ cudaError_t launch_typed(const QKArgs& a, QKP& p, cudaStream_t s) {
         // fills one balanced wave (by 6-8%); two vectors win elsewhere up to
         // w = 1.6 (by 8-18%, over four threads per head from w = 1); four
         // threads per head beyond.
-        const bool two = sizeof(T) == 2 && hbytes == 512 && a.layout == kRotateHalf &&
+        const bool two = !axes && sizeof(T) == 2 && hbytes == 512 && a.layout == kRotateHalf &&
                          a.rotary_dim <= D / 2 && (a.mode & kModeUnrounded) == 0;
         const double w = (double)blocks / (double)(resident_ctas((const void*)vfn, threads) * sms);
-        const bool take_quad = two ? w > 1.6 : (double)blocks > wave;
+        const bool take_quad = !axes && (two ? w > 1.6 : (double)blocks > wave);
         if (take_quad && quad_suits(a.layout, a.rotary_dim, hbytes)) {
             bool handled = false;
             cudaError_t e = launch_qk_quad<T, FP8>(a, p, cfg, &handled);
@@ -249,12 +267,13 @@ cudaError_t launch_typed(const QKArgs& a, QKP& p, cudaStream_t s) {
     cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
+    void (*gfn)(QKP, int) = axes ? qk_generic_kernel<T, FP8, true> : qk_generic_kernel<T, FP8, false>;
     if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(qk_generic_kernel<T, FP8>,
+        cudaError_t e = cudaFuncSetAttribute((const void*)gfn,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    return cudaLaunchKernelEx(&cfg, qk_generic_kernel<T, FP8>, p, a.layout);
+    return cudaLaunchKernelEx(&cfg, gfn, p, a.layout);
 }
 
 }  // namespace
@@ -295,6 +314,7 @@ cudaError_t launch_qk(const QKArgs& args, cudaStream_t s) {
     p.inv = a.inv_scale;
     p.invD = 1.0f / (float)a.head_dim;
     p.mode = a.mode;
+    set_axes(p, a.axes);
     const bool fp8 = a.out_dt == kFP8;
     switch (a.dt) {
         case kF32:

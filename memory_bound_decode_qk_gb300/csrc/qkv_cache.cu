@@ -25,7 +25,8 @@
 namespace edge {
 namespace {
 
-template <typename T, int LPH, int LAYOUT>
+// AXES: several positions per token, as in the prologue.
+template <typename T, int LPH, int LAYOUT, bool AXES = false>
 __global__ void __launch_bounds__(256) qkv_vec_kernel(QKVP a) {
     constexpr int N = vec_elems<T>();
     constexpr int HPW = 32 / LPH;
@@ -60,9 +61,15 @@ __global__ void __launch_bounds__(256) qkv_vec_kernel(QKVP a) {
     const int lane_role = p.rot > 0 ? rotary_role<T, LAYOUT>(p, sub) : 0;
     uint4 raw = make_uint4(0u, 0u, 0u, 0u);
     int64_t pos = -1, slot = -1;
+    AxisPos ap;
+    ap.in = false;
     if (active) {
         raw = __ldcs(reinterpret_cast<const uint4*>(src) + sub);
-        if (p.rot > 0 && !isv) pos = __ldg(p.pos + t);
+        if constexpr (AXES) {
+            if (p.rot > 0 && !isv) ap = load_axis_pos(p, t);
+        } else {
+            if (p.rot > 0 && !isv) pos = __ldg(p.pos + t);
+        }
         if (!isq && a.slots != nullptr) slot = __ldg(a.slots + t);
     }
     char* dst = nullptr;
@@ -73,10 +80,16 @@ __global__ void __launch_bounds__(256) qkv_vec_kernel(QKVP a) {
     }
     float w[N];
     weights_plus_delta<T>(p, isq ? p.wq : p.wk, sub, w);
-    const bool rot = active && !isv && pos >= 0 && pos < p.cache_len;
+    const bool rot = AXES ? ap.in : active && !isv && pos >= 0 && pos < p.cache_len;
     const int role = rot ? lane_role : 0;
     CacheRegs<T, LAYOUT> cr;
-    if (role != 0) load_cache<T, LAYOUT>(p, pos, sub, role, cr);
+    if (role != 0) {
+        if constexpr (AXES) {
+            load_cache_axes<T, LAYOUT>(p, ap, sub, role, cr);
+        } else {
+            load_cache<T, LAYOUT>(p, pos, sub, role, cr);
+        }
+    }
     qk_core<T, false, LPH, LAYOUT>(p, dst, active && dst != nullptr, lane, sub, raw, w, role, cr,
                                    isv);
 }
@@ -144,7 +157,7 @@ __global__ void __launch_bounds__(256, 4) qkv_vec2_kernel(QKVP a) {
 }
 
 // Any head size or alignment: one warp per head, staged in shared memory.
-template <typename T>
+template <typename T, bool AXES = false>
 __global__ void __launch_bounds__(128) qkv_generic_kernel(QKVP a, int layout) {
     extern __shared__ float qkv_smem[];
     const QKP& p = a.p;
@@ -179,14 +192,18 @@ __global__ void __launch_bounds__(128) qkv_generic_kernel(QKVP a, int layout) {
                 reinterpret_cast<T*>(dst)[e] = reinterpret_cast<const T*>(src)[e];
             }
         } else {
-            generic_head<T, false>(p, src, dst, isq ? p.wq : p.wk, t, (p.mode & kModeNorm) != 0,
-                                   hm, lane, layout);
+            generic_head<T, false, AXES>(p, src, dst, isq ? p.wq : p.wk, t,
+                                         (p.mode & kModeNorm) != 0, hm, lane, layout);
         }
     }
 }
 
 template <typename T, int LPH>
-void (*qkv_vec_fn(int layout))(QKVP) {
+void (*qkv_vec_fn(int layout, bool axes))(QKVP) {
+    if (axes) {
+        return layout == kInterleaved ? qkv_vec_kernel<T, LPH, kInterleaved, true>
+                                      : qkv_vec_kernel<T, LPH, kRotateHalf, true>;
+    }
     return layout == kInterleaved ? qkv_vec_kernel<T, LPH, kInterleaved>
                                   : qkv_vec_kernel<T, LPH, kRotateHalf>;
 }
@@ -196,6 +213,7 @@ cudaError_t launch_typed(const QKVArgs& a, QKVP& k, cudaStream_t s, bool* handle
     constexpr int N = vec_elems<T>();
     *handled = false;
     const int D = a.head_dim;
+    const bool axes = a.axes.n > 0 && k.p.rot > 0;
     const int nvec = (D * (int)sizeof(T)) % 16 == 0 ? D * (int)sizeof(T) / 16 : 0;
     auto aligned = [](const void* ptr, uintptr_t n) {
         return ptr == nullptr || (reinterpret_cast<uintptr_t>(ptr) % n) == 0;
@@ -227,24 +245,25 @@ cudaError_t launch_typed(const QKVArgs& a, QKVP& k, cudaStream_t s, bool* handle
         cfg.gridDim = dim3((unsigned)blocks);
         cfg.blockDim = dim3(threads);
         cfg.dynamicSmemBytes = smem;
+        void (*gfn)(QKVP, int) = axes ? qkv_generic_kernel<T, true> : qkv_generic_kernel<T, false>;
         if (smem > 48 * 1024) {
-            cudaError_t e = cudaFuncSetAttribute(qkv_generic_kernel<T>,
+            cudaError_t e = cudaFuncSetAttribute((const void*)gfn,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  (int)smem);
             if (e != cudaSuccess) return e;
         }
-        return cudaLaunchKernelEx(&cfg, qkv_generic_kernel<T>, k, a.layout);
+        return cudaLaunchKernelEx(&cfg, gfn, k, a.layout);
     }
     const int lph = nvec;
     const int hpw = 32 / lph;
     void (*vfn)(QKVP) = nullptr;
     switch (lph) {
-        case 1: vfn = qkv_vec_fn<T, 1>(a.layout); break;
-        case 2: vfn = qkv_vec_fn<T, 2>(a.layout); break;
-        case 4: vfn = qkv_vec_fn<T, 4>(a.layout); break;
-        case 8: vfn = qkv_vec_fn<T, 8>(a.layout); break;
-        case 16: vfn = qkv_vec_fn<T, 16>(a.layout); break;
-        default: vfn = qkv_vec_fn<T, 32>(a.layout); break;
+        case 1: vfn = qkv_vec_fn<T, 1>(a.layout, axes); break;
+        case 2: vfn = qkv_vec_fn<T, 2>(a.layout, axes); break;
+        case 4: vfn = qkv_vec_fn<T, 4>(a.layout, axes); break;
+        case 8: vfn = qkv_vec_fn<T, 8>(a.layout, axes); break;
+        case 16: vfn = qkv_vec_fn<T, 16>(a.layout, axes); break;
+        default: vfn = qkv_vec_fn<T, 32>(a.layout, axes); break;
     }
     const int threads = 256;
     const int64_t per_block = (int64_t)(threads / 32) * hpw;
@@ -256,10 +275,10 @@ cudaError_t launch_typed(const QKVArgs& a, QKVP& k, cudaStream_t s, bool* handle
     // (one vector to 0.25 and from 0.8 to 1, two vectors elsewhere up to 1.6,
     // four threads per head beyond)
     const int64_t wave = (int64_t)resident_ctas((const void*)vfn, threads) * sm_count();
-    const bool two = sizeof(T) == 2 && D * (int)sizeof(T) == 512 && a.layout == kRotateHalf &&
+    const bool two = !axes && sizeof(T) == 2 && D * (int)sizeof(T) == 512 && a.layout == kRotateHalf &&
                      k.p.rot <= D / 2;
     const double w = (double)blocks / (double)wave;
-    const bool take_quad = two ? w > 1.6 : blocks > wave;
+    const bool take_quad = !axes && (two ? w > 1.6 : blocks > wave);
     if (take_quad && quad_suits(a.layout, k.p.rot, (int64_t)D * (int64_t)sizeof(T))) {
         bool quad = false;
         cudaError_t e = launch_qkv_quad<T>(a, k, cfg, &quad);
@@ -315,6 +334,7 @@ cudaError_t launch_qkv_cache(const QKVArgs& a, cudaStream_t s, bool* handled) {
     p.inv = 1.0f;
     p.invD = 1.0f / (float)a.head_dim;
     p.mode = a.normalize ? kModeNorm : 0;
+    set_axes(p, a.axes);
     k.kc = static_cast<char*>(a.k_cache);
     k.vc = static_cast<char*>(a.v_cache);
     k.slots = a.slots;

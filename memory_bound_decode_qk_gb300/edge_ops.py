@@ -18,6 +18,7 @@ from . import _build
 F32, F16, BF16, FP8_E4M3 = 0, 1, 2, 3
 ROTATE_HALF, INTERLEAVED = 0, 1
 SILU, GELU_TANH = 0, 1
+AXES_BLOCKS, AXES_CYCLED = 0, 1
 
 STATUS = {
     0: "EDGE_OK", 1: "EDGE_ERR_NULL", 2: "EDGE_ERR_DTYPE", 3: "EDGE_ERR_SHAPE",
@@ -27,6 +28,7 @@ STATUS = {
 EXPORTS = ("edge_rmsnorm", "edge_add_rmsnorm", "edge_glu_act", "edge_qk_norm_rope",
            "edge_qk_norm_rope_ex", "edge_rope", "edge_layernorm", "edge_quantize_fp8",
            "edge_qkv_rope_cache", "edge_copy",
+           "edge_qk_norm_rope_axes", "edge_rope_axes", "edge_qkv_rope_cache_axes",
            "edge_paged_attention", "edge_paged_attention_workspace",
            "edge_status_str", "edge_last_cuda_error", "edge_version")
 QK_ROTATE_UNROUNDED = 1
@@ -80,6 +82,14 @@ def lib(build_if_missing: bool = False) -> ctypes.CDLL:
     for name in ("edge_rmsnorm", "edge_add_rmsnorm", "edge_glu_act", "edge_qk_norm_rope",
                  "edge_qk_norm_rope_ex", "edge_rope", "edge_layernorm", "edge_quantize_fp8",
                  "edge_qkv_rope_cache", "edge_copy"):
+        getattr(L, name).restype = I
+    L.edge_qk_norm_rope_axes.argtypes = [P, P, I, P, P, P, P, I, I64, I32, I32, I32, I32, I, P,
+                                         I32, P, I, P, P, I64, F, I, F, ctypes.c_uint32, P]
+    L.edge_rope_axes.argtypes = [P, P, I, P, P, I, I64, I32, I32, I32, I32, I, P, I32, P, I, P, P,
+                                 I64, F, P]
+    L.edge_qkv_rope_cache_axes.argtypes = [P, P, P, P, P, P, I, I64, I32, I32, I32, I32, I, P, I32,
+                                           P, I, P, P, I64, P, I64, F, I, I, P]
+    for name in ("edge_qk_norm_rope_axes", "edge_rope_axes", "edge_qkv_rope_cache_axes"):
         getattr(L, name).restype = I
     L.edge_paged_attention.argtypes = [P, I, P, P, P, P, I, I64, I32, I32, I32, I64, I32, P, I32,
                                        I32, P, P, F, I, I32, F, P, I64, P]
@@ -203,11 +213,23 @@ def quantize_fp8(x, inv_scale, *, out=None, stream=None):
     return out
 
 
+def _axis_args(sections, axis_order, positions, tokens):
+    """(axes, sections array, order) of a rotary embedding with several axes."""
+    order = {"blocks": AXES_BLOCKS, "cycled": AXES_CYCLED}.get(axis_order, axis_order)
+    n = len(sections)
+    if positions is not None and (positions.dtype != torch.int64 or
+                                  tuple(positions.shape) != (n, tokens)):
+        raise ValueError(f"positions must be int64 [{n}, {tokens}] for {n} sections")
+    return n, (ctypes.c_int32 * n)(*sections), order
+
+
 def qkv_rope_cache(qkv, q_heads, kv_heads, wq, wk, positions, cos, sin, slots, k_cache, v_cache,
                    *, rotary_dim=None, layout=ROTATE_HALF, eps=1e-6, weight_offset=0,
-                   normalize=True, q_out=None, cache_len=None, stream=None):
+                   normalize=True, q_out=None, cache_len=None, stream=None, sections=None,
+                   axis_order="blocks"):
     """Fused QKV split + prologue + KV-cache write.  qkv: [T, (Hq + 2 Hk) D];
-    k_cache, v_cache: [S, Hk, D] (written at rows slots[t]).  Returns q_out."""
+    k_cache, v_cache: [S, Hk, D] (written at rows slots[t]).  sections, axis_order:
+    as in qk_norm_rope.  Returns q_out."""
     _need_contig(qkv, wq, wk, positions, cos, sin, slots, k_cache, v_cache, q_out)
     T = qkv.shape[0]
     D = qkv.shape[-1] // (q_heads + 2 * kv_heads)
@@ -220,6 +242,14 @@ def qkv_rope_cache(qkv, q_heads, kv_heads, wq, wk, positions, cos, sin, slots, k
     if q_out is None:
         q_out = torch.empty((T, q_heads, D), dtype=qkv.dtype, device=qkv.device)
     S = k_cache.shape[0] if k_cache is not None else 0
+    if sections is not None:
+        axes, counts, order = _axis_args(sections, axis_order, positions, T)
+        _check(lib().edge_qkv_rope_cache_axes(
+            _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(qkv), _ptr(wq), _ptr(wk), _dt(qkv), T,
+            q_heads, kv_heads, D, rotary_dim, layout, _ptr(positions), axes, counts, order,
+            _ptr(cos), _ptr(sin), cache_len, _ptr(slots), S, eps, weight_offset,
+            1 if normalize else 0, _stream(stream)), "edge_qkv_rope_cache_axes")
+        return q_out
     _check(lib().edge_qkv_rope_cache(_ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(qkv),
                                      _ptr(wq), _ptr(wk), _dt(qkv), T, q_heads, kv_heads, D,
                                      rotary_dim, layout, _ptr(positions), _ptr(cos), _ptr(sin),
@@ -262,12 +292,15 @@ def _qk_shapes(q, k, cos, rotary_dim, cache_len, layout, fp8, q_out, k_out):
 
 def qk_norm_rope(q, k, wq, wk, positions, cos, sin, *, rotary_dim=None, layout=ROTATE_HALF,
                  eps=1e-6, weight_offset=0, q_out=None, k_out=None, fp8=False, inv_scale=1.0,
-                 cache_len=None, unrounded=False, stream=None):
+                 cache_len=None, unrounded=False, stream=None, sections=None,
+                 axis_order="blocks"):
     """Per-head QK-RMSNorm + RoPE.  q: [T, Hq, D], k: [T, Hk, D];
     cos/sin: [P, rotary_dim/2] fp32; positions: [T] int64.  Pass q_out=q and
     k_out=k for the in-place form.  unrounded=True rotates the fp32 normalized
-    value (edge_qk_norm_rope_ex with EDGE_QK_ROTATE_UNROUNDED).  Returns
-    (q_out, k_out)."""
+    value (edge_qk_norm_rope_ex with EDGE_QK_ROTATE_UNROUNDED).  sections: the
+    pairs of each of A axes, for positions [A, T] (rotary positions with several
+    axes); axis_order "blocks" (one axis after the other) or "cycled" (dealt in
+    turn).  Returns (q_out, k_out)."""
     _need_contig(q, k, wq, wk, positions, cos, sin, q_out, k_out)
     T, Hq, Hk, D, rotary_dim, cache_len, layout, q_out, k_out = _qk_shapes(
         q, k, cos, rotary_dim, cache_len, layout, fp8, q_out, k_out)
@@ -275,7 +308,12 @@ def qk_norm_rope(q, k, wq, wk, positions, cos, sin, *, rotary_dim=None, layout=R
     args = (_ptr(q_out), _ptr(k_out), _out_dt(fp8, dt), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), dt,
             T, Hq, Hk, D, rotary_dim, layout, _ptr(positions), _ptr(cos), _ptr(sin), cache_len,
             eps, weight_offset, inv_scale)
-    if unrounded:
+    if sections is not None:
+        axes, counts, order = _axis_args(sections, axis_order, positions, T)
+        _check(lib().edge_qk_norm_rope_axes(
+            *args[:15], axes, counts, order, *args[15:], QK_ROTATE_UNROUNDED if unrounded else 0,
+            _stream(stream)), "edge_qk_norm_rope_axes")
+    elif unrounded:
         _check(lib().edge_qk_norm_rope_ex(*args, QK_ROTATE_UNROUNDED, _stream(stream)),
                "edge_qk_norm_rope_ex")
     else:
@@ -284,13 +322,22 @@ def qk_norm_rope(q, k, wq, wk, positions, cos, sin, *, rotary_dim=None, layout=R
 
 
 def rope(q, k, positions, cos, sin, *, rotary_dim=None, layout=ROTATE_HALF, q_out=None,
-         k_out=None, fp8=False, inv_scale=1.0, cache_len=None, stream=None):
+         k_out=None, fp8=False, inv_scale=1.0, cache_len=None, stream=None, sections=None,
+         axis_order="blocks"):
     """Standalone rotary embedding of q: [T, Hq, D] and k: [T, Hk, D] (k may
-    be None).  Pass q_out=q (k_out=k) for the in-place form.  Returns (q_out, k_out)."""
+    be None).  Pass q_out=q (k_out=k) for the in-place form.  sections,
+    axis_order: as in qk_norm_rope.  Returns (q_out, k_out)."""
     _need_contig(q, k, positions, cos, sin, q_out, k_out)
     T, Hq, Hk, D, rotary_dim, cache_len, layout, q_out, k_out = _qk_shapes(
         q, k, cos, rotary_dim, cache_len, layout, fp8, q_out, k_out)
     dt = _dt(q)
+    if sections is not None:
+        axes, counts, order = _axis_args(sections, axis_order, positions, T)
+        _check(lib().edge_rope_axes(
+            _ptr(q_out), _ptr(k_out), _out_dt(fp8, dt), _ptr(q), _ptr(k), dt, T, Hq, Hk, D,
+            rotary_dim, layout, _ptr(positions), axes, counts, order, _ptr(cos), _ptr(sin),
+            cache_len, inv_scale, _stream(stream)), "edge_rope_axes")
+        return q_out, k_out
     _check(lib().edge_rope(_ptr(q_out), _ptr(k_out), _out_dt(fp8, dt), _ptr(q), _ptr(k), dt, T, Hq,
                            Hk, D, rotary_dim, layout, _ptr(positions), _ptr(cos), _ptr(sin),
                            cache_len, inv_scale, _stream(stream)), "edge_rope")

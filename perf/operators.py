@@ -396,7 +396,7 @@ def _beam(s):
     if own:
         from memory_bound_decode_qk_gb300 import edge_ops
 
-        edge_ops.pages_free(table, lens, refs, s["children"], page_size=ps)
+        edge_ops.pages_free(table, lens, refs, s["children"])
         status = edge_ops.pages_fork(s["caches"], table, lens, refs, s["parents"], s["children"])
         return table, lens, refs, status, s["pool"]
     children, parents = s["children"].long(), s["parents"].long()

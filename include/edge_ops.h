@@ -384,6 +384,78 @@ int64_t edge_paged_attention_workspace(edge_dtype dt, int32_t q_heads, int32_t k
                                        int32_t head_dim);
 
 /*
+ * Pages of a KV cache.  A pool of num_pages pages is common to num_caches caches
+ * (the key and value caches of every layer); page p of a cache is its bytes
+ * [p * page_bytes, (p + 1) * page_bytes), that is slots [p * page_size, (p + 1)
+ * * page_size).  Sequence b holds the pages named in row b of block_table
+ * (entries outside [0, num_pages) name none), and refs[p] counts the entries
+ * that name page p; a page is free when refs[p] <= 0.
+ *
+ * caches:      [num_caches] device pointers in HOST memory, read during the
+ *              call, of any alignment (16-byte aligned caches and pages take the
+ *              vector path).  num_caches = 0 moves no data.
+ * block_table: [num_seqs, max_pages] int32.   lens: [num_seqs] int32.
+ * refs:        [num_pages] int32.   All index arrays are device memory.
+ * Written buffers must not overlap each other or any other buffer.  Results do
+ * not depend on timing.  EDGE_ERR_UNSUPPORTED: page_bytes of 2^31 or more, or
+ * more than 2^31 pieces of 1024 bytes in one cache's moves.
+ *
+ * edge_pages_copy copies page src[i] to page dst[i] in every cache, for i < n.
+ *   Pairs with a page outside the pool, or with src[i] == dst[i], are passed
+ *   over.  Of the other pairs with the same destination the last is carried
+ *   out, and a pair whose source is the destination of another is not.
+ */
+edge_status edge_pages_copy(void* const* caches, int32_t num_caches, int64_t page_bytes,
+                            int32_t num_pages, const int32_t* src, const int32_t* dst, int32_t n,
+                            void* stream);
+
+/*
+ * edge_pages_free gives back the pages of the sequences seqs[i], i < n: every
+ *   entry of the row is taken out (-1) and its page's count lowered, and the
+ *   length becomes 0.  Numbers outside [0, num_seqs) are passed over, and a
+ *   sequence that is named twice is freed once.
+ */
+edge_status edge_pages_free(int32_t* block_table, int32_t num_seqs, int32_t max_pages,
+                            int32_t* lens, int32_t* refs, int32_t num_pages, const int32_t* seqs,
+                            int32_t n, void* stream);
+
+/*
+ * edge_pages_fork makes sequence children[i] a copy of parents[i], for i < n:
+ *   it shares the parent's full pages (their counts are raised), and a last page
+ *   that is filled in part is copied, in every cache, into the lowest free page;
+ *   forks take pages in the order of i.
+ * status: [n]: 0 forked; 1 no free page was left (the child stays as it was);
+ *         2 refused: a number outside [0, num_seqs), a child whose row holds a
+ *         page or whose length is not 0, or a child that the call names as a
+ *         parent or earlier as a child.
+ * pairs:  [2 n]: source and destination of each page copied, -1 -1 where none.
+ * lens are read clamped to [0, max_pages * page_size].
+ * EDGE_ERR_UNSUPPORTED: n above 8192, or max_pages * page_size above 2^30.
+ */
+edge_status edge_pages_fork(void* const* caches, int32_t num_caches, int64_t page_bytes,
+                            int32_t num_pages, int32_t page_size, int32_t* block_table,
+                            int32_t num_seqs, int32_t max_pages, int32_t* lens, int32_t* refs,
+                            const int32_t* parents, const int32_t* children, int32_t n,
+                            int32_t* status, int32_t* pairs, void* stream);
+
+/*
+ * edge_pages_compact moves the L pages in use to the first L numbers: the k-th
+ *   page in use from L on moves to the k-th free page below L, in every cache.
+ *   block_table_out and refs_out (each may be its input) receive the table with
+ *   the new numbers (entries that name a free page become -1, entries outside
+ *   the pool stay) and the counts.
+ * workspace: at least edge_pages_compact_workspace(num_pages) bytes, 16-byte
+ *   aligned.  After the call its first num_pages int32 hold the new number of
+ *   each page, -1 for a page that was free.
+ */
+edge_status edge_pages_compact(void* const* caches, int32_t num_caches, int64_t page_bytes,
+                               int32_t num_pages, int32_t* block_table_out,
+                               const int32_t* block_table, int32_t num_seqs, int32_t max_pages,
+                               int32_t* refs_out, const int32_t* refs, void* workspace,
+                               int64_t workspace_bytes, void* stream);
+int64_t edge_pages_compact_workspace(int32_t num_pages);
+
+/*
  * Plain device copy of `bytes` bytes from src to dst, in the launch form of the
  * operators above (a one-shot grid of 16-byte vectors, each CTA's source span
  * prefetched into L2 before the dependent-launch wait).  It computes nothing:

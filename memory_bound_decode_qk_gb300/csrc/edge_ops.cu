@@ -373,6 +373,39 @@ static edge_status qkv_entry(void* q_out, void* k_cache, void* v_cache, const vo
     return finish(e);
 }
 
+// The caches of a page pool: none overlaps another, or one of `other`.
+edge_status check_pool(void* const* caches, int32_t num_caches, int64_t page_bytes,
+                       int32_t num_pages, int64_t pairs, const Span* other, int others) {
+    if (num_caches < 0 || page_bytes < 1 || num_pages < 0) return EDGE_ERR_SHAPE;
+    if (num_caches > 0 && caches == nullptr) return EDGE_ERR_NULL;
+    int64_t bytes = 0;
+    if (!checked_bytes(num_pages, page_bytes, 1, &bytes)) return EDGE_ERR_SHAPE;
+    if (!edge::pages_fit(page_bytes, pairs)) return EDGE_ERR_UNSUPPORTED;
+    for (int i = 0; i < num_caches; ++i) {
+        if (caches[i] == nullptr) return EDGE_ERR_NULL;
+    }
+    for (int i = 0; i < num_caches; ++i) {
+        const Span c = span(caches[i], bytes);
+        for (int j = 0; j < i; ++j) {
+            if (overlap(c, span(caches[j], bytes))) return EDGE_ERR_ALIAS;
+        }
+        for (int j = 0; j < others; ++j) {
+            if (overlap(c, other[j])) return EDGE_ERR_ALIAS;
+        }
+    }
+    return EDGE_OK;
+}
+
+// Whether two of the spans overlap.
+bool any_overlap(const Span* s, int n) {
+    for (int i = 0; i < n; ++i) {
+        for (int j = 0; j < i; ++j) {
+            if (overlap(s[i], s[j])) return true;
+        }
+    }
+    return false;
+}
+
 }  // namespace
 
 extern "C" {
@@ -672,6 +705,129 @@ edge_status edge_paged_attention(void* out, edge_dtype out_dt, float* lse, const
     a.scale = scale;
     a.inv_scale = inv_scale;
     return finish(edge::launch_attn(a, static_cast<cudaStream_t>(stream)));
+}
+
+edge_status edge_pages_copy(void* const* caches, int32_t num_caches, int64_t page_bytes,
+                            int32_t num_pages, const int32_t* src, const int32_t* dst, int32_t n,
+                            void* stream) {
+    if (n < 0) return EDGE_ERR_SHAPE;
+    if (n > 0 && (src == nullptr || dst == nullptr)) return EDGE_ERR_NULL;
+    if (!aligned(src, 4) || !aligned(dst, 4)) return EDGE_ERR_ALIGN;
+    const Span lists[] = {span(src, (int64_t)n * 4), span(dst, (int64_t)n * 4)};
+    const edge_status st = check_pool(caches, num_caches, page_bytes, num_pages, n, lists, 2);
+    if (st != EDGE_OK) return st;
+    if (n == 0 || num_caches == 0 || num_pages == 0) return EDGE_OK;
+    const edge::PagePool pool{caches, num_caches, num_pages, page_bytes};
+    return finish(edge::launch_pages_copy(pool, src, dst, n, static_cast<cudaStream_t>(stream)));
+}
+
+edge_status edge_pages_free(int32_t* block_table, int32_t num_seqs, int32_t max_pages,
+                            int32_t* lens, int32_t* refs, int32_t num_pages, const int32_t* seqs,
+                            int32_t n, void* stream) {
+    if (num_seqs < 0 || max_pages < 0 || num_pages < 0 || n < 0) return EDGE_ERR_SHAPE;
+    if (n > 0 && (seqs == nullptr || (num_seqs > 0 && lens == nullptr) ||
+                  (num_pages > 0 && refs == nullptr) ||
+                  (num_seqs > 0 && max_pages > 0 && block_table == nullptr))) {
+        return EDGE_ERR_NULL;
+    }
+    int64_t t_b = 0;
+    if (!checked_bytes(num_seqs, max_pages, 4, &t_b)) return EDGE_ERR_SHAPE;
+    if (!aligned(block_table, 4) || !aligned(lens, 4) || !aligned(refs, 4) || !aligned(seqs, 4)) {
+        return EDGE_ERR_ALIGN;
+    }
+    const Span s[] = {span(block_table, t_b), span(lens, (int64_t)num_seqs * 4),
+                      span(refs, (int64_t)num_pages * 4), span(seqs, (int64_t)n * 4)};
+    if (any_overlap(s, 4)) return EDGE_ERR_ALIAS;
+    if (n == 0 || num_seqs == 0) return EDGE_OK;
+    const edge::PageRows rows{block_table, lens, num_seqs, max_pages};
+    return finish(edge::launch_pages_free(rows, refs, num_pages, seqs, n,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+edge_status edge_pages_fork(void* const* caches, int32_t num_caches, int64_t page_bytes,
+                            int32_t num_pages, int32_t page_size, int32_t* block_table,
+                            int32_t num_seqs, int32_t max_pages, int32_t* lens, int32_t* refs,
+                            const int32_t* parents, const int32_t* children, int32_t n,
+                            int32_t* status, int32_t* pairs, void* stream) {
+    if (num_seqs < 0 || max_pages < 0 || n < 0 || page_size < 1 || num_pages < 0) {
+        return EDGE_ERR_SHAPE;
+    }
+    if (n > 0 && (parents == nullptr || children == nullptr || status == nullptr ||
+                  pairs == nullptr || (num_seqs > 0 && lens == nullptr) ||
+                  (num_pages > 0 && refs == nullptr) ||
+                  (num_seqs > 0 && max_pages > 0 && block_table == nullptr))) {
+        return EDGE_ERR_NULL;
+    }
+    int64_t t_b = 0;
+    if (!checked_bytes(num_seqs, max_pages, 4, &t_b)) return EDGE_ERR_SHAPE;
+    if (n > edge::kMaxPageForks || (int64_t)max_pages * page_size > edge::kMaxAttnRows) {
+        return EDGE_ERR_UNSUPPORTED;
+    }
+    if (!aligned(block_table, 4) || !aligned(lens, 4) || !aligned(refs, 4) ||
+        !aligned(parents, 4) || !aligned(children, 4) || !aligned(status, 4) || !aligned(pairs, 4)) {
+        return EDGE_ERR_ALIGN;
+    }
+    const int64_t n_b = (int64_t)n * 4;
+    const Span s[] = {span(block_table, t_b), span(lens, (int64_t)num_seqs * 4),
+                      span(refs, (int64_t)num_pages * 4), span(status, n_b), span(pairs, 2 * n_b),
+                      span(parents, n_b), span(children, n_b)};
+    // the two lists may be one
+    if (any_overlap(s, 6)) return EDGE_ERR_ALIAS;
+    for (int i = 0; i < 5; ++i) {
+        if (overlap(s[i], s[6])) return EDGE_ERR_ALIAS;
+    }
+    const edge_status st = check_pool(caches, num_caches, page_bytes, num_pages, n, s, 7);
+    if (st != EDGE_OK) return st;
+    if (n == 0) return EDGE_OK;
+    const edge::PagePool pool{caches, num_caches, num_pages, page_bytes};
+    const edge::PageRows rows{block_table, lens, num_seqs, max_pages};
+    return finish(edge::launch_pages_fork(pool, rows, page_size, refs, parents, children, n, status,
+                                          pairs, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t edge_pages_compact_workspace(int32_t num_pages) {
+    return num_pages < 0 ? -1 : edge::pages_compact_workspace(num_pages);
+}
+
+edge_status edge_pages_compact(void* const* caches, int32_t num_caches, int64_t page_bytes,
+                               int32_t num_pages, int32_t* block_table_out,
+                               const int32_t* block_table, int32_t num_seqs, int32_t max_pages,
+                               int32_t* refs_out, const int32_t* refs, void* workspace,
+                               int64_t workspace_bytes, void* stream) {
+    if (num_seqs < 0 || max_pages < 0 || num_pages < 0) return EDGE_ERR_SHAPE;
+    if (num_pages > 0 && (refs == nullptr || refs_out == nullptr || workspace == nullptr)) {
+        return EDGE_ERR_NULL;
+    }
+    if (num_seqs > 0 && max_pages > 0 && (block_table == nullptr || block_table_out == nullptr)) {
+        return EDGE_ERR_NULL;
+    }
+    int64_t t_b = 0;
+    if (!checked_bytes(num_seqs, max_pages, 4, &t_b)) return EDGE_ERR_SHAPE;
+    if (num_pages > 0 && workspace_bytes < edge::pages_compact_workspace(num_pages)) {
+        return EDGE_ERR_SHAPE;
+    }
+    if (!aligned(block_table, 4) || !aligned(block_table_out, 4) || !aligned(refs, 4) ||
+        !aligned(refs_out, 4) || !aligned(workspace, 16)) {
+        return EDGE_ERR_ALIGN;
+    }
+    const int64_t r_b = (int64_t)num_pages * 4;
+    const Span to = span(block_table_out, t_b), ti = span(block_table, t_b);
+    const Span ro = span(refs_out, r_b), ri = span(refs, r_b);
+    const Span ws = span(workspace, workspace_bytes < 0 ? 0 : workspace_bytes);
+    if (bad_alias(to, ti, true) || bad_alias(ro, ri, true) || overlap(to, ro) || overlap(to, ri) ||
+        overlap(ti, ro) || overlap(ws, to) || overlap(ws, ti) || overlap(ws, ro) ||
+        overlap(ws, ri)) {
+        return EDGE_ERR_ALIAS;
+    }
+    const Span s[] = {to, ti, ro, ri, ws};
+    const edge_status st =
+        check_pool(caches, num_caches, page_bytes, num_pages, num_pages / 2, s, 5);
+    if (st != EDGE_OK) return st;
+    if (num_pages == 0) return EDGE_OK;
+    const edge::PagePool pool{caches, num_caches, num_pages, page_bytes};
+    const edge::PageRows rows{const_cast<int32_t*>(block_table), nullptr, num_seqs, max_pages};
+    return finish(edge::launch_pages_compact(pool, block_table_out, rows, refs_out, refs, workspace,
+                                             static_cast<cudaStream_t>(stream)));
 }
 
 edge_status edge_copy(void* dst, const void* src, int64_t bytes, void* stream) {

@@ -121,6 +121,31 @@ constexpr int64_t kMaxAttnRows = int64_t(1) << 30;  // tokens * q_heads, max_pag
 int64_t attn_workspace(int dt, int q_heads, int kv_heads, int head_dim);
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s);
 
+// Pages of a KV cache (pages.cu).
+struct PagePool {
+    void* const* caches;     // host array of device pointers
+    int num_caches, num_pages;
+    int64_t page_bytes;
+};
+struct PageRows {
+    int32_t* table;          // [num_seqs, max_pages]
+    int32_t* lens;           // [num_seqs]
+    int num_seqs, max_pages;
+};
+constexpr int64_t kMaxPageForks = 8192;  // of one call
+bool pages_fit(int64_t page_bytes, int64_t pairs);
+int64_t pages_compact_workspace(int num_pages);
+cudaError_t launch_pages_copy(const PagePool& pool, const int32_t* src, const int32_t* dst, int n,
+                              cudaStream_t s);
+cudaError_t launch_pages_free(const PageRows& r, int32_t* refs, int num_pages,
+                              const int32_t* seqs, int n, cudaStream_t s);
+cudaError_t launch_pages_fork(const PagePool& pool, const PageRows& r, int page_size,
+                              int32_t* refs, const int32_t* parents, const int32_t* children,
+                              int n, int32_t* status, int32_t* pairs, cudaStream_t s);
+cudaError_t launch_pages_compact(const PagePool& pool, int32_t* table_out, const PageRows& r,
+                                 int32_t* refs_out, const int32_t* refs, void* workspace,
+                                 cudaStream_t s);
+
 // The yardstick copy (copy.cu): bytes from src to dst, validated.
 cudaError_t launch_copy(void* dst, const void* src, int64_t bytes, cudaStream_t s);
 

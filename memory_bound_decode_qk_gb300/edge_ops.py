@@ -30,6 +30,8 @@ EXPORTS = ("edge_rmsnorm", "edge_add_rmsnorm", "edge_glu_act", "edge_qk_norm_rop
            "edge_qkv_rope_cache", "edge_copy",
            "edge_qk_norm_rope_axes", "edge_rope_axes", "edge_qkv_rope_cache_axes",
            "edge_paged_attention", "edge_paged_attention_workspace",
+           "edge_pages_copy", "edge_pages_free", "edge_pages_fork", "edge_pages_compact",
+           "edge_pages_compact_workspace",
            "edge_status_str", "edge_last_cuda_error", "edge_version")
 QK_ROTATE_UNROUNDED = 1
 
@@ -96,6 +98,14 @@ def lib(build_if_missing: bool = False) -> ctypes.CDLL:
     L.edge_paged_attention.restype = I
     L.edge_paged_attention_workspace.argtypes = [I, I32, I32, I32]
     L.edge_paged_attention_workspace.restype = I64
+    L.edge_pages_copy.argtypes = [P, I32, I64, I32, P, P, I32, P]
+    L.edge_pages_free.argtypes = [P, I32, I32, P, P, I32, P, I32, P]
+    L.edge_pages_fork.argtypes = [P, I32, I64, I32, I32, P, I32, I32, P, P, P, P, I32, P, P, P]
+    L.edge_pages_compact.argtypes = [P, I32, I64, I32, P, P, I32, I32, P, P, P, I64, P]
+    for name in ("edge_pages_copy", "edge_pages_free", "edge_pages_fork", "edge_pages_compact"):
+        getattr(L, name).restype = I
+    L.edge_pages_compact_workspace.argtypes = [I32]
+    L.edge_pages_compact_workspace.restype = I64
     L.edge_status_str.argtypes = [I]
     L.edge_status_str.restype = ctypes.c_char_p
     L.edge_last_cuda_error.restype = I
@@ -434,3 +444,135 @@ def paged_attention(q, k_cache, v_cache, block_table, lens, *, page_size, q_star
         lens.data_ptr(), _ptr(q_starts), scale, 1 if causal else 0, window, inv_scale,
         workspace.data_ptr(), workspace.numel(), _stream(None)), "edge_paged_attention")
     return out
+
+
+class PageCaches:
+    """The caches of one page pool: tensors of one dtype and shape [S, ...] (S =
+    pages * page_size slots, as qkv_rope_cache and paged_attention take them) on
+    one device.  Holds the tensors and their addresses for the page calls."""
+
+    def __init__(self, caches, page_size):
+        caches = list(caches)
+        if not caches:
+            raise ValueError("PageCaches needs at least one cache")
+        first = caches[0]
+        if page_size < 1 or first.shape[0] % page_size:
+            raise ValueError(f"{first.shape[0]} slots are not whole pages of {page_size}")
+        if first.device.type != "cuda":
+            raise ValueError(f"caches must be CUDA tensors, not on {first.device}")
+        for t in caches:
+            _want(t, "cache", first.dtype, first.shape, first.device)
+        self.tensors = caches
+        self.device = first.device
+        self.page_size = page_size
+        self.num_pages = first.shape[0] // page_size
+        slot = first.numel() // first.shape[0] if first.shape[0] else 1
+        self.page_bytes = max(1, slot * first.element_size()) * page_size
+        self.pointers = (ctypes.c_void_p * len(caches))(*[t.data_ptr() for t in caches])
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def pages_copy(caches, src, dst, *, stream=None):
+    """Copies page src[i] to page dst[i] in every cache of `caches` (PageCaches).
+    src, dst: [n] int32.  See edge_pages_copy for pairs that meet."""
+    dev = caches.device
+    _want(src, "src", torch.int32, (None,), dev)
+    _want(dst, "dst", torch.int32, tuple(src.shape), dev)
+    if not _plain(dev, stream):
+        with _on(dev, stream):
+            return pages_copy(caches, src, dst)
+    _check(lib().edge_pages_copy(caches.pointers, len(caches), caches.page_bytes, caches.num_pages,
+                                 src.data_ptr(), dst.data_ptr(), src.shape[0], _stream(None)),
+           "edge_pages_copy")
+
+
+def _want_rows(block_table, lens, refs, pages, dev):
+    _want(block_table, "block_table", torch.int32, (None, None), dev)
+    if lens is not None:
+        _want(lens, "lens", torch.int32, (block_table.shape[0],), dev)
+    _want(refs, "refs", torch.int32, (pages,), dev)
+
+
+def pages_free(block_table, lens, refs, seqs, *, stream=None):
+    """Gives back the pages of sequences `seqs` ([n] int32): their entries of
+    block_table ([B, P] int32) become -1, their lens ([B] int32) 0, and the
+    counts refs ([pages] int32) of their pages go down."""
+    dev = refs.device
+    _want_rows(block_table, lens, refs, None, dev)
+    _want(seqs, "seqs", torch.int32, (None,), dev)
+    if dev.type != "cuda":
+        raise ValueError(f"refs must be a CUDA tensor, not on {dev}")
+    if not _plain(dev, stream):
+        with _on(dev, stream):
+            return pages_free(block_table, lens, refs, seqs)
+    _check(lib().edge_pages_free(block_table.data_ptr(), *block_table.shape, lens.data_ptr(),
+                                 refs.data_ptr(), refs.shape[0], seqs.data_ptr(), seqs.shape[0],
+                                 _stream(None)), "edge_pages_free")
+
+
+def pages_fork(caches, block_table, lens, refs, parents, children, *, status=None, pairs=None,
+               stream=None):
+    """Makes sequence children[i] a copy of parents[i] ([n] int32 each): full
+    pages are shared, a partly filled last page is copied into the lowest free
+    page of `caches` (PageCaches).  Returns status ([n] int32: 0 forked, 1 no
+    free page, 2 refused); pairs ([n, 2] int32), where given, receives the pages
+    copied."""
+    dev = caches.device
+    _want_rows(block_table, lens, refs, caches.num_pages, dev)
+    _want(parents, "parents", torch.int32, (None,), dev)
+    n = parents.shape[0]
+    _want(children, "children", torch.int32, (n,), dev)
+    if status is not None:
+        _want(status, "status", torch.int32, (n,), dev)
+    if pairs is not None:
+        _want(pairs, "pairs", torch.int32, (n, 2), dev)
+    if not _plain(dev, stream):
+        with _on(dev, stream):
+            return pages_fork(caches, block_table, lens, refs, parents, children, status=status,
+                              pairs=pairs)
+    if status is None:
+        status = torch.empty(n, dtype=torch.int32, device=dev)
+    if pairs is None:
+        pairs = torch.empty((n, 2), dtype=torch.int32, device=dev)
+    _check(lib().edge_pages_fork(caches.pointers, len(caches), caches.page_bytes, caches.num_pages,
+                                 caches.page_size, block_table.data_ptr(), *block_table.shape,
+                                 lens.data_ptr(), refs.data_ptr(), parents.data_ptr(),
+                                 children.data_ptr(), n, status.data_ptr(), pairs.data_ptr(),
+                                 _stream(None)), "edge_pages_fork")
+    return status
+
+
+def pages_compact_workspace(refs):
+    """A workspace for pages_compact of a pool with counts refs ([pages] int32)."""
+    n = lib().edge_pages_compact_workspace(refs.shape[0])
+    return torch.empty(n, dtype=torch.uint8, device=refs.device)
+
+
+def pages_compact(caches, block_table, refs, *, table_out=None, refs_out=None, workspace=None,
+                  stream=None):
+    """Moves the pages in use to the lowest numbers in every cache of `caches`
+    (PageCaches), and renumbers block_table ([B, P] int32) and refs ([pages]
+    int32), in place or into table_out and refs_out.  Returns the new number of
+    each page ([pages] int32, -1 for free pages), a view of the workspace."""
+    dev = caches.device
+    table_out = block_table if table_out is None else table_out
+    refs_out = refs if refs_out is None else refs_out
+    _want_rows(block_table, None, refs, caches.num_pages, dev)
+    _want(table_out, "table_out", torch.int32, tuple(block_table.shape), dev)
+    _want(refs_out, "refs_out", torch.int32, tuple(refs.shape), dev)
+    if workspace is not None:
+        _want(workspace, "workspace", torch.uint8, (None,), dev)
+    if not _plain(dev, stream):
+        with _on(dev, stream):
+            return pages_compact(caches, block_table, refs, table_out=table_out, refs_out=refs_out,
+                                 workspace=workspace)
+    if workspace is None:
+        workspace = pages_compact_workspace(refs)
+    _check(lib().edge_pages_compact(caches.pointers, len(caches), caches.page_bytes,
+                                    caches.num_pages, table_out.data_ptr(), block_table.data_ptr(),
+                                    *block_table.shape, refs_out.data_ptr(), refs.data_ptr(),
+                                    workspace.data_ptr(), workspace.numel(), _stream(None)),
+           "edge_pages_compact")
+    return workspace[:4 * caches.num_pages].view(torch.int32)

@@ -98,6 +98,12 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
         : "memory");
 }
 
+// 16 bytes from global to shared memory, asynchronously; zeros if !ok.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // ---------------------------------------------------------------- tcgen05
 
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -306,19 +312,28 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
             const int np = KE / rows;                              // boxes per panel
             const int oob = p.num_pages * p.page_size;             // a slot behind the tensor
             uint32_t e = 0;
-            auto copy = [&](int t, bool isv) {
+            // the slot of this lane's page in each part of tile t (lane l < np:
+            // page l), looked up a tile ahead of its copies
+            struct Slots {
+                int part[C::kParts];
+            };
+            auto look = [&](int t) {
+                Slots r;
+#pragma unroll
+                for (int h = 0; h < C::kParts; ++h) {
+                    r.part[h] = oob;
+                    const int j = (w.k0 + w.off + t) * KT + h * KE + lane * rows;
+                    if (lane < np && j + rows > w.keys.lo && j < w.keys.hi) {
+                        const int64_t x = key_slot(p, w.b, j);
+                        if (x >= 0) r.part[h] = (int)x;
+                    }
+                }
+                return r;
+            };
+            auto copy = [&](int t, bool isv, const Slots& slots) {
 #pragma unroll
                 for (int h = 0; h < C::kParts; ++h, ++e) {
                     const int j0 = (w.k0 + w.off + t) * KT + h * KE;
-                    // lane l < np looks up page l
-                    int slot = oob;
-                    if (lane < np) {
-                        const int j = j0 + lane * rows;
-                        if (j + rows > w.keys.lo && j < w.keys.hi) {
-                            const int64_t x = key_slot(p, w.b, j);
-                            if (x >= 0) slot = (int)x;
-                        }
-                    }
                     const uint32_t st = e % ST;
                     const uint32_t dst = ring + st * C::kBytes;
                     bar_wait(smem_addr(&sh.empty[st]), ((e / ST) & 1) ^ 1, failed);
@@ -327,7 +342,7 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                     __syncwarp();
                     for (int i0 = 0; i0 < np * C::kPanels; i0 += 32) {
                         const int page = (i0 + lane) % np, panel = (i0 + lane) / np;
-                        const int z = __shfl_sync(0xffffffffu, slot, page);
+                        const int z = __shfl_sync(0xffffffffu, slots.part[h], page);
                         if (panel < C::kPanels) {
                             tma_load(dst + panel * (KE * 128) + page * rows * 128, isv ? &vmap : &kmap, panel * 64, w.h, z, bar);
                         }
@@ -336,14 +351,19 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                 }
             };
             do {
-                if constexpr (NQ == 1) copy(0, false);
+                Slots now = look(0);
+                if constexpr (NQ == 1) copy(0, false, now);
                 for (int t = 0; t < w.cnt; ++t) {
+                    const bool more = t + 1 < w.cnt;
+                    Slots next = now;
+                    if (more) next = look(t + 1);
                     if constexpr (NQ == 2) {
-                        copy(t, false);
-                    } else if (t + 1 < w.cnt) {
-                        copy(t + 1, false);
+                        copy(t, false, now);
+                    } else if (more) {
+                        copy(t + 1, false, next);
                     }
-                    copy(t, true);
+                    copy(t, true, now);
+                    now = next;
                 }
             } while (walk_next<M, KT, kTcUC>(p, w));
         } else if (wid == 1) {
@@ -462,18 +482,27 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                         bar_wait(smem_addr(&sh.edge[st]), (phase >> st) & 1, failed);
                         phase ^= 1u << st;
                         char* v = tiles + NQ * C::kQ + st * C::kBytes;
-                        bool odd = false;
-                        for (int i = lane; i < KE * (DP / 8); i += 32) {
-                            const int r = i / (DP / 8), c = i % (DP / 8);
-                            const int j = j0 + r;
-                            uint4* x = reinterpret_cast<uint4*>(v + panel_at<KE>(r, c));
-                            if (j < w.keys.lo || j >= w.keys.hi) {
-                                *x = make_uint4(0u, 0u, 0u, 0u);
-                            } else if (j < w.keys.flo || j >= w.keys.fhi) {
-                                const uint4 y = *x;
-                                odd |= unbounded<T>(y.x) || unbounded<T>(y.y) || unbounded<T>(y.z) || unbounded<T>(y.w);
+                        // rows [0, a) and [d, KE) are nobody's, [a, b) and [c, d) some rows'
+                        const int a = min(max(w.keys.lo - j0, 0), KE), d = min(max(w.keys.hi - j0, a), KE);
+                        const int b = min(max(w.keys.flo - j0, a), d), c = min(max(w.keys.fhi - j0, b), d);
+                        constexpr int kRow = DP / 8;  // chunks of a row
+                        auto wipe = [&](int from, int to) {
+                            for (int i = from * kRow + lane; i < to * kRow; i += 32) {
+                                *reinterpret_cast<uint4*>(v + panel_at<KE>(i / kRow, i % kRow)) = make_uint4(0u, 0u, 0u, 0u);
                             }
-                        }
+                        };
+                        bool odd = false;
+                        auto scan = [&](int from, int to) {
+#pragma unroll 8
+                            for (int i = from * kRow + lane; i < to * kRow; i += 32) {
+                                const uint4 y = *reinterpret_cast<const uint4*>(v + panel_at<KE>(i / kRow, i % kRow));
+                                odd |= unbounded<T>(y.x) | unbounded<T>(y.y) | unbounded<T>(y.z) | unbounded<T>(y.w);
+                            }
+                        };
+                        wipe(0, a);
+                        wipe(d, KE);
+                        scan(a, b);
+                        scan(c, d);
                         if (__any_sync(0xffffffffu, odd) && lane == 0) atomicOr(&sh.careful, 1u << (unit & 31));
                         fence_async_smem();
                         __syncwarp();
@@ -493,9 +522,36 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
         const uint32_t to = tmem + 256 + i * 128 + lanes;
         char* qt = tiles + i * C::kQ;
         uint32_t step = 0, done = 0, unit = 0;
-        do {
-            int a, b;
-            tile_span<NQ>(p, w, i, a, b);
+        // this group's queries of a unit into shared memory, asynchronously
+        auto fetch = [&](const Walk& u) {
+            const int r0 = u.rt * M + i * kTile;
+            const int rows = u.s.n * p.G - r0;
+#pragma unroll 4
+            for (int x = row; x < kTile * (DP / 8); x += kTile) {
+                const int r = x / (DP / 8), c = x % (DP / 8);
+                const bool ok = r < rows && c * 8 < p.D;
+                const int64_t e = ok ? out_row(p, u.s, u.h, r0 + r) * p.D + c * 8 : 0;
+                cp_async16(smem_addr(qt) + panel_at<kTile>(r, c), p.q + e * 2, ok);
+            }
+        };
+        // the queries are in place and S may be overwritten
+        auto give_queries = [&] {
+            cp_async_wait_all();
+            fence_async_smem();
+            tc_before();
+            bar_arrive(smem_addr(&sh.q_full[i]));
+        };
+        int a, b;
+        tile_span<NQ>(p, w, i, a, b);
+        if (a < b) {
+            fetch(w);
+            give_queries();
+        }
+        for (bool go = true; go;) {
+            Walk nw = w;
+            go = walk_next<M, KT, kTcUC>(p, nw);
+            int na = 0, nb = 0;
+            if (go) tile_span<NQ>(p, nw, i, na, nb);
             const int r0 = w.rt * M + i * kTile;
             const int rows = min(w.s.n * p.G - r0, kTile);  // may be <= 0
             float ref = -INFINITY, sum = 0.0f;
@@ -503,31 +559,20 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
             // keys [from, upto) are this row's
             const int upto = p.causal ? min(at + 1, w.s.L) : w.s.L;
             const int from = p.causal && p.window > 0 ? at - p.window + 1 : 0;
-            if (a < b) {
-                for (int x = row; x < kTile * (DP / 8); x += kTile) {
-                    const int r = x / (DP / 8), c = x % (DP / 8);
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (r < rows && c * 8 < p.D) {
-                        v = __ldg(reinterpret_cast<const uint4*>(p.q + (out_row(p, w.s, w.h, r0 + r) * p.D + c * 8) * 2));
-                    }
-                    *reinterpret_cast<uint4*>(qt + panel_at<kTile>(r, c)) = v;
-                }
-                fence_async_smem();
-                tc_before();
-                bar_arrive(smem_addr(&sh.q_full[i]));
-            }
             const Keys keys = tile_keys<kTile>(p, w.s, w.rt * NQ + i);
             const int box = p.page_size < kTile ? p.page_size : kTile;
             const int box_shift = 31 - __clz(box);
+            // whether this lane's page of tile t is outside the pool, looked up a
+            // tile ahead
+            auto missing = [&](int t) {
+                const int j = (w.k0 + w.off + t) * KT + lane * box;
+                return t < b && lane * box < kTile && j < w.s.L && key_slot(p, w.b, j) < 0;
+            };
+            bool gone = missing(a);
             for (int t = a; t < b; ++t) {
                 const int j0 = (w.k0 + w.off + t) * KT;
-                // pages outside the pool, one lane each
-                bool gone = false;
-                if (lane * box < kTile) {
-                    const int j = j0 + lane * box;
-                    gone = j < w.s.L && key_slot(p, w.b, j) < 0;
-                }
                 const uint32_t lost = __ballot_sync(0xffffffffu, gone);
+                gone = missing(t + 1);
                 // two query tiles: each its own S; one: the two S in turn
                 const uint32_t buf = NQ == 2 ? i : step & 1;
                 const uint32_t ts = tmem + buf * 128 + lanes;
@@ -537,6 +582,8 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
 #pragma unroll
                 for (int c = 0; c < KT / 32; ++c) tc_ld32(ts + c * 32, reinterpret_cast<uint32_t*>(s) + c * 32);
                 tc_wait_ld();
+                // the last scores of the unit are read: its queries are done with
+                if (t == b - 1 && na < nb) fetch(nw);
                 if (lost || j0 < keys.flo || j0 + KT > keys.fhi) {
                     const int lo = from - j0, hi = upto - j0;
 #pragma unroll
@@ -615,7 +662,11 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                 bar_wait(smem_addr(&sh.o_full[i]), (NQ == 2 ? done : step - 1) & 1, failed);
                 ++done;
                 tc_after();
+            } else if (na < nb) {
+                fetch(nw);
             }
+            // the next unit's scores may start; its values wait for its weights
+            if (na < nb) give_queries();
             if (rows > 0) {
                 const bool mine = row < rows;
                 const bool again = a < b && ((*(volatile uint32_t*)&sh.careful >> (unit & 31)) & 1u) != 0;
@@ -645,10 +696,9 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                             if (ks < 0) continue;
                             const T* kr = reinterpret_cast<const T*>(p.k) + (ks * p.hk + w.h) * p.D;
                             const T* vr = reinterpret_cast<const T*>(p.v) + (ks * p.hk + w.h) * p.D;
+                            const T* qr = reinterpret_cast<const T*>(p.q) + orow * p.D;
                             float x = 0.0f;
-                            for (int d = 0; d < p.D; ++d) {
-                                x = fmaf(to_f(*reinterpret_cast<const T*>(qt + panel_at<kTile>(row, d >> 3) + (d & 7) * 2)), to_f(kr[d]), x);
-                            }
+                            for (int d = 0; d < p.D; ++d) x = fmaf(to_f(qr[d]), to_f(kr[d]), x);
                             x = ex2(fmaf(x, p.scale_log2, ref == -INFINITY ? 0.0f : -ref));
                             x = round_to<T>(x);
                             if (x == 0.0f) continue;
@@ -693,7 +743,10 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
             asm volatile("bar.sync 1, %0;" ::"n"(C::kThreads - 128) : "memory");
             if (tid == 128) atomicAnd(&sh.careful, ~(1u << (unit & 31)));
             ++unit;
-        } while (walk_next<M, KT, kTcUC>(p, w));
+            w = nw;
+            a = na;
+            b = nb;
+        }
     }
     tc_before();
     __syncthreads();

@@ -55,8 +55,11 @@ __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
+        "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes), "r"(lead)
+        : "memory");
 }
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
@@ -91,10 +94,29 @@ __device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, volatile
 
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+// The copies and products are issued by one lane of a warp whose lanes all run
+// the same code: the instruction alone is predicated (`lead`), so that its
+// operands stay in uniform registers.  (Measured: with the whole loop under "if
+// lane 0" a product cost its thread about 105 cycles to issue, against 64 that
+// the pipe needs for it, and a copy 120.)
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t p;
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p;
+}
+// A value that is the same in all lanes, marked as such for the compiler.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar,
+                                         uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %6, 0;\n\t"
+        "@q cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(lead)
         : "memory");
 }
 
@@ -111,24 +133,27 @@ __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // Arrives on the barrier once every tcgen05 operation issued before is complete.
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void tc_commit(uint32_t bar, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(lead)
+        : "memory");
 }
 
 // d[128, N] (+)= A B, both operands in shared memory.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t lead) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
         : "memory");
 }
 // The same with A in TMEM.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t lead) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
         : "memory");
 }
 
@@ -264,7 +289,7 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
     extern __shared__ char raw[];
     __shared__ WalkSmem<1> wsm;
     __shared__ TcSmem sh;
-    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, wid = uniform(tid >> 5);
     // the swizzle works on address bits: tiles start on 1024 bytes
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
     char* tiles = raw + (base - smem_addr(raw));
@@ -300,7 +325,7 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
     tc_before();
     __syncthreads();
     tc_after();
-    const uint32_t tmem = sh.tmem;
+    const uint32_t tmem = (uint32_t)uniform((int)sh.tmem);
     volatile uint32_t* failed = &sh.failed;
     // registers with two softmax groups: 128 threads at 88 and 256 at 208 are
     // the launch's 384 at 168
@@ -311,6 +336,7 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
             const int rows = p.page_size < KE ? p.page_size : KE;  // rows of a box
             const int np = KE / rows;                              // boxes per panel
             const int oob = p.num_pages * p.page_size;             // a slot behind the tensor
+            const uint32_t lead = elect_lane();
             uint32_t e = 0;
             // the slot of this lane's page in each part of tile t (lane l < np:
             // page l), looked up a tile ahead of its copies
@@ -330,6 +356,7 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                 }
                 return r;
             };
+            int head = 0;
             auto copy = [&](int t, bool isv, const Slots& slots) {
 #pragma unroll
                 for (int h = 0; h < C::kParts; ++h, ++e) {
@@ -337,24 +364,25 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                     const uint32_t st = e % ST;
                     const uint32_t dst = ring + st * C::kBytes;
                     bar_wait(smem_addr(&sh.empty[st]), ((e / ST) & 1) ^ 1, failed);
-                    const uint32_t bar = smem_addr(isv && is_edge(w, j0, KE) ? &sh.edge[st] : &sh.full[st]);
-                    if (lane == 0) bar_expect(bar, C::kBytes);
-                    __syncwarp();
-                    for (int i0 = 0; i0 < np * C::kPanels; i0 += 32) {
-                        const int page = (i0 + lane) % np, panel = (i0 + lane) / np;
+                    const uint32_t bar = smem_addr(isv && uniform(is_edge(w, j0, KE)) ? &sh.edge[st] : &sh.full[st]);
+                    bar_expect(bar, C::kBytes, lead);
+                    for (int page = 0; page < np; ++page) {
                         const int z = __shfl_sync(0xffffffffu, slots.part[h], page);
-                        if (panel < C::kPanels) {
-                            tma_load(dst + panel * (KE * 128) + page * rows * 128, isv ? &vmap : &kmap, panel * 64, w.h, z, bar);
+#pragma unroll
+                        for (int panel = 0; panel < C::kPanels; ++panel) {
+                            tma_load(dst + panel * (KE * 128) + page * rows * 128, isv ? &vmap : &kmap, panel * 64, head, z, bar, lead);
                         }
                     }
-                    __syncwarp();
                 }
             };
+            bool go = true;
             do {
+                head = uniform(w.h);
+                const int cnt = uniform(w.cnt);
                 Slots now = look(0);
                 if constexpr (NQ == 1) copy(0, false, now);
-                for (int t = 0; t < w.cnt; ++t) {
-                    const bool more = t + 1 < w.cnt;
+                for (int t = 0; t < cnt; ++t) {
+                    const bool more = t + 1 < cnt;
                     Slots next = now;
                     if (more) next = look(t + 1);
                     if constexpr (NQ == 2) {
@@ -365,20 +393,26 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                     copy(t, true, now);
                     now = next;
                 }
-            } while (walk_next<M, KT, kTcUC>(p, w));
+                go = uniform(walk_next<M, KT, kTcUC>(p, w));
+            } while (go);
         } else if (wid == 1) {
             // ---- products
-            if (lane == 0) {
+            {
+                const uint32_t lead = elect_lane();
                 constexpr uint32_t is = instr_desc<T>(KE, 0), io = instr_desc<T>(DP, 1);
+                // descriptors of the first query tile and the first ring entry, as keys
+                // and as values; an offset in the tile is added in 16-byte units
+                const uint64_t dq = smem_desc(base, 16), dk = smem_desc(ring, 16), dv = smem_desc(ring, KE * 128);
+                auto entry = [&](uint32_t e) { return (uint64_t)((e % ST) * (uint32_t)(C::kBytes >> 4)); };
                 // S (at column ts of TMEM) of query tile i and the keys of entries e ..
                 auto scores = [&](uint32_t ts, int i, uint32_t e) {
 #pragma unroll
                     for (int h = 0; h < C::kParts; ++h) {
-                        const uint32_t a = base + i * C::kQ, b = ring + ((e + h) % ST) * C::kBytes;
+                        const uint64_t b = dk + entry(e + h);
 #pragma unroll
                         for (int k = 0; k < DP / 16; ++k) {
-                            mma_ss(tmem + ts + h * KE, smem_desc(a + (k >> 2) * (kTile * 128) + (k & 3) * 32, 16),
-                                   smem_desc(b + (k >> 2) * (KE * 128) + (k & 3) * 32, 16), is, k > 0);
+                            mma_ss(tmem + ts + h * KE, dq + (uint32_t)((i * C::kQ + (k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4),
+                                   b + (uint32_t)(((k >> 2) * (KE * 128) + (k & 3) * 32) >> 4), is, k > 0, lead);
                         }
                     }
                 };
@@ -386,11 +420,11 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                 auto values = [&](uint32_t to, uint32_t ts, uint32_t e, bool add) {
 #pragma unroll
                     for (int h = 0; h < C::kParts; ++h) {
-                        const uint32_t b = ring + ((e + h) % ST) * C::kBytes;
+                        const uint64_t b = dv + entry(e + h);
 #pragma unroll
                         for (int k = 0; k < KE / 16; ++k) {
-                            mma_ts(tmem + to, tmem + ts + h * (KE / 2) + k * 8, smem_desc(b + k * 16 * 128, KE * 128), io,
-                                   add || h > 0 || k > 0);
+                            mma_ts(tmem + to, tmem + ts + h * (KE / 2) + k * 8, b + (uint32_t)((k * 16 * 128) >> 4), io,
+                                   h > 0 || k > 0 ? 1u : (uint32_t)add, lead);
                         }
                     }
                 };
@@ -400,17 +434,23 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                 };
                 auto give_back = [&](uint32_t e) {
 #pragma unroll
-                    for (int h = 0; h < C::kParts; ++h) tc_commit(smem_addr(&sh.empty[(e + h) % ST]));
+                    for (int h = 0; h < C::kParts; ++h) tc_commit(smem_addr(&sh.empty[(e + h) % ST]), lead);
                 };
                 uint32_t e = 0, unit[2] = {0, 0}, step[2] = {0, 0};
+                bool go = true;
                 do {
                     int a[NQ], b[NQ];
 #pragma unroll
-                    for (int i = 0; i < NQ; ++i) tile_span<NQ>(p, w, i, a[i], b[i]);
-                    for (int t = -1; t < w.cnt; ++t) {
-                        const bool next = t + 1 < w.cnt;
+                    for (int i = 0; i < NQ; ++i) {
+                        tile_span<NQ>(p, w, i, a[i], b[i]);
+                        a[i] = uniform(a[i]);
+                        b[i] = uniform(b[i]);
+                    }
+                    const int cnt = uniform(w.cnt);
+                    for (int t = -1; t < cnt; ++t) {
+                        const bool next = t + 1 < cnt;
                         const uint32_t ek = e + C::kParts * (NQ == 2 || t < 0 ? 2 * (t + 1) : 2 * t + 1);
-                        const uint32_t ev = e + C::kParts * value_place<NQ>(t, w.cnt);
+                        const uint32_t ev = e + C::kParts * value_place<NQ>(t, cnt);
                         if constexpr (NQ == 2) {
                             if (t >= 0) wait_full(ev);
                             if (next) wait_full(ek);
@@ -421,7 +461,7 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                                     ++step[i];
                                     tc_after();
                                     values(256 + i * 128, i * 128, ev, t > a[i]);
-                                    if (t == b[i] - 1) tc_commit(smem_addr(&sh.o_full[i]));
+                                    if (t == b[i] - 1) tc_commit(smem_addr(&sh.o_full[i]), lead);
                                 }
                                 if (t + 1 >= a[i] && t + 1 < b[i]) {
                                     if (t + 1 == a[i]) {
@@ -430,7 +470,7 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                                         tc_after();
                                     }
                                     scores(i * 128, i, ek);
-                                    tc_commit(smem_addr(&sh.s_full[i]));
+                                    tc_commit(smem_addr(&sh.s_full[i]), lead);
                                 }
                             }
                             if (t >= 0) give_back(ev);
@@ -446,7 +486,7 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                                         tc_after();
                                     }
                                     scores((unit[1] & 1) * 128, 0, ek);
-                                    tc_commit(smem_addr(&sh.s_full[unit[1] & 1]));
+                                    tc_commit(smem_addr(&sh.s_full[unit[1] & 1]), lead);
                                     ++unit[1];
                                 }
                                 give_back(ek);
@@ -458,16 +498,16 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                                     bar_wait(smem_addr(&sh.p_full[u & 1]), (u >> 1) & 1, failed);
                                     tc_after();
                                     values(256, (u & 1) * 128, ev, t > 0);
-                                    tc_commit(smem_addr(&sh.o_full[0]));
+                                    tc_commit(smem_addr(&sh.o_full[0]), lead);
                                 }
                                 give_back(ev);
                             }
                         }
                     }
-                    e += 2 * C::kParts * w.cnt;
-                } while (walk_next<M, KT, kTcUC>(p, w));
+                    e += 2 * C::kParts * cnt;
+                    go = uniform(walk_next<M, KT, kTcUC>(p, w));
+                } while (go);
             }
-            __syncwarp();
         } else if (wid == 2) {
             // ---- values at an edge: rows that no query sees become zero;
             // infinities and NaN in rows that some see mark the unit

@@ -228,6 +228,32 @@ __device__ __forceinline__ bool unbounded(uint32_t w) {
     return __vcmpeq2(w & e, e) != 0;
 }
 
+// 4 x 4 transpose over groups of four lanes: u[k] of lane l becomes u[l & 3] of
+// lane (l & ~3) + k.  Rows that lie in lanes become pieces of one row in
+// neighbouring lanes, so that a store fills whole sectors (a lane per row
+// writes 32 lines at once: 18,000 cycles for a tile of 128 x 256 outputs).
+template <int R>
+__device__ __forceinline__ void transpose4(uint32_t (&u)[4][R], int lane) {
+#pragma unroll
+    for (int d = 1; d <= 2; d <<= 1) {
+        const bool up = (lane & d) != 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (k & d) continue;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const uint32_t give = up ? u[k][r] : u[k | d][r];
+                const uint32_t take = __shfl_xor_sync(0xffffffffu, give, d);
+                if (up) {
+                    u[k][r] = take;
+                } else {
+                    u[k | d][r] = take;
+                }
+            }
+        }
+    }
+}
+
 // The lowest n bits (n clamped to 0 .. 32).
 __device__ __forceinline__ uint32_t bits_below(int n) {
     return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
@@ -283,7 +309,8 @@ __device__ __forceinline__ uint32_t value_place(int t, int cnt) {
 
 template <typename T, int DP>
 __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
-attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+               const __grid_constant__ CUtensorMap qmap, int q_boxes) {
     using C = Tc<DP>;
     constexpr int NQ = C::kNQ, M = C::kM, KT = kTile, KE = C::kKeys, ST = C::kStages;
     extern __shared__ char raw[];
@@ -312,7 +339,7 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
             bar_init(smem_addr(&sh.edge[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
-            bar_init(smem_addr(&sh.q_full[i]), kTile);
+            bar_init(smem_addr(&sh.q_full[i]), q_boxes ? 1 : kTile);
             bar_init(smem_addr(&sh.s_full[i]), 1);
             bar_init(smem_addr(&sh.p_full[i]), kTile);
             bar_init(smem_addr(&sh.o_full[i]), 1);
@@ -562,9 +589,22 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
         const uint32_t to = tmem + 256 + i * 128 + lanes;
         char* qt = tiles + i * C::kQ;
         uint32_t step = 0, done = 0, unit = 0;
-        // this group's queries of a unit into shared memory, asynchronously
+        // this group's queries of a unit into shared memory: one box per 64
+        // channels where the heads of the group divide a tile, else row by row
         auto fetch = [&](const Walk& u) {
             const int r0 = u.rt * M + i * kTile;
+            if (q_boxes) {
+                if (row == 0) {
+                    const uint32_t bar = smem_addr(&sh.q_full[i]);
+                    const int tok = u.s.q0 + (int)fast_div((uint32_t)r0, p.gdiv);
+                    bar_expect(bar, C::kQ, 1);
+#pragma unroll
+                    for (int panel = 0; panel < C::kPanels; ++panel) {
+                        tma_load(smem_addr(qt) + panel * (kTile * 128), &qmap, panel * 64, u.h * p.G, tok, bar, 1);
+                    }
+                }
+                return;
+            }
             const int rows = u.s.n * p.G - r0;
 #pragma unroll 4
             for (int x = row; x < kTile * (DP / 8); x += kTile) {
@@ -574,11 +614,11 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                 cp_async16(smem_addr(qt) + panel_at<kTile>(r, c), p.q + e * 2, ok);
             }
         };
-        // the queries are in place and S may be overwritten
+        // queries that came row by row are in place
         auto give_queries = [&] {
+            if (q_boxes) return;
             cp_async_wait_all();
             fence_async_smem();
-            tc_before();
             bar_arrive(smem_addr(&sh.q_full[i]));
         };
         int a, b;
@@ -705,7 +745,8 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
             } else if (na < nb) {
                 fetch(nw);
             }
-            // the next unit's scores may start; its values wait for its weights
+            // the next unit's scores may start (they overwrite weights that are used
+            // up); its values wait for its weights, which come after this unit's end
             if (na < nb) give_queries();
             if (rows > 0) {
                 const bool mine = row < rows;
@@ -714,6 +755,9 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                 const float nan = *failed ? NAN : 0.0f;
                 float* part = slot < 0 ? nullptr : part_of<M>(p, w.piece, slot);
                 const int64_t orow = mine ? out_row(p, w.s, w.h, r0 + row) : 0;
+                int64_t quad_row[4];  // of the rows of this lane's group of four
+#pragma unroll
+                for (int k = 0; k < 4; ++k) quad_row[k] = __shfl_sync(0xffffffffu, orow, (lane & ~3) + k);
                 const float scale = (part != nullptr ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum) + nan;
 #pragma unroll 1
                 for (int c = 0; c < DP / 32; ++c) {
@@ -751,21 +795,56 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                         for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(y[k]);
                         __syncwarp();
                     }
-                    if (mine) {
+                    // scaled by the row's own factor, then four lanes' rows in turn
+                    const int piece = lane & 3, first = row & ~3;
+                    if (part != nullptr) {
 #pragma unroll
-                        for (int k = 0; k < 32; k += 8) {
-                            if (c * 32 + k >= p.D) continue;
+                        for (int half = 0; half < 2; ++half) {
+                            uint32_t u[4][4];
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) u[k >> 2][k & 3] = __float_as_uint(__uint_as_float(o[half * 16 + k]) * scale);
+                            transpose4<4>(u, lane);
+                            const int d = c * 32 + half * 16 + piece * 4;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                if (first + k < rows && d < p.D) {
+                                    *reinterpret_cast<uint4*>(part + (int64_t)(i * kTile + first + k) * p.D + d) =
+                                        make_uint4(u[k][0], u[k][1], u[k][2], u[k][3]);
+                                }
+                            }
+                        }
+                    } else if (p.out_fp8) {
+                        uint32_t u[4][2];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
                             float y[8];
 #pragma unroll
-                            for (int z = 0; z < 8; ++z) y[z] = __uint_as_float(o[k + z]) * scale;
-                            if (part != nullptr) {
-                                float4* dst = reinterpret_cast<float4*>(part + (int64_t)(i * kTile + row) * p.D + c * 32 + k);
-                                dst[0] = make_float4(y[0], y[1], y[2], y[3]);
-                                dst[1] = make_float4(y[4], y[5], y[6], y[7]);
-                            } else if (p.out_fp8) {
-                                *reinterpret_cast<uint2*>(p.out + orow * p.D + c * 32 + k) = quantize_vec<8>(y, p.inv);
-                            } else {
-                                *reinterpret_cast<uint4*>(p.out + (orow * p.D + c * 32 + k) * 2) = pack_vec<T, 8>(y);
+                            for (int z = 0; z < 8; ++z) y[z] = __uint_as_float(o[k * 8 + z]) * scale;
+                            const uint2 q8 = quantize_vec<8>(y, p.inv);
+                            u[k][0] = q8.x;
+                            u[k][1] = q8.y;
+                        }
+                        transpose4<2>(u, lane);
+                        const int d = c * 32 + piece * 8;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (first + k < rows && d < p.D) {
+                                *reinterpret_cast<uint2*>(p.out + quad_row[k] * p.D + d) = make_uint2(u[k][0], u[k][1]);
+                            }
+                        }
+                    } else {
+                        uint32_t u[4][4];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            u[k >> 2][k & 3] = pack2<T>(__uint_as_float(o[2 * k]) * scale, __uint_as_float(o[2 * k + 1]) * scale);
+                        }
+                        transpose4<4>(u, lane);
+                        const int d = c * 32 + piece * 8;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (first + k < rows && d < p.D) {
+                                *reinterpret_cast<uint4*>(p.out + (quad_row[k] * p.D + d) * 2) =
+                                    make_uint4(u[k][0], u[k][1], u[k][2], u[k][3]);
                             }
                         }
                     }
@@ -823,6 +902,17 @@ Encode encoder() {
     return fn;
 }
 
+bool query_map(CUtensorMap* map, const AttnP& p, int dt) {
+    const cuuint64_t dims[3] = {(cuuint64_t)p.D, (cuuint64_t)p.hq, (cuuint64_t)p.tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)p.D * 2, (cuuint64_t)p.hq * p.D * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)(kTile / p.G)};
+    const cuuint32_t ones[3] = {1, 1, 1};
+    return encoder()(map, dt == kF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                     const_cast<char*>(p.q), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool cache_map(CUtensorMap* map, const AttnP& p, const char* base, int dt) {
     const cuuint64_t dims[3] = {(cuuint64_t)p.D, (cuuint64_t)p.hk, (cuuint64_t)p.num_pages * p.page_size};
     const cuuint64_t strides[2] = {(cuuint64_t)p.D * 2, (cuuint64_t)p.hk * p.D * 2};
@@ -836,13 +926,13 @@ bool cache_map(CUtensorMap* map, const AttnP& p, const char* base, int dt) {
 }
 
 template <typename T, int DP>
-cudaError_t launch_typed(const AttnP& p, const CUtensorMap& km, const CUtensorMap& vm, cudaLaunchConfig_t cfg) {
+cudaError_t launch_typed(const AttnP& p, const CUtensorMap (&m)[3], int q_boxes, cudaLaunchConfig_t cfg) {
     cudaError_t e = cudaFuncSetAttribute((const void*)attn_tc_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          Tc<DP>::kSmem);
     if (e != cudaSuccess) return e;
     cfg.blockDim = dim3(Tc<DP>::kThreads);
     cfg.dynamicSmemBytes = Tc<DP>::kSmem;
-    return cudaLaunchKernelEx(&cfg, attn_tc_kernel<T, DP>, p, km, vm);
+    return cudaLaunchKernelEx(&cfg, attn_tc_kernel<T, DP>, p, m[0], m[1], m[2], q_boxes);
 }
 
 }  // namespace
@@ -859,17 +949,20 @@ bool tc_suits(const AttnP& p) {
 }
 
 template <typename T>
-cudaError_t launch_by_size(const AttnP& p, const CUtensorMap& km, const CUtensorMap& vm, cudaLaunchConfig_t cfg) {
-    if (p.D <= 64) return launch_typed<T, 64>(p, km, vm, cfg);
-    if (p.D <= 128) return launch_typed<T, 128>(p, km, vm, cfg);
-    if (p.D <= 192) return launch_typed<T, 192>(p, km, vm, cfg);
-    return launch_typed<T, 256>(p, km, vm, cfg);
+cudaError_t launch_by_size(const AttnP& p, const CUtensorMap (&m)[3], int q_boxes, cudaLaunchConfig_t cfg) {
+    if (p.D <= 64) return launch_typed<T, 64>(p, m, q_boxes, cfg);
+    if (p.D <= 128) return launch_typed<T, 128>(p, m, q_boxes, cfg);
+    if (p.D <= 192) return launch_typed<T, 192>(p, m, q_boxes, cfg);
+    return launch_typed<T, 256>(p, m, q_boxes, cfg);
 }
 
 cudaError_t launch_attn_tc(const AttnP& p, int dt, cudaLaunchConfig_t cfg) {
-    CUtensorMap km, vm;
-    if (!cache_map(&km, p, p.k, dt) || !cache_map(&vm, p, p.v, dt)) return cudaErrorInvalidValue;
-    return dt == kF16 ? launch_by_size<__half>(p, km, vm, cfg) : launch_by_size<__nv_bfloat16>(p, km, vm, cfg);
+    CUtensorMap m[3];
+    const int q_boxes = kTile % p.G == 0;
+    if (!cache_map(&m[0], p, p.k, dt) || !cache_map(&m[1], p, p.v, dt)) return cudaErrorInvalidValue;
+    m[2] = m[0];
+    if (q_boxes && !query_map(&m[2], p, dt)) return cudaErrorInvalidValue;
+    return dt == kF16 ? launch_by_size<__half>(p, m, q_boxes, cfg) : launch_by_size<__nv_bfloat16>(p, m, q_boxes, cfg);
 }
 
 }  // namespace edge

@@ -15,7 +15,7 @@
 // Roles of the warps:
 //   warp 0        copies keys and values by TMA into a ring in shared memory
 //   warp 1        issues tcgen05.mma (one thread)
-//   warp 2        values at the edges of what the rows see (below)
+//   warps 2, 3    values at the edges of what the rows see (below)
 //   warps 4-7     softmax, a thread per row;  warps 8-11: of the second tile
 // P goes back to TMEM over S as 16-bit values and is the A operand of the
 // second product.
@@ -24,9 +24,9 @@
 // rows of it) is one box per 64 channels, stored with the 128-byte swizzle.  A
 // page outside the pool or outside the keys that the unit sees is copied from
 // behind the tensor's end, which fills zeros.  A page that is seen in part
-// brings rows that no query may touch, and rows that only some see: warp 2
-// zeroes the first before the tile is used, and looks for infinities and NaN
-// in the second, since 0 * NaN is NaN in a matrix product.  If it finds any, the
+// brings rows that no query may touch, and rows that only some see: warps 2
+// and 3 zero the first before the tile is used, and look for infinities and NaN
+// in the second, since 0 * NaN is NaN in a matrix product.  If they find any, the
 // unit's values are summed again row by row with masked keys skipped.
 //
 // Every wait has a limit of two seconds.  A wait that runs out (which correct
@@ -177,6 +177,16 @@ __device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t* r) {
         : "r"(addr)
         : "memory");
 }
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
+        "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),
+        "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+        : "memory");
+}
 __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
@@ -222,10 +232,11 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     }
 }
 
+// Bits 15 and 31 are set where the exponent of the pair's value is all ones (an
+// infinity or NaN): the exponent field plus one at its lowest bit carries there.
 template <typename T>
-__device__ __forceinline__ bool unbounded(uint32_t w) {
-    constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7C007C00u : 0x7F807F80u;
-    return __vcmpeq2(w & e, e) != 0;
+__device__ __forceinline__ uint32_t exponent_bits(uint32_t w) {
+    return std::is_same<T, __half>::value ? (w & 0x7C007C00u) + 0x04000400u : (w & 0x7F807F80u) + 0x00800080u;
 }
 
 // 4 x 4 transpose over groups of four lanes: u[k] of lane l becomes u[l & 3] of
@@ -265,18 +276,22 @@ template <int DP>
 struct Tc {
     static constexpr int kNQ = DP <= 128 ? 2 : 1;       // query tiles of a unit
     static constexpr int kM = kNQ * kTile;
-    static constexpr int kKeys = DP <= 128 ? 128 : 64;  // keys of a ring entry
-    static constexpr int kParts = kTile / kKeys;        // entries of a key tile
-    static constexpr int kStages = DP == 64 ? 8 : DP == 192 ? 7 : 5;
-    static constexpr int kPanels = DP / 64;
+    // a ring entry: 128 keys and CW channels of them.  Wide heads are cut by
+    // channels, not by keys: 64-key operands made the pipe read Q twice as often
+    // from shared memory, whose bandwidth then bound it (3100 cycles a tile).
+    static constexpr int kCW = DP == 192 ? 64 : DP <= 128 ? DP : 128;
+    static constexpr int kParts = DP / kCW;             // entries of a key tile
+    static constexpr int kStages = DP == 64 ? 8 : DP == 192 ? 10 : 5;
+    static constexpr int kPanels = kCW / 64;            // of an entry
+    static constexpr int kQPanels = DP / 64;
     static constexpr int kQ = kTile * DP * 2;           // bytes of a query tile
-    static constexpr int kBytes = kKeys * DP * 2;       // bytes of an entry
+    static constexpr int kBytes = kTile * kCW * 2;      // bytes of an entry
     static constexpr int kSmem = kNQ * kQ + kStages * kBytes + 1024;
     static constexpr int kThreads = 128 + 128 * kNQ;
 };
 
 struct TcSmem {
-    uint64_t full[8], empty[8], edge[8];
+    uint64_t full[10], empty[10], edge[10];
     uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
     uint32_t tmem;
     uint32_t failed;
@@ -312,7 +327,7 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
 attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                const __grid_constant__ CUtensorMap qmap, int q_boxes) {
     using C = Tc<DP>;
-    constexpr int NQ = C::kNQ, M = C::kM, KT = kTile, KE = C::kKeys, ST = C::kStages;
+    constexpr int NQ = C::kNQ, M = C::kM, KT = kTile, CW = C::kCW, ST = C::kStages;
     extern __shared__ char raw[];
     __shared__ WalkSmem<1> wsm;
     __shared__ TcSmem sh;
@@ -360,44 +375,37 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
         if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (wid == 0) {
             // ---- copies
-            const int rows = p.page_size < KE ? p.page_size : KE;  // rows of a box
-            const int np = KE / rows;                              // boxes per panel
+            const int rows = p.page_size < KT ? p.page_size : KT;  // rows of a box
+            const int np = KT / rows;                              // boxes per panel
             const int oob = p.num_pages * p.page_size;             // a slot behind the tensor
             const uint32_t lead = elect_lane();
             uint32_t e = 0;
-            // the slot of this lane's page in each part of tile t (lane l < np:
-            // page l), looked up a tile ahead of its copies
-            struct Slots {
-                int part[C::kParts];
-            };
-            auto look = [&](int t) {
-                Slots r;
-#pragma unroll
-                for (int h = 0; h < C::kParts; ++h) {
-                    r.part[h] = oob;
-                    const int j = (w.k0 + w.off + t) * KT + h * KE + lane * rows;
-                    if (lane < np && j + rows > w.keys.lo && j < w.keys.hi) {
-                        const int64_t x = key_slot(p, w.b, j);
-                        if (x >= 0) r.part[h] = (int)x;
-                    }
-                }
-                return r;
-            };
             int head = 0;
-            auto copy = [&](int t, bool isv, const Slots& slots) {
+            // the slot of this lane's page of tile t (lane l < np: page l), looked
+            // up a tile ahead of its copies
+            auto look = [&](int t) {
+                const int j = (w.k0 + w.off + t) * KT + lane * rows;
+                if (lane < np && j + rows > w.keys.lo && j < w.keys.hi) {
+                    const int64_t x = key_slot(p, w.b, j);
+                    if (x >= 0) return (int)x;
+                }
+                return oob;
+            };
+            auto copy = [&](int t, bool isv, int slot) {
+                const bool at_edge = isv && uniform(is_edge(w, (w.k0 + w.off + t) * KT, KT));
 #pragma unroll
                 for (int h = 0; h < C::kParts; ++h, ++e) {
-                    const int j0 = (w.k0 + w.off + t) * KT + h * KE;
                     const uint32_t st = e % ST;
                     const uint32_t dst = ring + st * C::kBytes;
                     bar_wait(smem_addr(&sh.empty[st]), ((e / ST) & 1) ^ 1, failed);
-                    const uint32_t bar = smem_addr(isv && uniform(is_edge(w, j0, KE)) ? &sh.edge[st] : &sh.full[st]);
+                    const uint32_t bar = smem_addr(at_edge ? &sh.edge[st] : &sh.full[st]);
                     bar_expect(bar, C::kBytes, lead);
                     for (int page = 0; page < np; ++page) {
-                        const int z = __shfl_sync(0xffffffffu, slots.part[h], page);
+                        const int z = __shfl_sync(0xffffffffu, slot, page);
 #pragma unroll
                         for (int panel = 0; panel < C::kPanels; ++panel) {
-                            tma_load(dst + panel * (KE * 128) + page * rows * 128, isv ? &vmap : &kmap, panel * 64, head, z, bar, lead);
+                            tma_load(dst + panel * (KT * 128) + page * rows * 128, isv ? &vmap : &kmap, h * CW + panel * 64, head,
+                                     z, bar, lead);
                         }
                     }
                 }
@@ -406,11 +414,11 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
             do {
                 head = uniform(w.h);
                 const int cnt = uniform(w.cnt);
-                Slots now = look(0);
+                int now = look(0);
                 if constexpr (NQ == 1) copy(0, false, now);
                 for (int t = 0; t < cnt; ++t) {
                     const bool more = t + 1 < cnt;
-                    Slots next = now;
+                    int next = now;
                     if (more) next = look(t + 1);
                     if constexpr (NQ == 2) {
                         copy(t, false, now);
@@ -426,32 +434,37 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
             // ---- products
             {
                 const uint32_t lead = elect_lane();
-                constexpr uint32_t is = instr_desc<T>(KE, 0), io = instr_desc<T>(DP, 1);
+                constexpr uint32_t is = instr_desc<T>(KT, 0), io = instr_desc<T>(CW, 1);
                 // descriptors of the first query tile and the first ring entry, as keys
                 // and as values; an offset in the tile is added in 16-byte units
-                const uint64_t dq = smem_desc(base, 16), dk = smem_desc(ring, 16), dv = smem_desc(ring, KE * 128);
+                const uint64_t dq = smem_desc(base, 16), dk = smem_desc(ring, 16), dv = smem_desc(ring, KT * 128);
                 auto entry = [&](uint32_t e) { return (uint64_t)((e % ST) * (uint32_t)(C::kBytes >> 4)); };
                 // S (at column ts of TMEM) of query tile i and the keys of entries e ..
                 auto scores = [&](uint32_t ts, int i, uint32_t e) {
 #pragma unroll
                     for (int h = 0; h < C::kParts; ++h) {
                         const uint64_t b = dk + entry(e + h);
+#pragma unroll 1
+                        for (int panel = 0; panel < C::kPanels; ++panel) {
+                            const uint32_t qo = (uint32_t)(i * C::kQ + (h * C::kPanels + panel) * (kTile * 128)) >> 4;
+                            const uint32_t ko = (uint32_t)(panel * (KT * 128)) >> 4;
 #pragma unroll
-                        for (int k = 0; k < DP / 16; ++k) {
-                            mma_ss(tmem + ts + h * KE, dq + (uint32_t)((i * C::kQ + (k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4),
-                                   b + (uint32_t)(((k >> 2) * (KE * 128) + (k & 3) * 32) >> 4), is, k > 0, lead);
+                            for (int k = 0; k < 4; ++k) {
+                                mma_ss(tmem + ts, dq + (qo + k * 2), b + (ko + k * 2), is, h > 0 || k > 0 ? 1u : (uint32_t)(panel > 0), lead);
+                            }
                         }
                     }
                 };
-                // O (at column to) += P (over S) times the values of entries e ..
-                auto values = [&](uint32_t to, uint32_t ts, uint32_t e, bool add) {
+                // O (at column to) += P (over S) times the values of entries e ..,
+                // half of the keys
+                auto values = [&](uint32_t to, uint32_t ts, uint32_t e, int half, bool add) {
 #pragma unroll
                     for (int h = 0; h < C::kParts; ++h) {
-                        const uint64_t b = dv + entry(e + h);
+                        const uint64_t b = dv + entry(e + h) + (uint32_t)(half * ((64 * 128) >> 4));
 #pragma unroll
-                        for (int k = 0; k < KE / 16; ++k) {
-                            mma_ts(tmem + to, tmem + ts + h * (KE / 2) + k * 8, b + (uint32_t)((k * 16 * 128) >> 4), io,
-                                   h > 0 || k > 0 ? 1u : (uint32_t)add, lead);
+                        for (int k = 0; k < 4; ++k) {
+                            mma_ts(tmem + to + h * CW, tmem + ts + half * 32 + k * 8, b + (uint32_t)((k * 16 * 128) >> 4), io,
+                                   k > 0 ? 1u : (uint32_t)(add || half > 0), lead);
                         }
                     }
                 };
@@ -487,7 +500,8 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                                     bar_wait(smem_addr(&sh.p_full[i]), step[i] & 1, failed);
                                     ++step[i];
                                     tc_after();
-                                    values(256 + i * 128, i * 128, ev, t > a[i]);
+#pragma unroll 1
+                                    for (int half = 0; half < 2; ++half) values(256 + i * 128, i * 128, ev, half, t > a[i]);
                                     if (t == b[i] - 1) tc_commit(smem_addr(&sh.o_full[i]), lead);
                                 }
                                 if (t + 1 >= a[i] && t + 1 < b[i]) {
@@ -522,10 +536,13 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                                 wait_full(ev);
                                 if (t < b[0]) {
                                     const uint32_t u = step[0]++;
-                                    bar_wait(smem_addr(&sh.p_full[u & 1]), (u >> 1) & 1, failed);
-                                    tc_after();
-                                    values(256, (u & 1) * 128, ev, t > 0);
-                                    tc_commit(smem_addr(&sh.o_full[0]), lead);
+#pragma unroll 1
+                                    for (int half = 0; half < 2; ++half) {
+                                        bar_wait(smem_addr(&sh.p_full[0]), half, failed);
+                                        tc_after();
+                                        values(256, (u & 1) * 128, ev, half, t > 0);
+                                        tc_commit(smem_addr(&sh.o_full[0]), lead);
+                                    }
                                 }
                                 give_back(ev);
                             }
@@ -535,45 +552,50 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                     go = uniform(walk_next<M, KT, kTcUC>(p, w));
                 } while (go);
             }
-        } else if (wid == 2) {
-            // ---- values at an edge: rows that no query sees become zero;
-            // infinities and NaN in rows that some see mark the unit
+        } else {
+            // ---- values at an edge (warps 2 and 3, half of the rows each): rows
+            // that no query sees become zero; infinities and NaN in rows that some
+            // see mark the unit
             uint32_t e = 0, phase = 0, unit = 0;
             do {
+                // the mark of a unit long past is cleared for a later one (the
+                // ring holds fewer than 16 units)
+                if (tid == 64) atomicAnd(&sh.careful, ~(1u << ((unit + 16) & 31)));
                 for (int t = 0; t < w.cnt; ++t) {
+                    const int j0 = (w.k0 + w.off + t) * KT;
+                    if (!is_edge(w, j0, KT)) continue;
+                    // rows [0, a) and [d, KT) are nobody's, [a, b) and [c, d) some rows'
+                    const int a = min(max(w.keys.lo - j0, 0), KT), d = min(max(w.keys.hi - j0, a), KT);
+                    const int b = min(max(w.keys.flo - j0, a), d), c = min(max(w.keys.fhi - j0, b), d);
 #pragma unroll 1
                     for (int h = 0; h < C::kParts; ++h) {
-                        const int j0 = (w.k0 + w.off + t) * KT + h * KE;
-                        if (!is_edge(w, j0, KE)) continue;
                         const uint32_t st = (e + C::kParts * value_place<NQ>(t, w.cnt) + h) % ST;
                         bar_wait(smem_addr(&sh.edge[st]), (phase >> st) & 1, failed);
                         phase ^= 1u << st;
                         char* v = tiles + NQ * C::kQ + st * C::kBytes;
-                        // rows [0, a) and [d, KE) are nobody's, [a, b) and [c, d) some rows'
-                        const int a = min(max(w.keys.lo - j0, 0), KE), d = min(max(w.keys.hi - j0, a), KE);
-                        const int b = min(max(w.keys.flo - j0, a), d), c = min(max(w.keys.fhi - j0, b), d);
-                        constexpr int kRow = DP / 8;  // chunks of a row
+                        constexpr int kRow = CW / 8;  // chunks of a row
+                        const int me = tid - 64;
+                        uint32_t odd = 0;
                         auto wipe = [&](int from, int to) {
-                            for (int i = from * kRow + lane; i < to * kRow; i += 32) {
-                                *reinterpret_cast<uint4*>(v + panel_at<KE>(i / kRow, i % kRow)) = make_uint4(0u, 0u, 0u, 0u);
+                            for (int i = from * kRow + me; i < to * kRow; i += 64) {
+                                *reinterpret_cast<uint4*>(v + panel_at<KT>(i / kRow, i % kRow)) = make_uint4(0u, 0u, 0u, 0u);
                             }
                         };
-                        bool odd = false;
                         auto scan = [&](int from, int to) {
 #pragma unroll 8
-                            for (int i = from * kRow + lane; i < to * kRow; i += 32) {
-                                const uint4 y = *reinterpret_cast<const uint4*>(v + panel_at<KE>(i / kRow, i % kRow));
-                                odd |= unbounded<T>(y.x) | unbounded<T>(y.y) | unbounded<T>(y.z) | unbounded<T>(y.w);
+                            for (int i = from * kRow + me; i < to * kRow; i += 64) {
+                                const uint4 y = *reinterpret_cast<const uint4*>(v + panel_at<KT>(i / kRow, i % kRow));
+                                odd |= exponent_bits<T>(y.x) | exponent_bits<T>(y.y) | exponent_bits<T>(y.z) | exponent_bits<T>(y.w);
                             }
                         };
                         wipe(0, a);
-                        wipe(d, KE);
+                        wipe(d, KT);
                         scan(a, b);
                         scan(c, d);
-                        if (__any_sync(0xffffffffu, odd) && lane == 0) atomicOr(&sh.careful, 1u << (unit & 31));
+                        if (__any_sync(0xffffffffu, (odd & 0x80008000u) != 0) && lane == 0) atomicOr(&sh.careful, 1u << (unit & 31));
                         fence_async_smem();
-                        __syncwarp();
-                        if (lane == 0) bar_arrive(smem_addr(&sh.full[st]));
+                        asm volatile("bar.sync 2, 64;" ::: "memory");
+                        if (me == 0) bar_arrive(smem_addr(&sh.full[st]));
                     }
                 }
                 e += 2 * C::kParts * w.cnt;
@@ -588,7 +610,8 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
         const uint32_t lanes = (uint32_t)(wid & 3) << 21;  // 32 lanes of TMEM per warp
         const uint32_t to = tmem + 256 + i * 128 + lanes;
         char* qt = tiles + i * C::kQ;
-        uint32_t step = 0, done = 0, unit = 0;
+        // products given (tiles, or half tiles with one query tile), tiles, units
+        uint32_t step = 0, tiles_done = 0, done = 0, unit = 0;
         // this group's queries of a unit into shared memory: one box per 64
         // channels where the heads of the group divide a tile, else row by row
         auto fetch = [&](const Walk& u) {
@@ -599,7 +622,7 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                     const int tok = u.s.q0 + (int)fast_div((uint32_t)r0, p.gdiv);
                     bar_expect(bar, C::kQ, 1);
 #pragma unroll
-                    for (int panel = 0; panel < C::kPanels; ++panel) {
+                    for (int panel = 0; panel < C::kQPanels; ++panel) {
                         tma_load(smem_addr(qt) + panel * (kTile * 128), &qmap, panel * 64, u.h * p.G, tok, bar, 1);
                     }
                 }
@@ -649,98 +672,175 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                 return t < b && lane * box < kTile && j < w.s.L && key_slot(p, w.b, j) < 0;
             };
             bool gone = missing(a);
+            const uint32_t first_step = step;
             for (int t = a; t < b; ++t) {
                 const int j0 = (w.k0 + w.off + t) * KT;
                 const uint32_t lost = __ballot_sync(0xffffffffu, gone);
                 gone = missing(t + 1);
                 // two query tiles: each its own S; one: the two S in turn
-                const uint32_t buf = NQ == 2 ? i : step & 1;
+                const uint32_t buf = NQ == 2 ? i : tiles_done & 1;
                 const uint32_t ts = tmem + buf * 128 + lanes;
-                bar_wait(smem_addr(&sh.s_full[buf]), (NQ == 2 ? step : step >> 1) & 1, failed);
+                bar_wait(smem_addr(&sh.s_full[buf]), (NQ == 2 ? tiles_done : tiles_done >> 1) & 1, failed);
                 tc_after();
-                float s[KT];
-#pragma unroll
-                for (int c = 0; c < KT / 32; ++c) tc_ld32(ts + c * 32, reinterpret_cast<uint32_t*>(s) + c * 32);
-                tc_wait_ld();
-                // the last scores of the unit are read: its queries are done with
+                // the last scores of the unit are computed: its queries are done with
                 if (t == b - 1 && na < nb) fetch(nw);
-                if (lost || j0 < keys.flo || j0 + KT > keys.fhi) {
-                    const int lo = from - j0, hi = upto - j0;
+                const bool masked = lost || j0 < keys.flo || j0 + KT > keys.fhi;
+                // the columns first .. first + 31 that this row sees
+                auto seen_of = [&](int first) {
+                    uint32_t seen = bits_below(upto - j0 - first) & ~bits_below(from - j0 - first);
+                    if (lost) {
+                        for (int k = 0; k < 32; k += 8) {  // a page is 8 keys at least
+                            if ((lost >> ((first + k) >> box_shift)) & 1u) seen &= ~(0xffu << k);
+                        }
+                    }
+                    return seen;
+                };
+                if constexpr (NQ == 2) {
+                    float s[KT];
 #pragma unroll
-                    for (int c = 0; c < KT / 32; ++c) {
-                        uint32_t seen = bits_below(hi - c * 32) & ~bits_below(lo - c * 32);
-                        if (lost) {
-                            for (int k = 0; k < 32; k += 8) {  // a page is 8 keys at least
-                                if ((lost >> ((c * 32 + k) >> box_shift)) & 1u) seen &= ~(0xffu << k);
+                    for (int c = 0; c < KT / 32; ++c) tc_ld32(ts + c * 32, reinterpret_cast<uint32_t*>(s) + c * 32);
+                    tc_wait_ld();
+                    if (masked) {
+#pragma unroll
+                        for (int c = 0; c < KT / 32; ++c) {
+                            const uint32_t seen = seen_of(c * 32);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) {
+                                if (!((seen >> k) & 1u)) s[c * 32 + k] = -INFINITY;
                             }
                         }
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            if (!((seen >> k) & 1u)) s[c * 32 + k] = -INFINITY;
-                        }
                     }
-                }
-                float top[4] = {s[0], s[1], s[2], s[3]};
+                    float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                for (int c = 4; c < KT; c += 4) {
+                    for (int c = 4; c < KT; c += 4) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) top[k] = fmaxf(top[k], s[c + k]);
-                }
-                const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
-                if (t == a) {
-                    ref = high;
-                } else if (__any_sync(0xffffffffu, high > ref + 8.0f)) {
-                    // lazily: the reference moves only when the weights would
-                    // pass 2^8.  The products into O before must be complete:
-                    // with two query tiles the commit of S is behind them
-                    if constexpr (NQ == 1) {
-                        bar_wait(smem_addr(&sh.o_full[0]), (step - 1) & 1, failed);
-                        tc_after();
+                        for (int k = 0; k < 4; ++k) top[k] = fmaxf(top[k], s[c + k]);
                     }
-                    const float next = fmaxf(ref, high);
-                    const float keep = next == -INFINITY ? 1.0f : ex2(ref - next);
-                    ref = next;
-                    sum *= keep;
+                    const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
+                    if (t == a) {
+                        ref = high;
+                    } else if (__any_sync(0xffffffffu, high > ref + 8.0f)) {
+                        // lazily: the reference moves only when the weights would
+                        // pass 2^8.  The products into O before must be complete:
+                        // with two query tiles the commit of S is behind them
+                        const float next = fmaxf(ref, high);
+                        const float keep = next == -INFINITY ? 1.0f : ex2(ref - next);
+                        ref = next;
+                        sum *= keep;
 #pragma unroll 1
-                    for (int c = 0; c < DP / 16; ++c) {
-                        uint32_t o[16];
-                        tc_ld16(to + c * 16, o);
-                        tc_wait_ld();
+                        for (int c = 0; c < DP / 16; ++c) {
+                            uint32_t o[16];
+                            tc_ld16(to + c * 16, o);
+                            tc_wait_ld();
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
-                        tc_st16(to + c * 16, o);
+                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
+                            tc_st16(to + c * 16, o);
+                        }
+                        tc_wait_st();
                     }
+                    const float sub = ref == -INFINITY ? 0.0f : -ref;
+                    const float2 f2 = splat2(p.scale_log2), r2 = splat2(sub);
+                    float2 acc[2] = {splat2(0.0f), splat2(0.0f)};
+#pragma unroll
+                    for (int c = 0; c < KT / 32; ++c) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            float2 x = __ffma2_rn(make_float2(s[c * 32 + 2 * k], s[c * 32 + 2 * k + 1]), f2, r2);
+                            x.x = ex2(x.x);
+                            x.y = ex2(x.y);
+                            acc[k & 1] = __fadd2_rn(acc[k & 1], x);
+                            pk[k] = pack2<T>(x.x, x.y);
+                        }
+                        tc_st16(ts + c * 16, pk);
+                    }
+                    sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
                     tc_wait_st();
-                }
-                const float sub = ref == -INFINITY ? 0.0f : -ref;
-                const float2 f2 = splat2(p.scale_log2), r2 = splat2(sub);
-                float2 acc[2] = {splat2(0.0f), splat2(0.0f)};
+                    tc_before();
+                    bar_arrive(smem_addr(&sh.p_full[i]));
+                    ++step;
+                } else {
+                    // Half of the tile at a time, so that the product with the first
+                    // 64 values runs under the second half's exponentials.  One pass
+                    // with the reference as it is; only where a row's maximum passes
+                    // it by more than 2^8 (or it is the unit's first half) is the
+                    // reference moved, O rescaled and the half done again: the result
+                    // carries the same factor in numerator and sum.  The code is kept
+                    // short: a form unrolled over all 128 columns outgrew the
+                    // instruction cache beside the other roles, and the same
+                    // arithmetic took two to three times as long.
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half, ++step) {
+                        uint32_t x[64], pk[32];
+                        tc_ld32(ts + half * 64, x);
+                        tc_ld32(ts + half * 64 + 32, x + 32);
+                        tc_wait_ld();
+                        if (masked) {
 #pragma unroll
-                for (int c = 0; c < KT / 32; ++c) {
-                    uint32_t pk[16];
+                            for (int c = 0; c < 2; ++c) {
+                                const uint32_t seen = seen_of(half * 64 + c * 32);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        float2 x = __ffma2_rn(make_float2(s[c * 32 + 2 * k], s[c * 32 + 2 * k + 1]), f2, r2);
-                        x.x = ex2(x.x);
-                        x.y = ex2(x.y);
-                        acc[k & 1] = __fadd2_rn(acc[k & 1], x);
-                        pk[k] = pack2<T>(x.x, x.y);
+                                for (int k = 0; k < 32; ++k) {
+                                    if (!((seen >> k) & 1u)) x[c * 32 + k] = __float_as_uint(-INFINITY);
+                                }
+                            }
+                        }
+                        float2 acc[2];
+                        bool early = step != first_step;
+                        for (;;) {
+                            const float2 f2 = splat2(p.scale_log2), r2 = splat2(ref == -INFINITY ? 0.0f : -ref);
+                            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                            acc[0] = splat2(0.0f);
+                            acc[1] = splat2(0.0f);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) {
+                                const float2 s2 = make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
+                                top[k & 3] = fmaxf(top[k & 3], fmaxf(s2.x, s2.y));
+                                float2 y = __ffma2_rn(s2, f2, r2);
+                                y.x = ex2(y.x);
+                                y.y = ex2(y.y);
+                                acc[k & 1] = __fadd2_rn(acc[k & 1], y);
+                                pk[k] = pack2<T>(y.x, y.y);
+                            }
+                            if (early) {
+                                // the product before is complete (every phase of the
+                                // barrier is waited for, so a parity names one phase)
+                                bar_wait(smem_addr(&sh.o_full[i]), (step - 1) & 1, failed);
+                                tc_after();
+                                early = false;
+                            }
+                            const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
+                            if (!__any_sync(0xffffffffu, high > ref + 8.0f)) break;
+                            const float next = fmaxf(ref, high);
+                            const float keep = next == -INFINITY ? 1.0f : ex2(ref - next);
+                            ref = next;
+                            sum *= keep;
+                            if (step != first_step) {
+#pragma unroll 1
+                                for (int c = 0; c < DP / 16; ++c) {
+                                    uint32_t o[16];
+                                    tc_ld16(to + c * 16, o);
+                                    tc_wait_ld();
+#pragma unroll
+                                    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
+                                    tc_st16(to + c * 16, o);
+                                }
+                            }
+                        }
+                        sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+                        // over scores that are read: the halves' weights lie in the
+                        // first half's columns
+                        tc_st32(ts + half * 32, pk);
+                        tc_wait_st();
+                        tc_before();
+                        bar_arrive(smem_addr(&sh.p_full[i]));
                     }
-                    tc_st16(ts + c * 16, pk);
                 }
-                sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
-                tc_wait_st();
-                tc_before();
-                // every phase of o_full is waited for, so that a parity names
-                // one phase only
-                if (NQ == 1 && t > a) bar_wait(smem_addr(&sh.o_full[0]), (step - 1) & 1, failed);
-                bar_arrive(smem_addr(&sh.p_full[buf]));
-                ++step;
+                ++tiles_done;
             }
             // ---- the unit's end
             if (a < b) {
-                bar_wait(smem_addr(&sh.o_full[i]), (NQ == 2 ? done : step - 1) & 1, failed);
-                ++done;
+                bar_wait(smem_addr(&sh.o_full[i]), (NQ == 2 ? done++ : step - 1) & 1, failed);
                 tc_after();
             } else if (na < nb) {
                 fetch(nw);
@@ -858,9 +958,6 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                 if (slot == 1 && row == 0 && i == 0) write_desc(p, w);
                 tc_before();
             }
-            // the softmax warps are done with the unit's mark
-            asm volatile("bar.sync 1, %0;" ::"n"(C::kThreads - 128) : "memory");
-            if (tid == 128) atomicAnd(&sh.careful, ~(1u << (unit & 31)));
             ++unit;
             w = nw;
             a = na;
@@ -916,8 +1013,7 @@ bool query_map(CUtensorMap* map, const AttnP& p, int dt) {
 bool cache_map(CUtensorMap* map, const AttnP& p, const char* base, int dt) {
     const cuuint64_t dims[3] = {(cuuint64_t)p.D, (cuuint64_t)p.hk, (cuuint64_t)p.num_pages * p.page_size};
     const cuuint64_t strides[2] = {(cuuint64_t)p.D * 2, (cuuint64_t)p.hk * p.D * 2};
-    const int keys = p.D <= 128 ? Tc<128>::kKeys : Tc<256>::kKeys;
-    const cuuint32_t box[3] = {64, 1, (cuuint32_t)(p.page_size < keys ? p.page_size : keys)};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)(p.page_size < kTile ? p.page_size : kTile)};
     const cuuint32_t ones[3] = {1, 1, 1};
     return encoder()(map, dt == kF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                      const_cast<char*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,

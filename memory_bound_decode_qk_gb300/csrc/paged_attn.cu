@@ -192,17 +192,19 @@ __global__ void __launch_bounds__(kAnyThreads) attn_any_kernel(AttnP p) {
 }
 
 // Joins the parts of the unit that started in piece blockIdx.x without ending
-// there: with M = max m_i, out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.  The
-// rows are spread over blockIdx.y; eight warps share a row's parts, a lane has
-// every 32nd channel, and the warps' sums are added in their order.
+// there: with M = max m_i, out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.  Eight
+// warps; W of them share a row's parts (a lane has every 32nd channel, the
+// warps' sums are added in their order), so a CTA does 8 / W rows at a time.
 constexpr int kJoinWarps = 8;
-template <typename T, int M>
+template <typename T, int M, int W>
 __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnP p) {
-    __shared__ float acc_of[kJoinWarps][256];
+    constexpr int R = kJoinWarps / W;
+    __shared__ float acc_of[W > 1 ? kJoinWarps : 1][256];
     __shared__ float top_of[kJoinWarps], sum_of[kJoinWarps];
     pdl_wait();
     pdl_launch_dependents();
     const int c0 = blockIdx.x, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    const int sub = wid % W, set = wid / W * W;
     const int4 u = p.desc[c0];
     if (u.w < 0) return;
     const Seq s = load_seq(p, u.x);
@@ -210,23 +212,25 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnP p) {
     const int64_t rec = M * (int64_t)p.D + 2 * M;
     // parts: slot 1 of c0, then slot 0 of c0 + 1 .. u.w
     const float* base = p.part + ((int64_t)c0 * 2 + 1) * rec;
+    auto part = [&](int i) { return base + (i == 0 ? 0 : (2 * i - 1) * rec); };
     const int n = u.w - c0 + 1;
-    for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    for (int r0 = blockIdx.y * R; r0 < rows; r0 += gridDim.y * R) {
+        const int r = min(r0 + wid / W, rows - 1);  // warps past the last row repeat it
         float top = -INFINITY;
-        for (int i = wid * 32 + lane; i < n; i += 32 * kJoinWarps) {
-            top = fmaxf(top, base[(i == 0 ? 0 : (2 * i - 1) * rec) + M * p.D + r]);
-        }
+        for (int i = sub * 32 + lane; i < n; i += 32 * W) top = fmaxf(top, part(i)[M * p.D + r]);
         top = group_max<32>(top);
-        if (lane == 0) top_of[wid] = top;
-        __syncthreads();
-        for (int i = 0; i < kJoinWarps; ++i) top = fmaxf(top, top_of[i]);
+        if constexpr (W > 1) {
+            if (lane == 0) top_of[wid] = top;
+            __syncthreads();
+            for (int i = 0; i < W; ++i) top = fmaxf(top, top_of[set + i]);
+        }
         const float ref = top == -INFINITY ? 0.0f : top;
         float l = 0.0f, acc[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) acc[k] = 0.0f;
 #pragma unroll 2
-        for (int i = wid; i < n; i += kJoinWarps) {
-            const float* pc = base + (i == 0 ? 0 : (2 * i - 1) * rec);
+        for (int i = sub; i < n; i += W) {
+            const float* pc = part(i);
             // a part that saw nothing wrote no outputs
             const float f = ex2(pc[M * p.D + r] - ref);
             if (f == 0.0f) continue;
@@ -237,22 +241,32 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnP p) {
                 if (d < p.D) acc[k] = fmaf(f, pc[(int64_t)r * p.D + d], acc[k]);
             }
         }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) acc_of[wid][lane + 32 * k] = acc[k];
-        if (lane == 0) sum_of[wid] = l;
-        __syncthreads();
-        l = 0.0f;
-        for (int i = 0; i < kJoinWarps; ++i) l += sum_of[i];
         const int64_t orow = out_row(p, s, u.y, u.z * M + r);
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        const int d = threadIdx.x;
-        if (d < p.D) {
-            float y = 0.0f;
-            for (int i = 0; i < kJoinWarps; ++i) y += acc_of[i][d];
-            store_one<T>(p, orow * p.D + d, y * inv);
+        const bool mine = r0 + wid / W < rows;
+        if constexpr (W > 1) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) acc_of[wid][lane + 32 * k] = acc[k];
+            if (lane == 0) sum_of[wid] = l;
+            __syncthreads();
+            l = 0.0f;
+            for (int i = 0; i < W; ++i) l += sum_of[set + i];
         }
-        if (d == 0 && p.lse != nullptr) p.lse[orow] = row_lse(top, l);
-        __syncthreads();  // the shared sums are read before the next row's
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        if constexpr (W > 1) {
+            for (int d = sub * 32 + lane; mine && d < p.D; d += 32 * W) {
+                float y = 0.0f;
+                for (int i = 0; i < W; ++i) y += acc_of[set + i][d];
+                store_one<T>(p, orow * p.D + d, y * inv);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int d = lane + 32 * k;
+                if (mine && d < p.D) store_one<T>(p, orow * p.D + d, acc[k] * inv);
+            }
+        }
+        if (mine && sub == 0 && lane == 0 && p.lse != nullptr) p.lse[orow] = row_lse(top, l);
+        if constexpr (W > 1) __syncthreads();  // the shared sums are read before the next rows'
     }
 }
 
@@ -272,20 +286,34 @@ cudaError_t launch_any(const AttnP& p, bool vec, cudaLaunchConfig_t cfg) {
     return cudaLaunchKernelEx(&cfg, fn, p);
 }
 
+template <typename T, int W>
+cudaError_t launch_join_of(const AttnP& p, int M, cudaLaunchConfig_t cfg) {
+    switch (M) {
+        case 16: return cudaLaunchKernelEx(&cfg, attn_join_kernel<T, 16, W>, p);
+        case 64: return cudaLaunchKernelEx(&cfg, attn_join_kernel<T, 64, W>, p);
+        case 128: return cudaLaunchKernelEx(&cfg, attn_join_kernel<T, 128, W>, p);
+        default: return cudaLaunchKernelEx(&cfg, attn_join_kernel<T, 256, W>, p);
+    }
+}
+
 template <typename T>
 cudaError_t launch_join(const AttnP& p, const AttnShape& sh, cudaLaunchConfig_t cfg) {
-    const int rows = sh.M < p.tokens * (int64_t)p.G ? sh.M : (int)(p.tokens * (int64_t)p.G);
-    cfg.gridDim = dim3((unsigned)(sh.ctas * sh.per_cta), rows < 16 ? rows : 16);
+    const int64_t all = p.tokens * (int64_t)p.G;
+    const int rows = sh.M < all ? sh.M : (int)all;
+    const int pieces = sh.ctas * sh.per_cta;
+    // a unit spans few pieces when there are about as many units: a warp per
+    // row then (one CTA per unit), else the eight warps of a CTA share a row
+    const bool few = pieces <= 8 * (int64_t)p.num_seqs * p.hk;
+    const int r = few ? kJoinWarps : 1;
+    const int y = (rows + r - 1) / r;
+    cfg.gridDim = dim3((unsigned)pieces, y < 16 ? y : 16);
     cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.dynamicSmemBytes = 0;
-    if (sh.M == 16) return cudaLaunchKernelEx(&cfg, attn_join_kernel<T, 16>, p);
-    if (sh.M == 64) return cudaLaunchKernelEx(&cfg, attn_join_kernel<T, 64>, p);
-    if (sh.M == 128) return cudaLaunchKernelEx(&cfg, attn_join_kernel<T, 128>, p);
-    return cudaLaunchKernelEx(&cfg, attn_join_kernel<T, 256>, p);
+    return few ? launch_join_of<T, 1>(p, sh.M, cfg) : launch_join_of<T, kJoinWarps>(p, sh.M, cfg);
 }
 
 // Two CTAs per SM fit at every head size (at most 88 KB each).
-AttnShape any_shape() { return AttnShape{kPathAny, kAnyM, 2 * sm_count(), 1}; }
+AttnShape any_shape() { return AttnShape{kPathAny, kAnyM, kAnyKT, kAnyUC, 2 * sm_count(), 1}; }
 
 int64_t shape_bytes(const AttnShape& sh, int head_dim) {
     return (int64_t)sh.ctas * sh.per_cta * (16 + 2 * 4 * ((int64_t)sh.M * head_dim + 2 * sh.M));
@@ -346,7 +374,16 @@ cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s) {
         if (rows > 64 && tc_suits(p)) sh = tc_shape(a.head_dim);
         else sh = mma_shape(rows <= 16 ? kPathFew : kPathMore, a.dt, a.head_dim);
     }
-    p.min_per = sh.path == kPathFew ? 4 : 1;
+    p.min_per = sh.path == kPathFew ? 2 : 1;
+    // no more CTAs than there can be pieces: the table's width bounds the tiles
+    // of a unit, the tokens the units
+    {
+        const int64_t units = a.num_seqs + a.tokens * p.G / sh.M;
+        const int64_t tiles = p.max_len / sh.KT + 2 + sh.UC;
+        const int64_t most = (units * a.kv_heads * tiles + p.min_per - 1) / p.min_per;
+        const int64_t ctas = (most + sh.per_cta - 1) / sh.per_cta;
+        if (ctas < sh.ctas) sh.ctas = ctas > 1 ? (int)ctas : 1;
+    }
     p.desc = static_cast<int4*>(a.workspace);
     p.part = reinterpret_cast<float*>(p.desc + sh.ctas * sh.per_cta);
 

@@ -653,7 +653,8 @@ AttnShape mma_shape(AttnPath path, int dt, int head_dim) {
     (void)dt;
     const int per_sm = padded(head_dim) <= 128 ? 2 : 1;
     const bool few = path == kPathFew;
-    return AttnShape{path, few ? 16 : 64, per_sm * sm_count(), few ? kFewWarps : 1};
+    return AttnShape{path, few ? 16 : 64, few ? kFewKeys : kMoreKeys, few ? kFewUC : kMoreUC, per_sm * sm_count(),
+                     few ? kFewWarps : 1};
 }
 
 cudaError_t launch_attn_mma(const AttnP& p, const AttnShape& sh, int dt, cudaLaunchConfig_t cfg) {

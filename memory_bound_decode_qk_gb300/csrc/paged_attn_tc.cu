@@ -40,7 +40,6 @@ namespace edge {
 namespace {
 
 constexpr int kTile = 128;  // query rows of a tile, and keys of a tile
-constexpr int kTcUC = 2;
 constexpr uint64_t kWaitLimit = 2000000000ull;  // nanoseconds
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
@@ -276,6 +275,7 @@ template <int DP>
 struct Tc {
     static constexpr int kNQ = DP <= 128 ? 2 : 1;       // query tiles of a unit
     static constexpr int kM = kNQ * kTile;
+    static constexpr int kUC = kNQ == 2 ? 2 : 4;        // a unit's start and end, in key tiles
     // a ring entry: 128 keys and CW channels of them.  Wide heads are cut by
     // channels, not by keys: 64-key operands made the pipe read Q twice as often
     // from shared memory, whose bandwidth then bound it (3100 cycles a tile).
@@ -341,7 +341,7 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
     pdl_launch_dependents();
     if (tid == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, -1);
     Walk w;
-    if (!walk_begin<M, KT, kTcUC, 1>(p, w, wsm, C::kThreads, 0)) return;
+    if (!walk_begin<M, KT, C::kUC, 1>(p, w, wsm, C::kThreads, 0)) return;
 
     if (wid == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem)) : "memory");
@@ -428,7 +428,7 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                     copy(t, true, now);
                     now = next;
                 }
-                go = uniform(walk_next<M, KT, kTcUC>(p, w));
+                go = uniform(walk_next<M, KT, C::kUC>(p, w));
             } while (go);
         } else if (wid == 1) {
             // ---- products
@@ -549,7 +549,7 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                         }
                     }
                     e += 2 * C::kParts * cnt;
-                    go = uniform(walk_next<M, KT, kTcUC>(p, w));
+                    go = uniform(walk_next<M, KT, C::kUC>(p, w));
                 } while (go);
             }
         } else {
@@ -600,7 +600,7 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                 }
                 e += 2 * C::kParts * w.cnt;
                 ++unit;
-            } while (walk_next<M, KT, kTcUC>(p, w));
+            } while (walk_next<M, KT, C::kUC>(p, w));
         }
     } else {
         if constexpr (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
@@ -652,7 +652,7 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
         }
         for (bool go = true; go;) {
             Walk nw = w;
-            go = walk_next<M, KT, kTcUC>(p, nw);
+            go = walk_next<M, KT, C::kUC>(p, nw);
             int na = 0, nb = 0;
             if (go) tile_span<NQ>(p, nw, i, na, nb);
             const int r0 = w.rt * M + i * kTile;
@@ -1033,7 +1033,10 @@ cudaError_t launch_typed(const AttnP& p, const CUtensorMap (&m)[3], int q_boxes,
 
 }  // namespace
 
-AttnShape tc_shape(int head_dim) { return AttnShape{kPathMany, head_dim <= 128 ? Tc<128>::kM : Tc<256>::kM, sm_count(), 1}; }
+AttnShape tc_shape(int head_dim) {
+    const bool wide = head_dim > 128;
+    return AttnShape{kPathMany, wide ? Tc<256>::kM : Tc<128>::kM, kTile, wide ? Tc<256>::kUC : Tc<128>::kUC, sm_count(), 1};
+}
 
 // 16-byte aligned 16-bit tensors of heads of at least 64 channels (a multiple of
 // 8); pages of 8, 16, 32, 64 or a multiple of 128 tokens, so that a ring entry

@@ -319,12 +319,12 @@ __device__ __forceinline__ void store_one(const AttnP& p, int64_t e, float y) {
     }
 }
 
-// A path of the operator: its rows per unit, its grid (CTAs that are resident
-// together) and the pieces each CTA takes.
+// A path of the operator: rows of a unit, keys of a tile, a unit's constant in the
+// line, its grid (CTAs that are resident together) and the pieces each takes.
 enum AttnPath { kPathAny = 0, kPathFew = 1, kPathMore = 2, kPathMany = 3 };
 struct AttnShape {
     AttnPath path;
-    int M;
+    int M, KT, UC;
     int ctas;
     int per_cta;
 };

@@ -373,6 +373,8 @@ def _plain(device, stream):
 
 def _want(t, name, dtype, shape, device):
     """t is a contiguous tensor of this dtype, shape (None: any extent) and device."""
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if t.device != device:

@@ -60,6 +60,35 @@ int resident_ctas(const void* fn, int threads) {
     return n;
 }
 
+cudaError_t allow_smem(const void* fn, int bytes) {
+    if (bytes <= 40 * 1024) return cudaSuccess;  // 48 KB with the static part need no leave
+    struct Entry {
+        const void* fn;
+        int dev, bytes;
+    };
+    static std::mutex mu;
+    static Entry table[128];
+    static int used = 0;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    int at = used;
+    for (int i = 0; i < used; ++i) {
+        if (table[i].fn == fn && table[i].dev == dev) {
+            if (table[i].bytes >= bytes) return cudaSuccess;
+            at = i;
+            break;
+        }
+    }
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && at < 128) {
+        table[at] = Entry{fn, dev, bytes};
+        if (at == used) ++used;
+    }
+    return e;
+}
+
 bool pdl_enabled() {
     static const bool on = [] {
         const char* v = std::getenv("EDGE_OPS_PDL");

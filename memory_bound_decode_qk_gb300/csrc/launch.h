@@ -156,6 +156,10 @@ int sm_count();
 // shared memory (the occupancy calculator, cached per kernel and device).
 int resident_ctas(const void* fn, int threads);
 
+// Lets kernel `fn` use `bytes` of dynamic shared memory (asked of the runtime
+// once per kernel and device).
+cudaError_t allow_smem(const void* fn, int bytes);
+
 // Programmatic dependent launch for all ops (on unless EDGE_OPS_PDL=0 in the
 // environment, read once per process).  Every kernel executes
 // griddepcontrol.wait before its first global load whose value it uses, so

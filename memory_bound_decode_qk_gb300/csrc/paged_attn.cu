@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kAnyThreads) attn_any_kernel(AttnP p) {
 
     pdl_wait();
     pdl_launch_dependents();
-    if (tid == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, -1);
+    if (tid == 0) clear_desc(p, blockIdx.x);
     // the padding channels stay zero
     for (int i = tid; i < (M + 2 * KT) * ds; i += kAnyThreads) smem[i] = 0.0f;
 
@@ -205,57 +205,64 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnP p) {
     pdl_launch_dependents();
     const int c0 = blockIdx.x, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const int sub = wid % W, set = wid / W * W;
-    const int4 u = p.desc[c0];
-    if (u.w < 0) return;
-    const Seq s = load_seq(p, u.x);
+    const int4 u = p.desc[2 * c0], v = p.desc[2 * c0 + 1];
+    if (u.x < 0) return;
+    const Seq s{v.x, v.y, 0};
     const int rows = min(M, s.n * p.G - u.z * M);
     const int64_t rec = M * (int64_t)p.D + 2 * M;
-    // parts: slot 1 of c0, then slot 0 of c0 + 1 .. u.w
+    // parts: slot 1 of c0, then slot 0 of c0 + 1 .. u.x
     const float* base = p.part + ((int64_t)c0 * 2 + 1) * rec;
-    auto part = [&](int i) { return base + (i == 0 ? 0 : (2 * i - 1) * rec); };
-    const int n = u.w - c0 + 1;
+    const int n = u.x - c0 + 1;
     for (int r0 = blockIdx.y * R; r0 < rows; r0 += gridDim.y * R) {
         const int r = min(r0 + wid / W, rows - 1);  // warps past the last row repeat it
-        float top = -INFINITY;
-        for (int i = sub * 32 + lane; i < n; i += 32 * W) top = fmaxf(top, part(i)[M * p.D + r]);
-        top = group_max<32>(top);
-        if constexpr (W > 1) {
-            if (lane == 0) top_of[wid] = top;
-            __syncthreads();
-            for (int i = 0; i < W; ++i) top = fmaxf(top, top_of[set + i]);
-        }
-        const float ref = top == -INFINITY ? 0.0f : top;
-        float l = 0.0f, acc[8];
+        // one pass over this warp's parts with their running maximum
+        float top = -INFINITY, l = 0.0f, acc[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) acc[k] = 0.0f;
 #pragma unroll 2
         for (int i = sub; i < n; i += W) {
-            const float* pc = part(i);
-            // a part that saw nothing wrote no outputs
-            const float f = ex2(pc[M * p.D + r] - ref);
-            if (f == 0.0f) continue;
-            l = fmaf(f, pc[M * p.D + M + r], l);
+            const float* pc = base + (i == 0 ? 0 : (2 * i - 1) * rec);
+            const float m = pc[M * p.D + r], li = pc[M * p.D + M + r];
+            float x[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const int d = lane + 32 * k;
-                if (d < p.D) acc[k] = fmaf(f, pc[(int64_t)r * p.D + d], acc[k]);
+                x[k] = d < p.D ? pc[(int64_t)r * p.D + d] : 0.0f;
+            }
+            // (a part that saw nothing has m = -inf and wrote no outputs)
+            if (m == -INFINITY) continue;
+            const float next = fmaxf(top, m);
+            const float keep = ex2(top - next), f = ex2(m - next);
+            top = next;
+            l = fmaf(l, keep, f * li);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) acc[k] = fmaf(acc[k], keep, f * x[k]);
+        }
+        if constexpr (W > 1) {
+            if (lane == 0) {
+                top_of[wid] = top;
+                sum_of[wid] = l;
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) acc_of[wid][lane + 32 * k] = acc[k];
+            __syncthreads();
+            float all = -INFINITY;
+            for (int i = 0; i < W; ++i) all = fmaxf(all, top_of[set + i]);
+            top = all;
+            l = 0.0f;
+            for (int i = 0; i < W; ++i) {
+                if (top_of[set + i] != -INFINITY) l = fmaf(ex2(top_of[set + i] - top), sum_of[set + i], l);
             }
         }
         const int64_t orow = out_row(p, s, u.y, u.z * M + r);
         const bool mine = r0 + wid / W < rows;
-        if constexpr (W > 1) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) acc_of[wid][lane + 32 * k] = acc[k];
-            if (lane == 0) sum_of[wid] = l;
-            __syncthreads();
-            l = 0.0f;
-            for (int i = 0; i < W; ++i) l += sum_of[set + i];
-        }
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         if constexpr (W > 1) {
             for (int d = sub * 32 + lane; mine && d < p.D; d += 32 * W) {
                 float y = 0.0f;
-                for (int i = 0; i < W; ++i) y += acc_of[set + i][d];
+                for (int i = 0; i < W; ++i) {
+                    if (top_of[set + i] != -INFINITY) y = fmaf(ex2(top_of[set + i] - top), acc_of[set + i][d], y);
+                }
                 store_one<T>(p, orow * p.D + d, y * inv);
             }
         } else {
@@ -278,11 +285,8 @@ cudaError_t launch_any(const AttnP& p, bool vec, cudaLaunchConfig_t cfg) {
     if (p.D <= 64) fn = vec ? attn_any_kernel<T, 2, true> : attn_any_kernel<T, 2, false>;
     else if (p.D <= 128) fn = vec ? attn_any_kernel<T, 4, true> : attn_any_kernel<T, 4, false>;
     else fn = vec ? attn_any_kernel<T, 8, true> : attn_any_kernel<T, 8, false>;
-    if (cfg.dynamicSmemBytes > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)cfg.dynamicSmemBytes);
-        if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = allow_smem((const void*)fn, (int)cfg.dynamicSmemBytes);
+    if (e != cudaSuccess) return e;
     return cudaLaunchKernelEx(&cfg, fn, p);
 }
 
@@ -316,7 +320,7 @@ cudaError_t launch_join(const AttnP& p, const AttnShape& sh, cudaLaunchConfig_t 
 AttnShape any_shape() { return AttnShape{kPathAny, kAnyM, kAnyKT, kAnyUC, 2 * sm_count(), 1}; }
 
 int64_t shape_bytes(const AttnShape& sh, int head_dim) {
-    return (int64_t)sh.ctas * sh.per_cta * (16 + 2 * 4 * ((int64_t)sh.M * head_dim + 2 * sh.M));
+    return (int64_t)sh.ctas * sh.per_cta * (32 + 2 * 4 * ((int64_t)sh.M * head_dim + 2 * sh.M));
 }
 
 }  // namespace
@@ -385,7 +389,7 @@ cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s) {
         if (ctas < sh.ctas) sh.ctas = ctas > 1 ? (int)ctas : 1;
     }
     p.desc = static_cast<int4*>(a.workspace);
-    p.part = reinterpret_cast<float*>(p.desc + sh.ctas * sh.per_cta);
+    p.part = reinterpret_cast<float*>(p.desc + 2 * (int64_t)sh.ctas * sh.per_cta);
 
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];

@@ -265,8 +265,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, DP <= 128 ? 2 : 1) attn_few_ke
 
     pdl_wait();
     pdl_launch_dependents();
-    if (tid < kFewWarps) p.desc[blockIdx.x + gridDim.x * tid] = make_int4(0, 0, 0, -1);
-    __syncthreads();
+    if (lane == 0) clear_desc(p, blockIdx.x + gridDim.x * wid);
 
     Walk w;
     if (!walk_begin<M, KT, UC, kFewWarps>(p, w, wsm, kFewWarps * 32, wid)) return;
@@ -319,23 +318,35 @@ __global__ void __launch_bounds__(kFewWarps * 32, DP <= 128 ? 2 : 1) attn_few_ke
         }
         cp_async_commit();
     };
+    // wide heads: a unit's queries into shared memory
+    auto queries = [&] {
+        const int rows = w.s.n * p.G - w.rt * M;
+#pragma unroll 4
+        for (int i = lane; i < 16 * (DP / 8); i += 32) {
+            const int r = i / (DP / 8), c = i % (DP / 8);
+            const bool ok = r < rows && c * 8 < p.D;
+            const int64_t e = ok ? out_row(p, w.s, w.h, w.rt * M + r) * p.D + c * 8 : 0;
+            cp_async16(smem_addr(qt) + chunk_at<DP>(r, c), p.q + e * 2, ok);
+        }
+        cp_async_commit();
+    };
+    if constexpr (kQS) queries();
     for (int i = 0; i < ST - 1; ++i) issue(i);
 
     int stage = 0;
+    bool again = false;
     do {
         const int rows = w.s.n * p.G - w.rt * M;  // rows of the unit (may exceed 16)
         uint32_t qf[kQS ? 1 : KS][4];
         if constexpr (kQS) {
-            __syncwarp();
-            for (int i = lane; i < 16 * (DP / 8); i += 32) {
-                const int r = i / (DP / 8), c = i % (DP / 8);
-                uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                if (r < rows && c * 8 < p.D) {
-                    x = __ldg(reinterpret_cast<const uint4*>(p.q + (out_row(p, w.s, w.h, w.rt * M + r) * p.D + c * 8) * 2));
-                }
-                *reinterpret_cast<uint4*>(qt + chunk_at<DP>(r, c)) = x;
+            if (again) {
+                // behind the stages of this unit that are on their way
+                __syncwarp();
+                queries();
+                cp_async_wait<0>();
+                __syncwarp();
             }
-            __syncwarp();
+            again = true;
         } else {
             // queries straight into the fragments of the first product
             const int g = lane >> 2, q = (lane & 3) * 2;
@@ -478,7 +489,7 @@ __global__ void __launch_bounds__(128, DP <= 128 ? 2 : 1) attn_more_kernel(AttnP
 
     pdl_wait();
     pdl_launch_dependents();
-    if (tid == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, -1);
+    if (tid == 0) clear_desc(p, blockIdx.x);
 
     Walk w;
     if (!walk_begin<M, KT, kMoreUC, 1>(p, w, wsm, 128, 0)) return;
@@ -640,7 +651,7 @@ cudaError_t launch_typed(const AttnP& p, const AttnShape& sh, cudaLaunchConfig_t
         case 192: fn = few ? attn_few_kernel<T, 192> : attn_more_kernel<T, 192>; smem = few ? few_smem<192>() : more_smem<192>(); break;
         default: fn = few ? attn_few_kernel<T, 256> : attn_more_kernel<T, 256>; smem = few ? few_smem<256>() : more_smem<256>(); break;
     }
-    cudaError_t e = cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = allow_smem((const void*)fn, (int)smem);
     if (e != cudaSuccess) return e;
     cfg.blockDim = dim3(128);
     cfg.dynamicSmemBytes = smem;

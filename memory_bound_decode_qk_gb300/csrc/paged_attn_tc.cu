@@ -339,7 +339,7 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
 
     pdl_wait();
     pdl_launch_dependents();
-    if (tid == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, -1);
+    if (tid == 0) clear_desc(p, blockIdx.x);
     Walk w;
     if (!walk_begin<M, KT, C::kUC, 1>(p, w, wsm, C::kThreads, 0)) return;
 
@@ -1023,8 +1023,7 @@ bool cache_map(CUtensorMap* map, const AttnP& p, const char* base, int dt) {
 
 template <typename T, int DP>
 cudaError_t launch_typed(const AttnP& p, const CUtensorMap (&m)[3], int q_boxes, cudaLaunchConfig_t cfg) {
-    cudaError_t e = cudaFuncSetAttribute((const void*)attn_tc_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         Tc<DP>::kSmem);
+    const cudaError_t e = allow_smem((const void*)attn_tc_kernel<T, DP>, Tc<DP>::kSmem);
     if (e != cudaSuccess) return e;
     cfg.blockDim = dim3(Tc<DP>::kThreads);
     cfg.dynamicSmemBytes = Tc<DP>::kSmem;

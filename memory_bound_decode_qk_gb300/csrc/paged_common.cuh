@@ -33,7 +33,8 @@ struct AttnP {
     const int32_t* lens;
     const int32_t* starts;  // nullable: one token per sequence
     float* part;        // [pieces][2][M * D + 2 M] fp32
-    int4* desc;         // [pieces]: unit of slot 1 (b, h, rt) and its last piece, or w < 0
+    int4* desc;         // [pieces][2]: unit of slot 1: (last piece or < 0, key head, row
+                        // tile, -) and (first query row, tokens, -, -) of its sequence
     int num_seqs, max_pages, num_pages, page_size;
     int tokens, hq, hk, G, D;
     FastDiv gdiv, pdiv;  // by G and by page_size
@@ -113,6 +114,12 @@ __device__ __forceinline__ Keys tile_range(const AttnP& p, const Seq& s, int rt,
     return k;
 }
 
+// a / b of non-negative values, which seldom need 64 bits.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if ((((uint64_t)a | (uint64_t)b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+    return a / b;
+}
+
 // Length of sequence b's units of one key head in the line.
 template <int M, int KT, int UC>
 __device__ __forceinline__ int64_t seq_length(const AttnP& p, const Seq& s) {
@@ -162,6 +169,35 @@ struct WalkSmem {
     int b[PP];
 };
 
+// The unit and tile at `rel` behind the start of sequence w.b's part of the line,
+// of which one key head takes per_head.
+template <int M, int KT, int UC>
+__device__ __forceinline__ bool walk_settle(const AttnP& p, Walk& w, int64_t total, int64_t per, int piece,
+                                            int64_t rel, int64_t per_head) {
+    const int64_t start = per * piece;
+    w.piece = piece;
+    w.per = per;
+    w.left = total - start < per ? total - start : per;
+    w.h = (int)quotient(rel, per_head);
+    rel -= w.h * per_head;
+    w.rt = 0;
+    for (;;) {
+        int k0, k1;
+        tile_range<M, KT>(p, w.s, w.rt, k0, k1);
+        const int len = UC + k1 - k0;
+        if (rel < len) break;
+        rel -= len;
+        ++w.rt;
+    }
+    return walk_enter<M, KT, UC>(p, w, start, rel);
+}
+
+// The line's pieces: equal lengths, at least min_per.
+__device__ __forceinline__ int64_t piece_length(const AttnP& p, int64_t total, int pieces) {
+    const int64_t per = quotient(total + pieces - 1, pieces);
+    return per > p.min_per ? per : p.min_per;
+}
+
 // Finds the pieces blockIdx.x + gridDim.x i, i < PP, of this CTA; the calling
 // thread's worker takes the one of i = `mine`.  Every thread of the block calls
 // it; false if the worker's piece is empty.  `threads` is the block size, a
@@ -169,6 +205,35 @@ struct WalkSmem {
 template <int M, int KT, int UC, int PP>
 __device__ bool walk_begin(const AttnP& p, Walk& w, WalkSmem<PP>& sm, int threads, int mine) {
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, nw = threads >> 5;
+    const int pieces = gridDim.x * PP;
+    const int piece = blockIdx.x + gridDim.x * mine;
+    if (p.num_seqs <= 32) {
+        // a lane per sequence: no shared memory, no barrier
+        Seq s{0, 0, 0};
+        int64_t c = 0;
+        if (lane < p.num_seqs) {
+            s = load_seq(p, lane);
+            c = seq_length<M, KT, UC>(p, s);
+        }
+        int64_t inc = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += up;
+        }
+        const int64_t total = __shfl_sync(0xffffffffu, inc, 31) * p.hk;
+        const int64_t per = piece_length(p, total, pieces);
+        const int64_t start = per * piece;
+        if (start >= total) return false;
+        const int64_t lo = (inc - c) * p.hk;
+        const int from = __ffs(__ballot_sync(0xffffffffu, lo <= start && start < inc * p.hk)) - 1;
+        w.b = from;
+        w.s.q0 = __shfl_sync(0xffffffffu, s.q0, from);
+        w.s.n = __shfl_sync(0xffffffffu, s.n, from);
+        w.s.L = __shfl_sync(0xffffffffu, s.L, from);
+        const int64_t rel = start - __shfl_sync(0xffffffffu, lo, from);
+        return walk_settle<M, KT, UC>(p, w, total, per, piece, rel, __shfl_sync(0xffffffffu, c, from));
+    }
     int64_t first = 0, own = 0;
     for (int b = tid; b < p.num_seqs; b += threads) {
         const int64_t c = seq_length<M, KT, UC>(p, load_seq(p, b));
@@ -182,9 +247,7 @@ __device__ bool walk_begin(const AttnP& p, Walk& w, WalkSmem<PP>& sm, int thread
     tot = 0;
     for (int i = 0; i < nw; ++i) tot += sm.warp[i];
     const int64_t total = tot * p.hk;
-    const int pieces = gridDim.x * PP;
-    int64_t per = (total + pieces - 1) / pieces;
-    if (per < p.min_per) per = p.min_per;
+    const int64_t per = piece_length(p, total, pieces);
     const int64_t low = per * blockIdx.x;  // the first of the CTA's pieces
     if (low >= total) return false;
     const int64_t high = per * ((int64_t)blockIdx.x + (int64_t)gridDim.x * (PP - 1));
@@ -226,25 +289,8 @@ __device__ bool walk_begin(const AttnP& p, Walk& w, WalkSmem<PP>& sm, int thread
     __syncthreads();
     w.b = sm.b[mine];
     if (w.b < 0) return false;
-    w.piece = blockIdx.x + gridDim.x * mine;
-    const int64_t start = per * w.piece;
-    w.per = per;
-    w.left = total - start < per ? total - start : per;
-    int64_t rel = sm.rel[mine];
     w.s = load_seq(p, w.b);
-    const int64_t per_head = seq_length<M, KT, UC>(p, w.s);
-    w.h = (int)(rel / per_head);
-    rel -= w.h * per_head;
-    w.rt = 0;
-    for (;;) {
-        int k0, k1;
-        tile_range<M, KT>(p, w.s, w.rt, k0, k1);
-        const int len = UC + k1 - k0;
-        if (rel < len) break;
-        rel -= len;
-        ++w.rt;
-    }
-    return walk_enter<M, KT, UC>(p, w, start, rel);
+    return walk_settle<M, KT, UC>(p, w, total, per, piece, sm.rel[mine], seq_length<M, KT, UC>(p, w.s));
 }
 
 // The next unit; false at the end of the piece.
@@ -279,7 +325,11 @@ __device__ __forceinline__ float* part_of(const AttnP& p, int piece, int slot) {
 // Names the unit of slot 1 and the last piece that holds a part of it (called
 // by one thread).
 __device__ __forceinline__ void write_desc(const AttnP& p, const Walk& w) {
-    p.desc[w.piece] = make_int4(w.b, w.h, w.rt, (int)((w.after - 1) / w.per));
+    p.desc[2 * w.piece] = make_int4((int)quotient(w.after - 1, w.per), w.h, w.rt, 0);
+    p.desc[2 * w.piece + 1] = make_int4(w.s.q0, w.s.n, 0, 0);
+}
+__device__ __forceinline__ void clear_desc(const AttnP& p, int piece) {
+    p.desc[2 * piece] = make_int4(-1, 0, 0, 0);
 }
 
 // Row r (of the sequence's packed rows) -> element offset of its output row.

@@ -198,33 +198,58 @@ __device__ __forceinline__ void load_cache(const QKP& p, int64_t pos, int sub, i
     }
 }
 
-// load_cache for several axes: four pairs at a time, as one vector where they
-// have one axis, else pair by pair (L1 hits: the heads of a token share the
-// rows).
-template <typename T, int LAYOUT>
-__device__ __forceinline__ void load_cache_axes(const QKP& p, const AxisPos& x, int sub, int role,
-                                                CacheRegs<T, LAYOUT>& cr) {
+// Cos and sin of a CTA's tokens t0 .. t0 + n - 1 with several axes, gathered once
+// for all their heads: entry j of a token comes from the cache row of its
+// pair's axis.  A CTA of 256 threads holds 256 / LPH heads of at most 4 LPH
+// pairs, so of at most 256 / LPH + 1 tokens.  (Measured on GB300 at 64 tokens
+// of 48 heads: 4.3 us with every lane gathering its own pairs.)
+template <typename T, int LPH>
+struct AxisRows {
+    static constexpr int kPairs = LPH * vec_elems<T>() / 2;
+    static constexpr int kTokens = 256 / LPH + 1;
+    __align__(16) float c[kTokens * kPairs];
+    __align__(16) float s[kTokens * kPairs];
+    bool in[kTokens];
+};
+
+template <typename T, int LPH>
+__device__ __forceinline__ void gather_axes(const QKP& p, AxisRows<T, LPH>& rows, int64_t t0, int n) {
+    if (p.rot > 0) {
+        for (int i = threadIdx.x; i < n * p.half; i += blockDim.x) {
+            const int k = i / p.half, j = i - k * p.half;
+            const AxisPos x = load_axis_pos(p, t0 + k);
+            if (j == 0) rows.in[k] = x.in;
+            if (x.in) {
+                const int64_t e = axis_row(p, x, j);
+                rows.c[k * p.half + j] = __ldg(p.cs + e);
+                rows.s[k * p.half + j] = __ldg(p.sn + e);
+            }
+        }
+    }
+    __syncthreads();
+}
+
+// load_cache from the gathered rows of token k.
+template <typename T, int LPH, int LAYOUT>
+__device__ __forceinline__ void load_axes(const QKP& p, const AxisRows<T, LPH>& rows, int k, int sub, int role,
+                                          CacheRegs<T, LAYOUT>& cr) {
     constexpr int N = vec_elems<T>();
     constexpr int n = CacheRegs<T, LAYOUT>::kCount;
-    constexpr int G = n < 4 ? n : 4;
     const int e0 = sub * N;
-    const int j0 = LAYOUT == kInterleaved ? e0 / 2 : (role == 1 ? e0 : e0 - p.half);
+    const int j0 = k * p.half + (LAYOUT == kInterleaved ? e0 / 2 : (role == 1 ? e0 : e0 - p.half));
+    if constexpr (n % 4 == 0) {
 #pragma unroll
-    for (int g = 0; g < n; g += G) {
-        const int j = j0 + g;
-        if (G == 4 && !p.cycled && pair_axis(p, j) == pair_axis(p, j + 3)) {
-            const int64_t e = axis_row(p, x, j);
-            const float4 c4 = __ldg(reinterpret_cast<const float4*>(p.cs + e));
-            const float4 s4 = __ldg(reinterpret_cast<const float4*>(p.sn + e));
-            cr.c[g] = c4.x; cr.c[g + 1] = c4.y; cr.c[g + 2 < n ? g + 2 : 0] = c4.z; cr.c[g + 3 < n ? g + 3 : 0] = c4.w;
-            cr.s[g] = s4.x; cr.s[g + 1] = s4.y; cr.s[g + 2 < n ? g + 2 : 0] = s4.z; cr.s[g + 3 < n ? g + 3 : 0] = s4.w;
-        } else {
+        for (int g = 0; g < n; g += 4) {
+            const float4 c4 = *reinterpret_cast<const float4*>(rows.c + j0 + g);
+            const float4 s4 = *reinterpret_cast<const float4*>(rows.s + j0 + g);
+            cr.c[g] = c4.x; cr.c[g + 1] = c4.y; cr.c[g + 2] = c4.z; cr.c[g + 3] = c4.w;
+            cr.s[g] = s4.x; cr.s[g + 1] = s4.y; cr.s[g + 2] = s4.z; cr.s[g + 3] = s4.w;
+        }
+    } else {
 #pragma unroll
-            for (int k = 0; k < G; ++k) {
-                const int64_t e = axis_row(p, x, j + k);
-                cr.c[g + k] = __ldg(p.cs + e);
-                cr.s[g + k] = __ldg(p.sn + e);
-            }
+        for (int g = 0; g < n; ++g) {
+            cr.c[g] = rows.c[j0 + g];
+            cr.s[g] = rows.s[j0 + g];
         }
     }
 }

@@ -43,11 +43,12 @@ namespace {
 // address hint for the row, to save that second round trip, was 0.03 to
 // 0.26 us slower per launch from T = 1 to 128, and so was a grid-stride loop
 // over the heads.)
-// AXES: several positions per token; each lane picks its pairs' cache rows.
+// AXES: several positions per token; the CTA gathers its tokens' angles first.
 template <typename T, bool FP8, int LPH, int LAYOUT, bool AXES = false>
 __global__ void __launch_bounds__(256) qk_vec_kernel(QKP p) {
     constexpr int N = vec_elems<T>();
     constexpr int HPW = 32 / LPH;
+    __shared__ std::conditional_t<AXES, AxisRows<T, LPH>, int> rows;
     const int lane = threadIdx.x & 31;
     const int sub = lane & (LPH - 1);
     // < 2^31 + 8 HPW: units are at most 2^31 - 1 (validated)
@@ -65,24 +66,30 @@ __global__ void __launch_bounds__(256) qk_vec_kernel(QKP p) {
     const int lane_role = p.rot > 0 ? rotary_role<T, LAYOUT>(p, sub) : 0;
     uint4 raw = make_uint4(0u, 0u, 0u, 0u);
     int64_t pos = -1;
-    AxisPos ap;
-    ap.in = false;
     if (active) {
         raw = __ldcs(reinterpret_cast<const uint4*>(un.src) + sub);
-        if constexpr (AXES) {
-            if (p.rot > 0) ap = load_axis_pos(p, un.t);
-        } else {
+        if constexpr (!AXES) {
             if (p.rot > 0) pos = __ldg(p.pos + un.t);
         }
     }
     float w[N];
     weights_plus_delta<T>(p, un.w, sub, w);
-    const bool rot = AXES ? ap.in : active && pos >= 0 && pos < p.cache_len;
+    bool rot = active && pos >= 0 && pos < p.cache_len;
+    int mine = 0;
+    if constexpr (AXES) {
+        // the tokens of this CTA's heads
+        const uint32_t per_cta = (blockDim.x >> 5) * HPW;
+        const uint32_t u0 = blockIdx.x * per_cta, u1 = min(u0 + per_cta, p.units);
+        const int t0 = (int)fast_div(u0, p.heads), t1 = (int)fast_div(u1 - 1, p.heads);
+        gather_axes<T, LPH>(p, rows, t0, t1 - t0 + 1);
+        mine = (int)un.t - t0;
+        rot = active && p.rot > 0 && rows.in[mine];
+    }
     const int role = rot ? lane_role : 0;
     CacheRegs<T, LAYOUT> cr;
     if (role != 0) {
         if constexpr (AXES) {
-            load_cache_axes<T, LAYOUT>(p, ap, sub, role, cr);
+            load_axes<T, LPH, LAYOUT>(p, rows, mine, sub, role, cr);
         } else {
             load_cache<T, LAYOUT>(p, pos, sub, role, cr);
         }

@@ -30,6 +30,7 @@ template <typename T, int LPH, int LAYOUT, bool AXES = false>
 __global__ void __launch_bounds__(256) qkv_vec_kernel(QKVP a) {
     constexpr int N = vec_elems<T>();
     constexpr int HPW = 32 / LPH;
+    __shared__ std::conditional_t<AXES, AxisRows<T, LPH>, int> rows;
     const QKP& p = a.p;
     const int lane = threadIdx.x & 31;
     const int sub = lane & (LPH - 1);
@@ -61,13 +62,9 @@ __global__ void __launch_bounds__(256) qkv_vec_kernel(QKVP a) {
     const int lane_role = p.rot > 0 ? rotary_role<T, LAYOUT>(p, sub) : 0;
     uint4 raw = make_uint4(0u, 0u, 0u, 0u);
     int64_t pos = -1, slot = -1;
-    AxisPos ap;
-    ap.in = false;
     if (active) {
         raw = __ldcs(reinterpret_cast<const uint4*>(src) + sub);
-        if constexpr (AXES) {
-            if (p.rot > 0 && !isv) ap = load_axis_pos(p, t);
-        } else {
+        if constexpr (!AXES) {
             if (p.rot > 0 && !isv) pos = __ldg(p.pos + t);
         }
         if (!isq && a.slots != nullptr) slot = __ldg(a.slots + t);
@@ -80,12 +77,21 @@ __global__ void __launch_bounds__(256) qkv_vec_kernel(QKVP a) {
     }
     float w[N];
     weights_plus_delta<T>(p, isq ? p.wq : p.wk, sub, w);
-    const bool rot = AXES ? ap.in : active && !isv && pos >= 0 && pos < p.cache_len;
+    bool rot = active && !isv && pos >= 0 && pos < p.cache_len;
+    int mine = 0;
+    if constexpr (AXES) {
+        const uint32_t per_cta = (blockDim.x >> 5) * HPW;
+        const uint32_t u0 = blockIdx.x * per_cta, u1 = min(u0 + per_cta, p.units);
+        const int t0 = (int)fast_div(u0, a.per_token), t1 = (int)fast_div(u1 - 1, a.per_token);
+        gather_axes<T, LPH>(p, rows, t0, t1 - t0 + 1);
+        mine = (int)t - t0;
+        rot = active && !isv && p.rot > 0 && rows.in[mine];
+    }
     const int role = rot ? lane_role : 0;
     CacheRegs<T, LAYOUT> cr;
     if (role != 0) {
         if constexpr (AXES) {
-            load_cache_axes<T, LAYOUT>(p, ap, sub, role, cr);
+            load_axes<T, LPH, LAYOUT>(p, rows, mine, sub, role, cr);
         } else {
             load_cache<T, LAYOUT>(p, pos, sub, role, cr);
         }

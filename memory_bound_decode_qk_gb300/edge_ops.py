@@ -367,8 +367,24 @@ def _on(device, stream):
     return torch.cuda.stream(stream)
 
 
-def _plain(device, stream):
-    return stream is None and device.index == torch.cuda.current_device()
+# The current device without torch's lazy-initialization check (a CUDA tensor
+# exists wherever it is asked for); the public route where torch lacks it.
+_CURRENT_DEVICE = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _here(index, stream):
+    """Whether a call with tensors on device `index` can launch as it stands."""
+    return stream is None and index == _CURRENT_DEVICE()
+
+
+def _fits(index, dtype, *tensors):
+    """Whether every tensor given has this dtype, is on device `index` and is
+    contiguous: the quick form of _want, which names what is wrong."""
+    for t in tensors:
+        if t is not None and not (t.dtype is dtype and t.get_device() == index and
+                                  t.is_contiguous()):
+            return False
+    return True
 
 
 def _want(t, name, dtype, shape, device):
@@ -409,10 +425,48 @@ def paged_attention(q, k_cache, v_cache, block_table, lens, *, page_size, q_star
     each row.  workspace: from paged_attention_workspace; one is taken from
     torch for the call when None.  Returns out ([T, Hq, D])."""
     T, Hq, D = q.shape
+    S, Hk, Dk = k_cache.shape
+    B, pages = block_table.shape
+    at = q.get_device()
+    dt = _dt(q)
+    if not (at >= 0 and Dk == D and v_cache.shape == k_cache.shape and lens.shape == (B,) and
+            _fits(at, q.dtype, q, k_cache, v_cache) and
+            _fits(at, torch.int32, block_table, lens, q_starts) and
+            (q_starts is None or q_starts.shape == (B + 1,)) and
+            (out is None or (out.shape == q.shape and
+                             _fits(at, torch.uint8 if fp8 else q.dtype, out))) and
+            (lse is None or (lse.shape == (T, Hq) and _fits(at, torch.float32, lse))) and
+            (workspace is None or _fits(at, torch.uint8, workspace))):
+        _explain_attention(q, k_cache, v_cache, block_table, lens, q_starts, out, lse, fp8,
+                           workspace)
+    if not _here(at, stream):
+        with _on(q.device, stream):
+            return paged_attention(q, k_cache, v_cache, block_table, lens, page_size=page_size,
+                                   q_starts=q_starts, scale=scale, causal=causal, window=window,
+                                   out=out, lse=lse, fp8=fp8, inv_scale=inv_scale,
+                                   workspace=workspace)
+    if out is None:
+        out = _alloc(q, q.shape, fp8)
+    if workspace is None:
+        workspace = paged_attention_workspace(q, k_cache)
+    if scale is None:
+        scale = D ** -0.5
+    st = lib().edge_paged_attention(
+        out.data_ptr(), FP8_E4M3 if fp8 else dt, _ptr(lse), q.data_ptr(), k_cache.data_ptr(),
+        v_cache.data_ptr(), dt, T, Hq, Hk, D, S, page_size, block_table.data_ptr(), B, pages,
+        lens.data_ptr(), _ptr(q_starts), scale, 1 if causal else 0, window, inv_scale,
+        workspace.data_ptr(), workspace.numel(), _stream(None))
+    if st:
+        raise EdgeError(st, "edge_paged_attention")
+    return out
+
+
+def _explain_attention(q, k_cache, v_cache, block_table, lens, q_starts, out, lse, fp8, workspace):
+    """Raises for the first tensor of a paged_attention call that does not fit."""
+    T, Hq, D = q.shape
     S, Hk, _ = k_cache.shape
     B, pages = block_table.shape
     dev = q.device
-    dt = _dt(q)
     if dev.type != "cuda":
         raise ValueError(f"q must be a CUDA tensor, not on {dev}")
     _want(q, "q", q.dtype, (T, Hq, D), dev)
@@ -428,24 +482,6 @@ def paged_attention(q, k_cache, v_cache, block_table, lens, *, page_size, q_star
         _want(lse, "lse", torch.float32, (T, Hq), dev)
     if workspace is not None:
         _want(workspace, "workspace", torch.uint8, (None,), dev)
-    if not _plain(dev, stream):
-        with _on(dev, stream):
-            return paged_attention(q, k_cache, v_cache, block_table, lens, page_size=page_size,
-                                   q_starts=q_starts, scale=scale, causal=causal, window=window,
-                                   out=out, lse=lse, fp8=fp8, inv_scale=inv_scale,
-                                   workspace=workspace)
-    if out is None:
-        out = _alloc(q, q.shape, fp8)
-    if workspace is None:
-        workspace = paged_attention_workspace(q, k_cache)
-    if scale is None:
-        scale = D ** -0.5
-    _check(lib().edge_paged_attention(
-        out.data_ptr(), _out_dt(fp8, dt), _ptr(lse), q.data_ptr(), k_cache.data_ptr(),
-        v_cache.data_ptr(), dt, T, Hq, Hk, D, S, page_size, block_table.data_ptr(), B, pages,
-        lens.data_ptr(), _ptr(q_starts), scale, 1 if causal else 0, window, inv_scale,
-        workspace.data_ptr(), workspace.numel(), _stream(None)), "edge_paged_attention")
-    return out
 
 
 class PageCaches:
@@ -471,6 +507,8 @@ class PageCaches:
         slot = first.numel() // first.shape[0] if first.shape[0] else 1
         self.page_bytes = max(1, slot * first.element_size()) * page_size
         self.pointers = (ctypes.c_void_p * len(caches))(*[t.data_ptr() for t in caches])
+        self.index = first.get_device()
+        self.count = len(caches)
 
     def __len__(self):
         return len(self.tensors)
@@ -479,15 +517,18 @@ class PageCaches:
 def pages_copy(caches, src, dst, *, stream=None):
     """Copies page src[i] to page dst[i] in every cache of `caches` (PageCaches).
     src, dst: [n] int32.  See edge_pages_copy for pairs that meet."""
-    dev = caches.device
-    _want(src, "src", torch.int32, (None,), dev)
-    _want(dst, "dst", torch.int32, tuple(src.shape), dev)
-    if not _plain(dev, stream):
-        with _on(dev, stream):
+    n = src.shape[0]
+    if not (src.dim() == 1 and dst.shape == src.shape and
+            _fits(caches.index, torch.int32, src, dst)):
+        _want(src, "src", torch.int32, (None,), caches.device)
+        _want(dst, "dst", torch.int32, (n,), caches.device)
+    if not _here(caches.index, stream):
+        with _on(caches.device, stream):
             return pages_copy(caches, src, dst)
-    _check(lib().edge_pages_copy(caches.pointers, len(caches), caches.page_bytes, caches.num_pages,
-                                 src.data_ptr(), dst.data_ptr(), src.shape[0], _stream(None)),
-           "edge_pages_copy")
+    st = lib().edge_pages_copy(caches.pointers, caches.count, caches.page_bytes, caches.num_pages,
+                               src.data_ptr(), dst.data_ptr(), n, _stream(None))
+    if st:
+        raise EdgeError(st, "edge_pages_copy")
 
 
 def _want_rows(block_table, lens, refs, pages, dev):
@@ -501,17 +542,20 @@ def pages_free(block_table, lens, refs, seqs, *, stream=None):
     """Gives back the pages of sequences `seqs` ([n] int32): their entries of
     block_table ([B, P] int32) become -1, their lens ([B] int32) 0, and the
     counts refs ([pages] int32) of their pages go down."""
-    dev = refs.device
-    _want_rows(block_table, lens, refs, None, dev)
-    _want(seqs, "seqs", torch.int32, (None,), dev)
-    if dev.type != "cuda":
-        raise ValueError(f"refs must be a CUDA tensor, not on {dev}")
-    if not _plain(dev, stream):
-        with _on(dev, stream):
+    at = refs.get_device()
+    B, width = block_table.shape
+    if not (at >= 0 and refs.dim() == 1 and seqs.dim() == 1 and lens.shape == (B,) and
+            _fits(at, torch.int32, block_table, lens, refs, seqs)):
+        _want_rows(block_table, lens, refs, None, refs.device)
+        _want(seqs, "seqs", torch.int32, (None,), refs.device)
+        raise ValueError(f"refs must be a CUDA tensor, not on {refs.device}")
+    if not _here(at, stream):
+        with _on(refs.device, stream):
             return pages_free(block_table, lens, refs, seqs)
-    _check(lib().edge_pages_free(block_table.data_ptr(), *block_table.shape, lens.data_ptr(),
-                                 refs.data_ptr(), refs.shape[0], seqs.data_ptr(), seqs.shape[0],
-                                 _stream(None)), "edge_pages_free")
+    st = lib().edge_pages_free(block_table.data_ptr(), B, width, lens.data_ptr(), refs.data_ptr(),
+                               refs.shape[0], seqs.data_ptr(), seqs.shape[0], _stream(None))
+    if st:
+        raise EdgeError(st, "edge_pages_free")
 
 
 def pages_fork(caches, block_table, lens, refs, parents, children, *, status=None, pairs=None,
@@ -521,28 +565,35 @@ def pages_fork(caches, block_table, lens, refs, parents, children, *, status=Non
     page of `caches` (PageCaches).  Returns status ([n] int32: 0 forked, 1 no
     free page, 2 refused); pairs ([n, 2] int32), where given, receives the pages
     copied."""
-    dev = caches.device
-    _want_rows(block_table, lens, refs, caches.num_pages, dev)
-    _want(parents, "parents", torch.int32, (None,), dev)
     n = parents.shape[0]
-    _want(children, "children", torch.int32, (n,), dev)
-    if status is not None:
-        _want(status, "status", torch.int32, (n,), dev)
-    if pairs is not None:
-        _want(pairs, "pairs", torch.int32, (n, 2), dev)
-    if not _plain(dev, stream):
-        with _on(dev, stream):
+    B, width = block_table.shape
+    if not (parents.dim() == 1 and children.shape == parents.shape and lens.shape == (B,) and
+            refs.shape == (caches.num_pages,) and
+            (status is None or status.shape == (n,)) and (pairs is None or pairs.shape == (n, 2)) and
+            _fits(caches.index, torch.int32, block_table, lens, refs, parents, children, status,
+                  pairs)):
+        dev = caches.device
+        _want_rows(block_table, lens, refs, caches.num_pages, dev)
+        _want(parents, "parents", torch.int32, (None,), dev)
+        _want(children, "children", torch.int32, (n,), dev)
+        if status is not None:
+            _want(status, "status", torch.int32, (n,), dev)
+        if pairs is not None:
+            _want(pairs, "pairs", torch.int32, (n, 2), dev)
+    if not _here(caches.index, stream):
+        with _on(caches.device, stream):
             return pages_fork(caches, block_table, lens, refs, parents, children, status=status,
                               pairs=pairs)
     if status is None:
-        status = torch.empty(n, dtype=torch.int32, device=dev)
+        status = torch.empty_like(parents)
     if pairs is None:
-        pairs = torch.empty((n, 2), dtype=torch.int32, device=dev)
-    _check(lib().edge_pages_fork(caches.pointers, len(caches), caches.page_bytes, caches.num_pages,
-                                 caches.page_size, block_table.data_ptr(), *block_table.shape,
-                                 lens.data_ptr(), refs.data_ptr(), parents.data_ptr(),
-                                 children.data_ptr(), n, status.data_ptr(), pairs.data_ptr(),
-                                 _stream(None)), "edge_pages_fork")
+        pairs = torch.empty((n, 2), dtype=torch.int32, device=caches.device)
+    st = lib().edge_pages_fork(caches.pointers, caches.count, caches.page_bytes, caches.num_pages,
+                               caches.page_size, block_table.data_ptr(), B, width, lens.data_ptr(),
+                               refs.data_ptr(), parents.data_ptr(), children.data_ptr(), n,
+                               status.data_ptr(), pairs.data_ptr(), _stream(None))
+    if st:
+        raise EdgeError(st, "edge_pages_fork")
     return status
 
 
@@ -566,7 +617,7 @@ def pages_compact(caches, block_table, refs, *, table_out=None, refs_out=None, w
     _want(refs_out, "refs_out", torch.int32, tuple(refs.shape), dev)
     if workspace is not None:
         _want(workspace, "workspace", torch.uint8, (None,), dev)
-    if not _plain(dev, stream):
+    if not _here(caches.index, stream):
         with _on(dev, stream):
             return pages_compact(caches, block_table, refs, table_out=table_out, refs_out=refs_out,
                                  workspace=workspace)

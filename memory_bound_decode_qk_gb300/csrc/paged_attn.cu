@@ -20,7 +20,8 @@ namespace {
 
 constexpr int kAnyM = 16;       // query rows of a unit
 constexpr int kAnyKT = 32;      // keys of a tile: one per lane
-constexpr int kAnyThreads = 128;
+constexpr int kAnyThreads = 256;
+constexpr int kAnyRows = 2;     // rows of a warp
 constexpr int kAnyUC = 1;
 
 // floats per staged row: a multiple of 4 whose quarter is odd, so that 8
@@ -29,86 +30,96 @@ __host__ __device__ constexpr int any_stride(int D) {
     return (((D + 3) / 4) | 1) * 4;
 }
 
-__host__ __device__ constexpr int any_smem_floats(int D) {
-    return (kAnyM + 2 * kAnyKT) * any_stride(D) + kAnyM * kAnyKT;
+// fp32 rows of whole 16-byte vectors are copied asynchronously into two stages.
+template <typename T, bool VEC>
+constexpr __host__ __device__ int any_stages() {
+    return std::is_same<T, float>::value && VEC ? 2 : 1;
+}
+__host__ __device__ constexpr int any_smem_floats(int D, int stages) {
+    return (kAnyM + 2 * stages * kAnyKT) * any_stride(D) + kAnyM * kAnyKT;
 }
 
-// Any type, head size up to 32 NV and alignment.  Four warps; a tile's keys
-// and values are staged as fp32 in shared memory.  Scores: lane = key, a warp
-// does its four rows, so a key's 16 bytes serve four rows.  Values: lane =
-// channel, four rows per load.  A key of weight zero (masked, or underflowed)
-// is skipped, so what the cache holds there does not matter.
-template <typename T, int NV, bool VEC>
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(ok ? 16 : 0)
+                 : "memory");
+}
+
+// Any type, head size up to 128 NC and alignment.  Eight warps of two rows each;
+// a tile's keys and values are staged as fp32 in shared memory.  Scores: lane =
+// key, so a key's 16 bytes serve two rows.  Values: four channels per lane, two
+// rows per load.  A key of weight zero (masked, or underflowed) is skipped, so
+// what the cache holds there does not matter.  Bound by the latency of a tile's
+// steps at small sizes and by shared-memory reads at large ones (per key and
+// channel quarter of two rows: one 16-byte read for 8 products).
+template <typename T, int NC, bool VEC>
 __global__ void __launch_bounds__(kAnyThreads) attn_any_kernel(AttnP p) {
-    constexpr int M = kAnyM, KT = kAnyKT;
+    constexpr int M = kAnyM, KT = kAnyKT, R = kAnyRows, ST = any_stages<T, VEC>();
     extern __shared__ __align__(16) float smem[];
     __shared__ WalkSmem<1> wsm;
-    __shared__ int64_t slot_of[KT];
+    // of three tiles: one is written while the slowest warp is a tile behind
+    __shared__ int64_t slot_of[3][KT];
     const int D = p.D, ds = any_stride(D);
     float* qs = smem;
-    float* ks = qs + M * ds;
-    float* vs = ks + KT * ds;
-    float* ps = vs + KT * ds;
+    float* ring = qs + M * ds;  // stages of [keys | values]
+    float* ps = ring + 2 * ST * KT * ds;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
 
     pdl_wait();
     pdl_launch_dependents();
     if (tid == 0) clear_desc(p, blockIdx.x);
     // the padding channels stay zero
-    for (int i = tid; i < (M + 2 * KT) * ds; i += kAnyThreads) smem[i] = 0.0f;
+    for (int i = tid; i < (M + 2 * ST * KT) * ds; i += kAnyThreads) smem[i] = 0.0f;
 
     Walk w;
     if (!walk_begin<M, KT, kAnyUC, 1>(p, w, wsm, kAnyThreads, 0)) return;
     do {
         const int rows = w.s.n * p.G;
         const int r0 = w.rt * M;
+        const int t0 = w.k0 + w.off;
         __syncthreads();
-        for (int i = tid; i < M * D; i += kAnyThreads) {
-            const int r = i / D, d = i - r * D;
-            float x = 0.0f;
-            if (r0 + r < rows) {
-                x = to_f(reinterpret_cast<const T*>(p.q)[out_row(p, w.s, w.h, r0 + r) * D + d]);
+        // slots of tile t's keys, by the first warp
+        auto look = [&](int t) {
+            if (tid < KT) {
+                const int j = (t0 + t) * KT + tid;
+                slot_of[t % 3][tid] = j < w.s.L ? key_slot(p, w.b, j) : -1;
             }
-            qs[r * ds + d] = x;
-        }
-        float acc[4][NV], m[4], l[4];
-        int at[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            m[r] = -INFINITY;
-            l[r] = 0.0f;
-            at[r] = w.s.L - w.s.n + (int)fast_div((uint32_t)(r0 + wid * 4 + r), p.gdiv);
-#pragma unroll
-            for (int i = 0; i < NV; ++i) acc[r][i] = 0.0f;
-        }
-        for (int kt = w.k0 + w.off; kt < w.k0 + w.off + w.cnt; ++kt) {
-            const int j0 = kt * KT;
-            __syncthreads();  // the tile before is consumed
-            if (tid < KT) slot_of[tid] = j0 + tid < w.s.L ? key_slot(p, w.b, j0 + tid) : -1;
-            __syncthreads();
+        };
+        // tile t into its stage (asynchronously with two stages)
+        auto load = [&](int t) {
+            float* ks = ring + (ST == 2 ? (t & 1) * 2 * KT * ds : 0);
+            float* vs = ks + KT * ds;
+            const int64_t* slots = slot_of[t % 3];
             if constexpr (VEC) {
                 constexpr int N = vec_elems<T>();
                 const int nv = D / N;
-                for (int i = tid; i < 2 * KT * nv; i += kAnyThreads) {
-                    const bool isv = i >= KT * nv;
-                    const int e = isv ? i - KT * nv : i;
-                    const int j = e / nv, c = e - j * nv;
-                    const int64_t slot = slot_of[j];
-                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                    if (slot >= 0) {
-                        x = __ldg(reinterpret_cast<const uint4*>(isv ? p.v : p.k) +
-                                  (slot * p.hk + w.h) * nv + c);
-                    }
-                    float f[N];
-                    unpack_vec<T, N>(x, f);
-                    float* dst = (isv ? vs : ks) + j * ds + c * N;
+                for (int i = tid; i < KT * nv; i += kAnyThreads) {
+                    const int j = i / nv, c = i - j * nv;
+                    const int64_t slot = slots[j];
+                    const int64_t e = slot >= 0 ? (slot * p.hk + w.h) * nv + c : 0;
+                    if constexpr (ST == 2) {
+                        cp_async16(ks + j * ds + c * N, reinterpret_cast<const uint4*>(p.k) + e, slot >= 0);
+                        cp_async16(vs + j * ds + c * N, reinterpret_cast<const uint4*>(p.v) + e, slot >= 0);
+                    } else {
+                        uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
+                        if (slot >= 0) {
+                            x = __ldg(reinterpret_cast<const uint4*>(p.k) + e);
+                            y = __ldg(reinterpret_cast<const uint4*>(p.v) + e);
+                        }
+                        float f[N], g[N];
+                        unpack_vec<T, N>(x, f);
+                        unpack_vec<T, N>(y, g);
 #pragma unroll
-                    for (int t = 0; t < N; ++t) dst[t] = f[t];
+                        for (int z = 0; z < N; ++z) {
+                            ks[j * ds + c * N + z] = f[z];
+                            vs[j * ds + c * N + z] = g[z];
+                        }
+                    }
                 }
             } else {
                 for (int i = tid; i < KT * D; i += kAnyThreads) {
                     const int j = i / D, d = i - j * D;
-                    const int64_t slot = slot_of[j];
+                    const int64_t slot = slots[j];
                     float a = 0.0f, b = 0.0f;
                     if (slot >= 0) {
                         const int64_t e = (slot * p.hk + w.h) * D + d;
@@ -119,24 +130,73 @@ __global__ void __launch_bounds__(kAnyThreads) attn_any_kernel(AttnP p) {
                     vs[j * ds + d] = b;
                 }
             }
+            if constexpr (ST == 2) asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        look(0);
+        for (int i = tid; i < M * D; i += kAnyThreads) {
+            const int r = i / D, d = i - r * D;
+            float x = 0.0f;
+            if (r0 + r < rows) {
+                x = to_f(reinterpret_cast<const T*>(p.q)[out_row(p, w.s, w.h, r0 + r) * D + d]);
+            }
+            qs[r * ds + d] = x;
+        }
+        float4 acc[R][NC];
+        float m[R], l[R];
+        int at[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            m[r] = -INFINITY;
+            l[r] = 0.0f;
+            at[r] = w.s.L - w.s.n + (int)fast_div((uint32_t)(r0 + wid * R + r), p.gdiv);
+#pragma unroll
+            for (int i = 0; i < NC; ++i) acc[r][i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+        __syncthreads();
+        if constexpr (ST == 2) load(0);
+        for (int t = 0; t < w.cnt; ++t) {
+            const int j0 = (t0 + t) * KT;
+            if constexpr (ST == 2) {
+                if (t + 1 < w.cnt) look(t + 1);
+                __syncthreads();  // the slots of t + 1; the tile before is consumed
+                if (t + 1 < w.cnt) {
+                    load(t + 1);
+                    asm volatile("cp.async.wait_group 1;" ::: "memory");
+                } else {
+                    asm volatile("cp.async.wait_group 0;" ::: "memory");
+                }
+            } else {
+                if (t > 0) {
+                    __syncthreads();  // the tile before is consumed
+                    look(t);
+                    __syncthreads();
+                }
+                load(t);
+            }
             __syncthreads();
-            float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            const float* ks = ring + (ST == 2 ? (t & 1) * 2 * KT * ds : 0);
+            const float* vs = ks + KT * ds;
+            const bool in = slot_of[t % 3][lane] >= 0;
+            // two sums per row, of even and odd quarters
+            float s[R][2] = {};
             const float4* kr = reinterpret_cast<const float4*>(ks + lane * ds);
-            for (int c = 0; c < (D + 3) / 4; ++c) {
+            const int nq = (D + 3) / 4;
+#pragma unroll 4
+            for (int c = 0; c < nq; ++c) {
                 const float4 kk = kr[c];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float4 qq = reinterpret_cast<const float4*>(qs + (wid * 4 + r) * ds)[c];
-                    s[r] = fmaf(qq.x, kk.x, s[r]);
-                    s[r] = fmaf(qq.y, kk.y, s[r]);
-                    s[r] = fmaf(qq.z, kk.z, s[r]);
-                    s[r] = fmaf(qq.w, kk.w, s[r]);
+                for (int r = 0; r < R; ++r) {
+                    const float4 qq = reinterpret_cast<const float4*>(qs + (wid * R + r) * ds)[c];
+                    float& x = s[r][c & 1];
+                    x = fmaf(qq.x, kk.x, x);
+                    x = fmaf(qq.y, kk.y, x);
+                    x = fmaf(qq.z, kk.z, x);
+                    x = fmaf(qq.w, kk.w, x);
                 }
             }
-            const bool in = slot_of[lane] >= 0;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float x = in && sees(p, at[r], j0 + lane) ? s[r] * p.scale_log2 : -INFINITY;
+            for (int r = 0; r < R; ++r) {
+                const float x = in && sees(p, at[r], j0 + lane) ? (s[r][0] + s[r][1]) * p.scale_log2 : -INFINITY;
                 const float top = fmaxf(m[r], group_max<32>(x));
                 const float ref = top == -INFINITY ? 0.0f : top;
                 const float keep = ex2(m[r] - ref);
@@ -144,20 +204,40 @@ __global__ void __launch_bounds__(kAnyThreads) attn_any_kernel(AttnP p) {
                 m[r] = top;
                 l[r] = l[r] * keep + group_sum<32>(e);
 #pragma unroll
-                for (int i = 0; i < NV; ++i) acc[r][i] *= keep;
-                ps[(wid * 4 + r) * KT + lane] = e;
+                for (int i = 0; i < NC; ++i) {
+                    acc[r][i].x *= keep;
+                    acc[r][i].y *= keep;
+                    acc[r][i].z *= keep;
+                    acc[r][i].w *= keep;
+                }
+                ps[(wid * R + r) * KT + lane] = e;
             }
             __syncwarp();
-            for (int j = 0; j < KT; ++j) {
-                float vv[NV];
+#pragma unroll 2
+            for (int j = 0; j < KT; j += 4) {
+                float4 e[R];
 #pragma unroll
-                for (int i = 0; i < NV; ++i) vv[i] = lane + 32 * i < D ? vs[j * ds + lane + 32 * i] : 0.0f;
+                for (int r = 0; r < R; ++r) e[r] = *reinterpret_cast<const float4*>(ps + (wid * R + r) * KT + j);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float e = ps[(wid * 4 + r) * KT + j];
-                    if (e != 0.0f) {
+                for (int z = 0; z < 4; ++z) {
+                    float4 vv[NC];
 #pragma unroll
-                        for (int i = 0; i < NV; ++i) acc[r][i] = fmaf(e, vv[i], acc[r][i]);
+                    for (int i = 0; i < NC; ++i) {
+                        const int d = 4 * lane + 128 * i;
+                        vv[i] = d < D ? *reinterpret_cast<const float4*>(vs + (j + z) * ds + d) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    }
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        const float x = z == 0 ? e[r].x : z == 1 ? e[r].y : z == 2 ? e[r].z : e[r].w;
+                        if (x != 0.0f) {
+#pragma unroll
+                            for (int i = 0; i < NC; ++i) {
+                                acc[r][i].x = fmaf(x, vv[i].x, acc[r][i].x);
+                                acc[r][i].y = fmaf(x, vv[i].y, acc[r][i].y);
+                                acc[r][i].z = fmaf(x, vv[i].z, acc[r][i].z);
+                                acc[r][i].w = fmaf(x, vv[i].w, acc[r][i].w);
+                            }
+                        }
                     }
                 }
             }
@@ -165,26 +245,32 @@ __global__ void __launch_bounds__(kAnyThreads) attn_any_kernel(AttnP p) {
         const int slot = walk_slot(w);
         float* part = slot < 0 ? nullptr : part_of<M>(p, w.piece, slot);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = wid * 4 + r;
+        for (int r = 0; r < R; ++r) {
+            const int row = wid * R + r;
             if (r0 + row >= rows) continue;
-            if (part != nullptr) {
+            const int64_t orow = out_row(p, w.s, w.h, r0 + row);
+            const float inv = part != nullptr ? 1.0f : l[r] == 0.0f ? 0.0f : 1.0f / l[r];
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    if (lane + 32 * i < D) part[row * D + lane + 32 * i] = acc[r][i];
+            for (int i = 0; i < NC; ++i) {
+                const float y[4] = {acc[r][i].x, acc[r][i].y, acc[r][i].z, acc[r][i].w};
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    const int d = 4 * lane + 128 * i + z;
+                    if (d >= D) continue;
+                    if (part != nullptr) {
+                        part[row * D + d] = y[z];
+                    } else {
+                        store_one<T>(p, orow * D + d, y[z] * inv);
+                    }
                 }
-                if (lane == 0) {
+            }
+            if (lane == 0) {
+                if (part != nullptr) {
                     part[M * D + row] = m[r];
                     part[M * D + M + row] = l[r];
+                } else if (p.lse != nullptr) {
+                    p.lse[orow] = row_lse(m[r], l[r]);
                 }
-            } else {
-                const int64_t orow = out_row(p, w.s, w.h, r0 + row);
-                const float inv = l[r] == 0.0f ? 0.0f : 1.0f / l[r];
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    if (lane + 32 * i < D) store_one<T>(p, orow * D + lane + 32 * i, acc[r][i] * inv);
-                }
-                if (lane == 0 && p.lse != nullptr) p.lse[orow] = row_lse(m[r], l[r]);
             }
         }
         if (slot == 1 && tid == 0) write_desc(p, w);
@@ -280,11 +366,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnP p) {
 template <typename T>
 cudaError_t launch_any(const AttnP& p, bool vec, cudaLaunchConfig_t cfg) {
     cfg.blockDim = dim3(kAnyThreads);
-    cfg.dynamicSmemBytes = (size_t)any_smem_floats(p.D) * 4;
+    cfg.dynamicSmemBytes = (size_t)any_smem_floats(p.D, vec ? any_stages<T, true>() : 1) * 4;
     void (*fn)(AttnP);
-    if (p.D <= 64) fn = vec ? attn_any_kernel<T, 2, true> : attn_any_kernel<T, 2, false>;
-    else if (p.D <= 128) fn = vec ? attn_any_kernel<T, 4, true> : attn_any_kernel<T, 4, false>;
-    else fn = vec ? attn_any_kernel<T, 8, true> : attn_any_kernel<T, 8, false>;
+    if (p.D <= 128) fn = vec ? attn_any_kernel<T, 1, true> : attn_any_kernel<T, 1, false>;
+    else fn = vec ? attn_any_kernel<T, 2, true> : attn_any_kernel<T, 2, false>;
     const cudaError_t e = allow_smem((const void*)fn, (int)cfg.dynamicSmemBytes);
     if (e != cudaSuccess) return e;
     return cudaLaunchKernelEx(&cfg, fn, p);
@@ -316,7 +401,7 @@ cudaError_t launch_join(const AttnP& p, const AttnShape& sh, cudaLaunchConfig_t 
     return few ? launch_join_of<T, 1>(p, sh.M, cfg) : launch_join_of<T, kJoinWarps>(p, sh.M, cfg);
 }
 
-// Two CTAs per SM fit at every head size (at most 88 KB each).
+// Two CTAs per SM fit up to 128 channels (at most 78 KB each; 152 KB at 256).
 AttnShape any_shape() { return AttnShape{kPathAny, kAnyM, kAnyKT, kAnyUC, 2 * sm_count(), 1}; }
 
 int64_t shape_bytes(const AttnShape& sh, int head_dim) {

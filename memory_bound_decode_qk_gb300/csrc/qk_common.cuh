@@ -534,6 +534,18 @@ __device__ void generic_head(const QKP& p, const char* src, char* dst, const cha
 template <typename T, bool FP8>
 cudaError_t launch_qk_quad(const QKArgs& a, const QKP& p, cudaLaunchConfig_t cfg, bool* handled);
 
+// Whether a call with several axes takes the four-threads-per-head path, w being
+// the waves of the lane-group grid.  Measured on GB300 at T = 64 to 4096, four
+// threads per head against the lane group: blocks, 16/8 heads of 256: 4.90
+// against 4.84 us at T = 256, 10.0 / 13.3 at 1156, 26.2 / 44.1 at 4096; 32/8
+// heads of 128: 7.1 / 6.4 at 512, 25.9 / 37.7 at 4096.  Dealt pairs cost each of
+// its threads a load per pair: 24/4 heads of 256 still gain from T = 512 (7.6 /
+// 8.4, 33.6 / 53.5 at 4096), the QKV write of 32/8 heads of 128 loses at every
+// T (65.4 / 53.1 at 4096).
+inline bool axes_take_quad(double w, int cycled, int64_t head_bytes) {
+    return w > 1.3 && (!cycled || head_bytes == 512);
+}
+
 // Whether the four-threads-per-head path suits a geometry at all (past the
 // geometry's quad_min_waves of the lane-group grid).
 bool quad_suits(int layout, int rotary_dim, int64_t head_bytes);

@@ -243,7 +243,7 @@ cudaError_t launch_typed(const QKArgs& a, QKP& p, cudaStream_t s) {
         const bool two = !axes && sizeof(T) == 2 && hbytes == 512 && a.layout == kRotateHalf &&
                          a.rotary_dim <= D / 2 && (a.mode & kModeUnrounded) == 0;
         const double w = (double)blocks / (double)(resident_ctas((const void*)vfn, threads) * sms);
-        const bool take_quad = !axes && (two ? w > 1.6 : (double)blocks > wave);
+        const bool take_quad = axes ? axes_take_quad(w, a.axes.cycled, hbytes) : two ? w > 1.6 : (double)blocks > wave;
         if (take_quad && quad_suits(a.layout, a.rotary_dim, hbytes)) {
             bool handled = false;
             cudaError_t e = launch_qk_quad<T, FP8>(a, p, cfg, &handled);

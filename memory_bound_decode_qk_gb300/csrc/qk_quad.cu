@@ -136,14 +136,34 @@ struct QKVMap {
     }
 };
 
+// Cache elements of a token's axes (several axes; the launcher checks that the
+// cache has fewer than 2^31 elements), and whether the token rotates.
+struct QuadAxes {
+    int row[4];
+    bool in;
+};
+
 // One head unit's loaded chunks and what the arithmetic needs besides them.
-template <int C>
+template <int C, bool AXES>
 struct QuadHead {
     uint4 raw[C];
     QuadUnit un;
-    int64_t pos;
+    std::conditional_t<AXES, QuadAxes, int64_t> pos;
     bool active, isv;
 };
+
+// Cos (or sin) of pairs j .. j + 3 of a token with several axes: one vector
+// where they have one axis, else pair by pair.
+__device__ __forceinline__ float4 axes4(const QKP& p, const QuadAxes& x, const float* base, int j) {
+    auto at = [&](int k) {
+        const int a = pair_axis(p, k);
+        return (a == 0 ? x.row[0] : a == 1 ? x.row[1] : a == 2 ? x.row[2] : x.row[3]) + k;
+    };
+    if (!p.cycled && pair_axis(p, j) == pair_axis(p, j + 3)) {
+        return __ldg(reinterpret_cast<const float4*>(base + at(j)));
+    }
+    return make_float4(__ldg(base + at(j)), __ldg(base + at(j + 1)), __ldg(base + at(j + 2)), __ldg(base + at(j + 3)));
+}
 
 // RQ: rotate-half: chunks per thread that are first members (HVQ); interleaved:
 // chunks per thread that rotate.  0: no channel rotates.
@@ -152,7 +172,9 @@ struct QuadHead {
 // overlap across iterations instead of alternating in lockstep waves.
 // UNR: the unrounded form (the rotation takes the fp32 normalized value; one
 // rounding after it), for the instantiated geometries only.
-template <typename T, bool FP8, int C, int LAYOUT, int RQ, bool PIPE, class Map, bool UNR = false>
+// AXES: several positions per token (rotate-half, rounded).
+template <typename T, bool FP8, int C, int LAYOUT, int RQ, bool PIPE, class Map, bool UNR = false,
+          bool AXES = false>
 __device__ __forceinline__ void quad_body(const QKP& p, const Map& map) {
     constexpr int N = vec_elems<T>();
     constexpr int D = C * K * N;
@@ -192,7 +214,7 @@ __device__ __forceinline__ void quad_body(const QKP& p, const Map& map) {
     };
 
     // issue every load of the unit in slot hs of the pass at `base`
-    auto load = [&](uint32_t base, QuadHead<C>& h) {
+    auto load = [&](uint32_t base, QuadHead<C, AXES>& h) {
         const uint32_t u = base + hs;
         h.active = u < p.units;
         h.un = map.unit(p, h.active ? u : base, hb);
@@ -202,18 +224,34 @@ __device__ __forceinline__ void quad_body(const QKP& p, const Map& map) {
                                 : make_uint4(0u, 0u, 0u, 0u);
         }
         h.isv = Map::kHasV && h.un.kind == kKindV;
-        h.pos = -1;
-        if (RQ > 0 && h.active && !h.isv) h.pos = __ldg(p.pos + h.un.t);
+        if constexpr (AXES) {
+            h.pos.in = false;
+            if (h.active && !h.isv) {
+                const AxisPos x = load_axis_pos(p, h.un.t);
+                h.pos.in = x.in;
+#pragma unroll
+                for (int a = 0; a < 4; ++a) h.pos.row[a] = x.in ? (int)x.at[a] * p.half : 0;
+            }
+        } else {
+            h.pos = -1;
+            if (RQ > 0 && h.active && !h.isv) h.pos = __ldg(p.pos + h.un.t);
+        }
     };
 
     // the arithmetic and stores of one loaded unit
-    auto process = [&](QuadHead<C>& h) {
+    auto process = [&](QuadHead<C, AXES>& h) {
         uint4 (&raw)[C] = h.raw;
         const QuadUnit& un = h.un;
         const bool active = h.active, isv = h.isv;
-        const int64_t pos = h.pos;
-        const bool rot = RQ > 0 && pos >= 0 && pos < p.cache_len;
-        if (rot) {
+        int64_t pos = -1;
+        bool rot = false;
+        if constexpr (AXES) {
+            rot = h.pos.in;
+        } else {
+            pos = h.pos;
+            rot = RQ > 0 && pos >= 0 && pos < p.cache_len;
+        }
+        if (!AXES && rot) {
             // the cos/sin lines of the rotated chunks into L1 now, so that
             // their round trip overlaps the normalization below
 #pragma unroll
@@ -349,7 +387,14 @@ __device__ __forceinline__ void quad_body(const QKP& p, const Map& map) {
                     const float4* s4 = reinterpret_cast<const float4*>(p.sn + pos * p.half + c * N);
 #pragma unroll
                     for (int v = 0; v < N / 4; ++v) {
-                        const float4 cc = __ldg(c4 + v), sv = __ldg(s4 + v);
+                        float4 cc, sv;
+                        if constexpr (AXES) {
+                            cc = axes4(p, h.pos, p.cs, c * N + 4 * v);
+                            sv = axes4(p, h.pos, p.sn, c * N + 4 * v);
+                        } else {
+                            cc = __ldg(c4 + v);
+                            sv = __ldg(s4 + v);
+                        }
                         const float cs[4] = {cc.x, cc.y, cc.z, cc.w};
                         const float sn[4] = {sv.x, sv.y, sv.z, sv.w};
 #pragma unroll
@@ -371,13 +416,13 @@ __device__ __forceinline__ void quad_body(const QKP& p, const Map& map) {
     uint32_t base = blockIdx.x * heads_per_cta;
     if (base >= p.units) return;  // the same for the whole CTA
     if constexpr (Map::kHasV) stage();
-    QuadHead<C> h0;
+    QuadHead<C, AXES> h0;
     load(base, h0);
     if constexpr (!Map::kHasV) stage();
     if constexpr (PIPE) {
         // two buffers in turn: the next pass is loaded into one while the
         // other is processed (passes are the same for the whole CTA)
-        QuadHead<C> h1;
+        QuadHead<C, AXES> h1;
         for (;;) {
             uint32_t next = base + stride;
             if (next >= p.units) {
@@ -412,6 +457,27 @@ __global__ void __launch_bounds__(256, (quad_min_blocks<T, FP8, C, LAYOUT, RQ,
     qk_quad_kernel(QKP p) {
     quad_body<T, FP8, C, LAYOUT, RQ, quad_pipe<T, C, LAYOUT, RQ>(), QKMap, UNR>(p, QKMap{});
 }
+
+// Several axes: the one-pass form (the positions of two heads in flight would not
+// fit the registers of the load-ahead one).
+template <typename T, int C, int RQ>
+__global__ void __launch_bounds__(256, (quad_min_blocks<T, false, C, kRotateHalf, RQ, false>()))
+    qk_quad_axes_kernel(QKP p) {
+    quad_body<T, false, C, kRotateHalf, RQ, false, QKMap, false, true>(p, QKMap{});
+}
+template <typename T, int C, int RQ>
+__global__ void __launch_bounds__(256, (quad_min_blocks<T, false, C, kRotateHalf, RQ, false>()))
+    qkv_quad_axes_kernel(QKVP a) {
+    quad_body<T, false, C, kRotateHalf, RQ, false, QKVMap, false, true>(a.p, QKVMap{&a});
+}
+template <typename T, bool FP8, int C, int LAYOUT, int RQ>
+struct QKAxesSel {
+    static constexpr void (*fn)(QKP) = qk_quad_axes_kernel<T, C, RQ>;
+};
+template <typename T, bool FP8, int C, int LAYOUT, int RQ>
+struct QKVAxesSel {
+    static constexpr void (*fn)(QKVP) = qkv_quad_axes_kernel<T, C, RQ>;
+};
 
 template <typename T, int C, int LAYOUT, int RQ>
 __global__ void __launch_bounds__(256, (quad_min_blocks<T, false, C, LAYOUT, RQ,
@@ -451,6 +517,24 @@ auto pick_rq(int layout, int rq) -> decltype(Sel<T, FP8, C, kRotateHalf, 0>::fn)
         case 4: return C >= 8 ? Sel<T, FP8, C, kRotateHalf, (C >= 8 ? 4 : 1)>::fn : nullptr;
         default: return nullptr;
     }
+}
+
+// The same for several axes, rotate-half.
+template <template <typename, bool, int, int, int> class Sel, typename T, int C>
+auto pick_axes(int rq) -> decltype(Sel<T, false, C, kRotateHalf, 1>::fn) {
+    switch (rq) {
+        case 1: return Sel<T, false, C, kRotateHalf, 1>::fn;
+        case 2: return C >= 4 ? Sel<T, false, C, kRotateHalf, (C >= 4 ? 2 : 1)>::fn : nullptr;
+        case 4: return C >= 8 ? Sel<T, false, C, kRotateHalf, (C >= 8 ? 4 : 1)>::fn : nullptr;
+        default: return nullptr;
+    }
+}
+
+// Whether the path serves a call with several axes: 16-bit, rotate-half, rounded,
+// not FP8, a cache of fewer than 2^31 elements (its rows are kept in 32 bits).
+bool axes_suit(int dt, int out_dt, int layout, int mode, const QKP& p) {
+    return dt != kF32 && out_dt == dt && layout == kRotateHalf && (mode & kModeUnrounded) == 0 && p.rot > 0 &&
+           p.cache_len <= ((int64_t(1) << 31) - 1) / p.half;
 }
 
 // Chunks per thread C and rotated chunks RQ of a geometry the path takes, or
@@ -523,6 +607,15 @@ cudaError_t launch_qk_quad(const QKArgs& a, const QKP& p, cudaLaunchConfig_t cfg
         return cudaSuccess;
     }
     void (*fn)(QKP) = nullptr;
+    if (a.axes.n > 0 && p.rot > 0) {
+        if constexpr (sizeof(T) == 2 && !FP8) {
+            if (!axes_suit(a.dt, a.out_dt, a.layout, a.mode, p)) return cudaSuccess;
+            fn = C == 2 ? pick_axes<QKAxesSel, T, 2>(rq) : C == 4 ? pick_axes<QKAxesSel, T, 4>(rq) : pick_axes<QKAxesSel, T, 8>(rq);
+        }
+        if (fn == nullptr) return cudaSuccess;
+        *handled = true;
+        return launch_quad(fn, p, p.units, false, C, cfg);
+    }
     if (unr) {
         // the unrounded form for 16-bit rotate-half heads of 512 bytes with
         // rotary 64 (the text profiles) and of 256 bytes rotating fully;
@@ -557,6 +650,15 @@ cudaError_t launch_qkv_quad(const QKVArgs& a, const QKVP& k, cudaLaunchConfig_t 
         return cudaSuccess;
     }
     void (*fn)(QKVP) = nullptr;
+    if (a.axes.n > 0 && k.p.rot > 0) {
+        if constexpr (sizeof(T) == 2) {
+            if (!axes_suit(a.dt, a.dt, a.layout, 0, k.p)) return cudaSuccess;
+            fn = C == 2 ? pick_axes<QKVAxesSel, T, 2>(rq) : C == 4 ? pick_axes<QKVAxesSel, T, 4>(rq) : pick_axes<QKVAxesSel, T, 8>(rq);
+        }
+        if (fn == nullptr) return cudaSuccess;
+        *handled = true;
+        return launch_quad(fn, k, k.p.units, false, C, cfg);
+    }
     switch (C) {
         case 2: fn = pick_rq<QKVSel, T, false, 2>(a.layout, rq); break;
         case 4: fn = pick_rq<QKVSel, T, false, 4>(a.layout, rq); break;

@@ -284,7 +284,7 @@ cudaError_t launch_typed(const QKVArgs& a, QKVP& k, cudaStream_t s, bool* handle
     const bool two = !axes && sizeof(T) == 2 && D * (int)sizeof(T) == 512 && a.layout == kRotateHalf &&
                      k.p.rot <= D / 2;
     const double w = (double)blocks / (double)wave;
-    const bool take_quad = !axes && (two ? w > 1.6 : blocks > wave);
+    const bool take_quad = axes ? axes_take_quad(w, a.axes.cycled, (int64_t)D * (int64_t)sizeof(T)) : two ? w > 1.6 : blocks > wave;
     if (take_quad && quad_suits(a.layout, k.p.rot, (int64_t)D * (int64_t)sizeof(T))) {
         bool quad = false;
         cudaError_t e = launch_qkv_quad<T>(a, k, cfg, &quad);

@@ -9,6 +9,7 @@ the caller passes none.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -223,14 +224,22 @@ def quantize_fp8(x, inv_scale, *, out=None, stream=None):
     return out
 
 
+_AXIS_ORDER = {"blocks": AXES_BLOCKS, "cycled": AXES_CYCLED}
+
+
+@functools.lru_cache(maxsize=256)
+def _section_array(sections):
+    return (ctypes.c_int32 * max(1, len(sections)))(*sections)
+
+
 def _axis_args(sections, axis_order, positions, tokens):
     """(axes, sections array, order) of a rotary embedding with several axes."""
-    order = {"blocks": AXES_BLOCKS, "cycled": AXES_CYCLED}.get(axis_order, axis_order)
+    sections = tuple(sections)
     n = len(sections)
-    if positions is not None and (positions.dtype != torch.int64 or
-                                  tuple(positions.shape) != (n, tokens)):
+    if positions is not None and not (positions.dtype is torch.int64 and
+                                      positions.shape == (n, tokens)):
         raise ValueError(f"positions must be int64 [{n}, {tokens}] for {n} sections")
-    return n, (ctypes.c_int32 * n)(*sections), order
+    return n, _section_array(sections), _AXIS_ORDER.get(axis_order, axis_order)
 
 
 def qkv_rope_cache(qkv, q_heads, kv_heads, wq, wk, positions, cos, sin, slots, k_cache, v_cache,

@@ -238,32 +238,6 @@ __device__ __forceinline__ uint32_t exponent_bits(uint32_t w) {
     return std::is_same<T, __half>::value ? (w & 0x7C007C00u) + 0x04000400u : (w & 0x7F807F80u) + 0x00800080u;
 }
 
-// 4 x 4 transpose over groups of four lanes: u[k] of lane l becomes u[l & 3] of
-// lane (l & ~3) + k.  Rows that lie in lanes become pieces of one row in
-// neighbouring lanes, so that a store fills whole sectors (a lane per row
-// writes 32 lines at once: 18,000 cycles for a tile of 128 x 256 outputs).
-template <int R>
-__device__ __forceinline__ void transpose4(uint32_t (&u)[4][R], int lane) {
-#pragma unroll
-    for (int d = 1; d <= 2; d <<= 1) {
-        const bool up = (lane & d) != 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (k & d) continue;
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const uint32_t give = up ? u[k][r] : u[k | d][r];
-                const uint32_t take = __shfl_xor_sync(0xffffffffu, give, d);
-                if (up) {
-                    u[k][r] = take;
-                } else {
-                    u[k | d][r] = take;
-                }
-            }
-        }
-    }
-}
-
 // The lowest n bits (n clamped to 0 .. 32).
 __device__ __forceinline__ uint32_t bits_below(int n) {
     return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
@@ -855,9 +829,6 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                 const float nan = *failed ? NAN : 0.0f;
                 float* part = slot < 0 ? nullptr : part_of<M>(p, w.piece, slot);
                 const int64_t orow = mine ? out_row(p, w.s, w.h, r0 + row) : 0;
-                int64_t quad_row[4];  // of the rows of this lane's group of four
-#pragma unroll
-                for (int k = 0; k < 4; ++k) quad_row[k] = __shfl_sync(0xffffffffu, orow, (lane & ~3) + k);
                 const float scale = (part != nullptr ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum) + nan;
 #pragma unroll 1
                 for (int c = 0; c < DP / 32; ++c) {
@@ -895,56 +866,22 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                         for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(y[k]);
                         __syncwarp();
                     }
-                    // scaled by the row's own factor, then four lanes' rows in turn
-                    const int piece = lane & 3, first = row & ~3;
-                    if (part != nullptr) {
+                    if (mine) {
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            uint32_t u[4][4];
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) u[k >> 2][k & 3] = __float_as_uint(__uint_as_float(o[half * 16 + k]) * scale);
-                            transpose4<4>(u, lane);
-                            const int d = c * 32 + half * 16 + piece * 4;
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                if (first + k < rows && d < p.D) {
-                                    *reinterpret_cast<uint4*>(part + (int64_t)(i * kTile + first + k) * p.D + d) =
-                                        make_uint4(u[k][0], u[k][1], u[k][2], u[k][3]);
-                                }
-                            }
-                        }
-                    } else if (p.out_fp8) {
-                        uint32_t u[4][2];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
+                        for (int k = 0; k < 32; k += 8) {
+                            const int d = c * 32 + k;
+                            if (d >= p.D) continue;
                             float y[8];
 #pragma unroll
-                            for (int z = 0; z < 8; ++z) y[z] = __uint_as_float(o[k * 8 + z]) * scale;
-                            const uint2 q8 = quantize_vec<8>(y, p.inv);
-                            u[k][0] = q8.x;
-                            u[k][1] = q8.y;
-                        }
-                        transpose4<2>(u, lane);
-                        const int d = c * 32 + piece * 8;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            if (first + k < rows && d < p.D) {
-                                *reinterpret_cast<uint2*>(p.out + quad_row[k] * p.D + d) = make_uint2(u[k][0], u[k][1]);
-                            }
-                        }
-                    } else {
-                        uint32_t u[4][4];
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            u[k >> 2][k & 3] = pack2<T>(__uint_as_float(o[2 * k]) * scale, __uint_as_float(o[2 * k + 1]) * scale);
-                        }
-                        transpose4<4>(u, lane);
-                        const int d = c * 32 + piece * 8;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            if (first + k < rows && d < p.D) {
-                                *reinterpret_cast<uint4*>(p.out + (quad_row[k] * p.D + d) * 2) =
-                                    make_uint4(u[k][0], u[k][1], u[k][2], u[k][3]);
+                            for (int z = 0; z < 8; ++z) y[z] = __uint_as_float(o[k + z]) * scale;
+                            if (part != nullptr) {
+                                float4* dst = reinterpret_cast<float4*>(part + (int64_t)(i * kTile + row) * p.D + d);
+                                dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+                                dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+                            } else if (p.out_fp8) {
+                                *reinterpret_cast<uint2*>(p.out + orow * p.D + d) = quantize_vec<8>(y, p.inv);
+                            } else {
+                                *reinterpret_cast<uint4*>(p.out + (orow * p.D + d) * 2) = pack_vec<T, 8>(y);
                             }
                         }
                     }

@@ -460,7 +460,7 @@ cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s) {
         // rows of a unit: packed (token, head of the group) rows of the
         // average sequence
         const int64_t rows = a.tokens * p.G / a.num_seqs;
-        if (rows > 64 && tc_suits(p)) sh = tc_shape(a.head_dim);
+        if (rows > 64 && aligned(a.out) && tc_suits(p)) sh = tc_shape(a.head_dim);
         else sh = mma_shape(rows <= 16 ? kPathFew : kPathMore, a.dt, a.head_dim);
     }
     p.min_per = sh.path == kPathFew ? 2 : 1;

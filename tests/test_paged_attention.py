@@ -294,6 +294,24 @@ def test_unaligned_caches(dt):
 
 
 @gpu
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("new", [1, 20, 200])
+def test_an_output_aligned_to_its_elements(new, fp8):
+    # every tensor but the output (and the statistics) on 16 bytes
+    c = make("bf16", 8, 2, 128, 16, [(300, new), (257, new)], seed=26)
+    d = {n: x.cuda() for n, x in c.items() if n != "page"}
+    odt = torch.uint8 if fp8 else torch.bfloat16
+    raw = torch.full((d["q"].numel() + 2,), 7, dtype=odt, device="cuda")
+    stats = torch.full((2 * new * 8 + 2,), 7.0, device="cuda")
+    edge_ops.paged_attention(d["q"], d["k"], d["v"], d["table"], d["lens"], page_size=16, q_starts=d["starts"],
+                             out=raw[1:-1].view(d["q"].shape), lse=stats[1:-1].view(-1, 8), fp8=fp8, inv_scale=50.0)
+    ref, tol, lse, lt = paged_ref.attention(c["q"], c["k"], c["v"], c["table"], c["lens"], c["starts"], 16, 128 ** -0.5)
+    paged_ref.check_rows(raw[1:-1].view(d["q"].shape), ref, tol, torch.bfloat16, 50.0 if fp8 else None)
+    assert ((stats[1:-1].view(-1, 8).cpu().double() - lse).abs() <= lt).all()
+    assert raw[0] == 7 and raw[-1] == 7 and stats[0] == 7 and stats[-1] == 7
+
+
+@gpu
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("new", [1, 60])
 def test_same_bits_again_and_with_a_dirty_workspace(dt, new):

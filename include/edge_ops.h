@@ -398,12 +398,14 @@ int64_t edge_paged_attention_workspace(edge_dtype dt, int32_t q_heads, int32_t k
  * refs:        [num_pages] int32.   All index arrays are device memory.
  * Written buffers must not overlap each other or any other buffer.  Results do
  * not depend on timing.  EDGE_ERR_UNSUPPORTED: page_bytes of 2^31 or more, or
- * more than 2^31 pieces of 1024 bytes in one cache's moves.
+ * more than 2^31 pieces of 1024 bytes in one cache's moves.  Numbers from the
+ * device are checked there: no call reads or writes outside its buffers.
  *
  * edge_pages_copy copies page src[i] to page dst[i] in every cache, for i < n.
  *   Pairs with a page outside the pool, or with src[i] == dst[i], are passed
  *   over.  Of the other pairs with the same destination the last is carried
  *   out, and a pair whose source is the destination of another is not.
+ * EDGE_ERR_UNSUPPORTED: n above 65536.
  */
 edge_status edge_pages_copy(void* const* caches, int32_t num_caches, int64_t page_bytes,
                             int32_t num_pages, const int32_t* src, const int32_t* dst, int32_t n,

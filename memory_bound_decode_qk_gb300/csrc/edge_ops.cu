@@ -741,6 +741,7 @@ edge_status edge_pages_copy(void* const* caches, int32_t num_caches, int64_t pag
                             void* stream) {
     if (n < 0) return EDGE_ERR_SHAPE;
     if (n > 0 && (src == nullptr || dst == nullptr)) return EDGE_ERR_NULL;
+    if (n > edge::kMaxPagePairs) return EDGE_ERR_UNSUPPORTED;
     if (!aligned(src, 4) || !aligned(dst, 4)) return EDGE_ERR_ALIGN;
     const Span lists[] = {span(src, (int64_t)n * 4), span(dst, (int64_t)n * 4)};
     const edge_status st = check_pool(caches, num_caches, page_bytes, num_pages, n, lists, 2);

@@ -132,7 +132,8 @@ struct PageRows {
     int32_t* lens;           // [num_seqs]
     int num_seqs, max_pages;
 };
-constexpr int64_t kMaxPageForks = 8192;  // of one call
+constexpr int64_t kMaxPageForks = 8192;   // of one call
+constexpr int64_t kMaxPagePairs = 65536;  // each pair is held against all of a call
 bool pages_fit(int64_t page_bytes, int64_t pairs);
 int64_t pages_compact_workspace(int num_pages);
 cudaError_t launch_pages_copy(const PagePool& pool, const int32_t* src, const int32_t* dst, int n,

@@ -447,7 +447,9 @@ cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s) {
     p.gdiv = make_fastdiv((uint32_t)p.G);
     p.pdiv = make_fastdiv((uint32_t)a.page_size);
     p.causal = a.causal;
-    p.window = a.causal ? a.window : 0;
+    // positions and keys are below 2^30, so a wider window is none, and the
+    // kernels' differences stay inside 32 bits
+    p.window = a.causal ? (a.window < (1 << 30) ? a.window : 1 << 30) : 0;
     p.out_fp8 = a.out_dt == kFP8;
     p.max_len = a.max_pages * a.page_size;
     p.scale_log2 = a.scale * 1.4426950408889634f;

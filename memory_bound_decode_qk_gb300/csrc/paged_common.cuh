@@ -266,7 +266,7 @@ __device__ bool walk_begin(const AttnP& p, Walk& w, WalkSmem<PP>& sm, int thread
             const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += up;
         }
-        __syncthreads();  // sm.warp's readers of the round before are done
+        __syncthreads();  // the readers of sm.warp before are done
         if (lane == 31) sm.warp[wid] = inc;
         __syncthreads();
         int64_t before = base, all = 0;

@@ -175,6 +175,17 @@ def test_window(dt, window, hq, hk, D):
 
 
 @gpu
+@pytest.mark.parametrize("dt,new", [("f32", 9), ("bf16", 1), ("bf16", 9), ("bf16", 90)])
+def test_the_widest_window_is_none(dt, new):
+    # fewer keys than new tokens in one sequence: its first positions are negative
+    c = make(dt, 8, 2, 128, 16, [(300, new), (5, new), (90, new)], seed=27)
+    want, _ = run(c)
+    for window in (300, 2 ** 30 - 1, 2 ** 31 - 1):
+        got, _ = verify(c, window=window)
+        assert torch.equal(got, want)
+
+
+@gpu
 @pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("hq,hk,D", [(8, 8, 64), (8, 2, 128), (4, 1, 256)])
 def test_cross_attention(dt, hq, hk, D):

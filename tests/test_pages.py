@@ -52,7 +52,7 @@ def compact(L, caches=(C0, C1), bytes=4096, pages=64, out=TAB2, tab=TAB, rows=8,
     (lambda L: copy(L, src=A + 2), ALIGN), (lambda L: copy(L, dst=B + 1), ALIGN),
     (lambda L: copy(L, caches=(C0, C0)), ALIAS), (lambda L: copy(L, caches=(C0, C0 + 4096)), ALIAS),
     (lambda L: copy(L, src=C0 + 64), ALIAS), (lambda L: copy(L, dst=C1), ALIAS),
-    (lambda L: copy(L, bytes=2 ** 31), UNSUP), (lambda L: copy(L, bytes=2 ** 30, n=2 ** 20), UNSUP),
+    (lambda L: copy(L, n=65537), UNSUP), (lambda L: copy(L, bytes=2 ** 31), UNSUP), (lambda L: copy(L, bytes=2 ** 30, n=2 ** 16), UNSUP),
     (lambda L: free(L, tab=None), NULL), (lambda L: free(L, lens=None), NULL), (lambda L: free(L, refs=None), NULL),
     (lambda L: free(L, seqs=None), NULL), (lambda L: free(L, rows=-1), SHAPE), (lambda L: free(L, n=-1), SHAPE),
     (lambda L: free(L, width=-1), SHAPE), (lambda L: free(L, pages=-1), SHAPE),

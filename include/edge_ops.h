@@ -8,7 +8,12 @@
  *   edge_rmsnorm       RMSNorm, with or without a weight
  *   edge_glu_act       SiLU / tanh-GELU gated activation of a merged gate+up
  * Each op can write a static-scale FP8 E4M3 output instead of the activation
- * dtype.
+ * dtype.  Beside them: the rotary embedding alone, LayerNorm, quantization, the
+ * QKV split with its KV-cache write, and what a paged KV cache needs next to
+ * that write:
+ *   edge_paged_attention   attention of new tokens over the cache's pages
+ *   edge_*_axes            rotary positions with several axes
+ *   edge_pages_*           copying, freeing, forking and compacting pages
  *
  * Sources, by page and section:
  *   "thox-edge-ops v2: fused decode kernels for small models on THOX edge

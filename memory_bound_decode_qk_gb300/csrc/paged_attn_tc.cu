@@ -266,7 +266,7 @@ struct Tc {
 
 struct TcSmem {
     uint64_t full[10], empty[10], edge[10];
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+    uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_full[2];
     uint32_t tmem;
     uint32_t failed;
     uint32_t careful;  // a bit per unit (its number mod 32): values to be summed row by row
@@ -330,6 +330,7 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
         for (int i = 0; i < 2; ++i) {
             bar_init(smem_addr(&sh.q_full[i]), q_boxes ? 1 : kTile);
             bar_init(smem_addr(&sh.s_full[i]), 1);
+            bar_init(smem_addr(&sh.p_half[i]), kTile);
             bar_init(smem_addr(&sh.p_full[i]), kTile);
             bar_init(smem_addr(&sh.o_full[i]), 1);
         }
@@ -471,11 +472,13 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
                                 if (t >= a[i] && t < b[i]) {
-                                    bar_wait(smem_addr(&sh.p_full[i]), step[i] & 1, failed);
-                                    ++step[i];
-                                    tc_after();
 #pragma unroll 1
-                                    for (int half = 0; half < 2; ++half) values(256 + i * 128, i * 128, ev, half, t > a[i]);
+                                    for (int half = 0; half < 2; ++half) {
+                                        bar_wait(smem_addr(half == 0 ? &sh.p_half[i] : &sh.p_full[i]), step[i] & 1, failed);
+                                        tc_after();
+                                        values(256 + i * 128, i * 128, ev, half, t > a[i]);
+                                    }
+                                    ++step[i];
                                     if (t == b[i] - 1) tc_commit(smem_addr(&sh.o_full[i]), lead);
                                 }
                                 if (t + 1 >= a[i] && t + 1 < b[i]) {
@@ -727,11 +730,16 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                             pk[k] = pack2<T>(x.x, x.y);
                         }
                         tc_st16(ts + c * 16, pk);
+                        if (c & 1) {
+                            // half of the weights: their product runs under the
+                            // other half's exponentials.  A barrier for each
+                            // half, since one warp may be a half ahead
+                            tc_wait_st();
+                            tc_before();
+                            bar_arrive(smem_addr(c == 1 ? &sh.p_half[i] : &sh.p_full[i]));
+                        }
                     }
                     sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
-                    tc_wait_st();
-                    tc_before();
-                    bar_arrive(smem_addr(&sh.p_full[i]));
                     ++step;
                 } else {
                     // Half of the tile at a time, so that the product with the first

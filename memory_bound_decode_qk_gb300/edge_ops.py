@@ -456,6 +456,8 @@ def paged_attention(q, k_cache, v_cache, block_table, lens, *, page_size, q_star
                                    workspace=workspace)
     if out is None:
         out = _alloc(q, q.shape, fp8)
+    if T == 0:
+        return out  # no rows (an empty tensor has no address to pass on)
     if workspace is None:
         workspace = paged_attention_workspace(q, k_cache)
     if scale is None:

@@ -365,6 +365,23 @@ def test_other_stream_and_graph(new):
 
 
 @gpu
+def test_empty_calls():
+    i32 = dict(dtype=torch.int32, device="cuda")
+    q = torch.zeros(0, 4, 64, device="cuda")
+    k = torch.zeros(32, 2, 64, device="cuda")
+    # no tokens, with and without sequences; a cache without pages; a table without columns
+    for b in (0, 2):
+        starts = torch.zeros(b + 1, **i32)
+        assert edge_ops.paged_attention(q, k, k, torch.zeros(b, 3, **i32), torch.ones(b, **i32), page_size=8,
+                                        q_starts=starts).shape == (0, 4, 64)
+    q = torch.ones(2, 4, 64, device="cuda")
+    for cache, width in ((k[:0], 3), (k, 0)):
+        out = edge_ops.paged_attention(q, cache, cache, torch.zeros(2, width, **i32), torch.full((2,), 9, **i32),
+                                       page_size=8)
+        assert (out == 0).all()
+
+
+@gpu
 def test_binding_checks_its_tensors():
     c = make("bf16", 4, 2, 64, 16, [(40, 2)], seed=19)
     d = {n: x.cuda() for n, x in c.items() if n != "page"}

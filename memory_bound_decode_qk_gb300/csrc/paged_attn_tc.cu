@@ -249,7 +249,9 @@ template <int DP>
 struct Tc {
     static constexpr int kNQ = DP <= 128 ? 2 : 1;       // query tiles of a unit
     static constexpr int kM = kNQ * kTile;
-    static constexpr int kUC = kNQ == 2 ? 2 : 4;        // a unit's start and end, in key tiles
+    // a unit's start and end, in key tiles (one query tile: about 10,000 cycles
+    // of edges and output against 3000 of a tile)
+    static constexpr int kUC = kNQ == 2 ? 2 : 3;
     // a ring entry: 128 keys and CW channels of them.  Wide heads are cut by
     // channels, not by keys: 64-key operands made the pipe read Q twice as often
     // from shared memory, whose bandwidth then bound it (3100 cycles a tile).

@@ -301,6 +301,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnP p) {
     // parts: slot 1 of c0, then slot 0 of c0 + 1 .. u.x
     const float* base = p.part + ((int64_t)c0 * 2 + 1) * rec;
     const int n = u.x - c0 + 1;
+    // whether warp i's parts saw anything (as for a part)
+    auto counts = [&](int i) { return top_of[i] != -INFINITY || sum_of[i] != 0.0f; };
     for (int r0 = blockIdx.y * R; r0 < rows; r0 += gridDim.y * R) {
         const int r = min(r0 + wid / W, rows - 1);  // warps past the last row repeat it
         // one pass over this warp's parts with their running maximum
@@ -317,8 +319,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnP p) {
                 const int d = lane + 32 * k;
                 x[k] = d < p.D ? pc[(int64_t)r * p.D + d] : 0.0f;
             }
-            // (a part that saw nothing has m = -inf and wrote no outputs)
-            if (m == -INFINITY) continue;
+            // a part that saw nothing has m = -inf and a sum of zero; one whose
+            // scores are all NaN has m = -inf (maxima pass NaN over) and the NaN in
+            // its sum, which the row takes on
+            if (m == -INFINITY && li == 0.0f) continue;
             const float next = fmaxf(top, m);
             const float keep = ex2(top - next), f = ex2(m - next);
             top = next;
@@ -339,7 +343,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnP p) {
             top = all;
             l = 0.0f;
             for (int i = 0; i < W; ++i) {
-                if (top_of[set + i] != -INFINITY) l = fmaf(ex2(top_of[set + i] - top), sum_of[set + i], l);
+                if (counts(set + i)) l = fmaf(ex2(top_of[set + i] - top), sum_of[set + i], l);
             }
         }
         const int64_t orow = out_row(p, s, u.y, u.z * M + r);
@@ -349,7 +353,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnP p) {
             for (int d = sub * 32 + lane; mine && d < p.D; d += 32 * W) {
                 float y = 0.0f;
                 for (int i = 0; i < W; ++i) {
-                    if (top_of[set + i] != -INFINITY) y = fmaf(ex2(top_of[set + i] - top), acc_of[set + i][d], y);
+                    if (counts(set + i)) y = fmaf(ex2(top_of[set + i] - top), acc_of[set + i][d], y);
                 }
                 store_one<T>(p, orow * p.D + d, y * inv);
             }

@@ -32,9 +32,13 @@
 // page outside the pool or outside the keys that the unit sees is copied from
 // behind the tensor's end, which fills zeros.  A page that is seen in part
 // brings rows that no query may touch, and rows that only some see: warps 2
-// and 3 zero the first before the tile is used, and look for infinities and NaN
-// in the second, since 0 * NaN is NaN in a matrix product.  If they find any, the
-// unit's values are summed again row by row with masked keys skipped.
+// and 3 zero the first before the tile is used, and in the second every infinity
+// and NaN, since 0 * NaN is NaN in a matrix product.  If they found any, the
+// rows that see such a key add its infinities and NaN at the unit's end (its
+// weight is positive, so they reach the sum as they are).  Only the keys that
+// some rows of the unit see and others do not are searched for that, at most two
+// for each of its tokens, so the time it takes does not depend on how long the
+// context is.
 //
 // Every wait has a limit of two seconds.  A wait that runs out (which correct
 // operation never does) ends all later waits of the CTA at once and makes its
@@ -245,6 +249,12 @@ __device__ __forceinline__ uint32_t exponent_bits(uint32_t w) {
     return std::is_same<T, __half>::value ? (w & 0x7C007C00u) + 0x04000400u : (w & 0x7F807F80u) + 0x00800080u;
 }
 
+// A pair with its infinities and NaN replaced by zero.
+template <typename T>
+__device__ __forceinline__ uint32_t bounded(uint32_t w) {
+    return w & ~(((exponent_bits<T>(w) >> 15) & 0x00010001u) * 0xFFFFu);
+}
+
 // The lowest n bits (n clamped to 0 .. 32).
 __device__ __forceinline__ uint32_t bits_below(int n) {
     return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
@@ -278,7 +288,7 @@ struct TcSmem {
     uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_full[2];
     uint32_t tmem;
     uint32_t failed;
-    uint32_t careful;  // a bit per unit (its number mod 32): values to be summed row by row
+    uint32_t careful;  // a bit per unit (its number mod 32): infinities and NaN taken out of its values
 };
 
 // The tiles [a, b) of the unit's part (relative to its first tile) of which query
@@ -303,6 +313,39 @@ __device__ __forceinline__ bool is_edge(const Walk& w, int j, int n) {
 template <int NQ>
 __device__ __forceinline__ uint32_t value_place(int t, int cnt) {
     return NQ == 2 || t + 1 == cnt ? 2 * t + 1 : 2 * t + 2;
+}
+
+// Adds the infinities and NaN of the values of keys [first, behind) that the
+// thread's row sees, [from, upto), to its outputs o of channels ch .. ch + 31.  All
+// lanes of the warp call it with the same first, behind and ch: a lane looks at
+// every 32nd key, and all take what a lane has found.
+template <typename T>
+__device__ __forceinline__ void add_unbounded(const AttnP& p, const Walk& w, int first, int behind, int from, int upto,
+                                              int ch, uint32_t (&o)[32]) {
+    const int lane = threadIdx.x & 31;
+    for (int j0 = first; j0 < behind; j0 += 32) {
+        const int64_t slot = j0 + lane < behind ? key_slot(p, w.b, j0 + lane) : -1;
+        uint32_t odd = 0;
+        if (slot >= 0) {
+            const char* v = p.v + ((slot * p.hk + w.h) * p.D + ch) * 2;
+            for (int k = 0; k < 32 && ch + k < p.D; k += 8) {
+                const uint4 y = __ldg(reinterpret_cast<const uint4*>(v + 2 * k));
+                odd |= exponent_bits<T>(y.x) | exponent_bits<T>(y.y) | exponent_bits<T>(y.z) | exponent_bits<T>(y.w);
+            }
+        }
+        uint32_t keys = __ballot_sync(0xffffffffu, (odd & 0x80008000u) != 0);
+        for (; keys != 0; keys &= keys - 1) {
+            const int src = __ffs(keys) - 1;
+            const int64_t at = __shfl_sync(0xffffffffu, slot, src);
+            const bool see = j0 + src >= from && j0 + src < upto;
+            const T* v = reinterpret_cast<const T*>(p.v) + (at * p.hk + w.h) * p.D + ch;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+                const float y = ch + k < p.D ? to_f(v[k]) : 0.0f;
+                if (see && !(fabsf(y) < INFINITY)) o[k] = __float_as_uint(__uint_as_float(o[k]) + y);
+            }
+        }
+    }
 }
 
 template <typename T, int DP>
@@ -540,8 +583,8 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
             }
         } else {
             // ---- values at an edge (warps 2 and 3, half of the rows each): rows
-            // that no query sees become zero; infinities and NaN in rows that some
-            // see mark the unit
+            // that no query sees become zero, and so do infinities and NaN in rows
+            // that some see; those mark the unit
             uint32_t e = 0, phase = 0, unit = 0;
             do {
                 // the mark of a unit long past is cleared for a later one (the
@@ -574,10 +617,20 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                                 odd |= exponent_bits<T>(y.x) | exponent_bits<T>(y.y) | exponent_bits<T>(y.z) | exponent_bits<T>(y.w);
                             }
                         };
+                        auto clean = [&](int from, int to) {
+                            for (int i = from * kRow + me; i < to * kRow; i += 64) {
+                                uint4* y = reinterpret_cast<uint4*>(v + panel_at<KT>(i / kRow, i % kRow));
+                                *y = make_uint4(bounded<T>(y->x), bounded<T>(y->y), bounded<T>(y->z), bounded<T>(y->w));
+                            }
+                        };
                         wipe(0, a);
                         wipe(d, KT);
                         scan(a, b);
                         scan(c, d);
+                        if ((odd & 0x80008000u) != 0) {
+                            clean(a, b);
+                            clean(c, d);
+                        }
                         if (__any_sync(0xffffffffu, (odd & 0x80008000u) != 0) && lane == 0) atomicOr(&sh.careful, 1u << (unit & 31));
                         fence_async_smem();
                         asm volatile("bar.sync 2, 64;" ::: "memory");
@@ -858,30 +911,11 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                         for (int k = 0; k < 32; ++k) o[k] = 0u;
                     }
                     if (again) {
-                        // key by key, weights of zero skipped
-                        float y[32];
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) y[k] = 0.0f;
-                        const int j1 = min((w.k0 + w.off + b) * KT, upto);
-                        for (int j = max((w.k0 + w.off + a) * KT, from); mine && j < j1; ++j) {
-                            const int64_t ks = key_slot(p, w.b, j);
-                            if (ks < 0) continue;
-                            const T* kr = reinterpret_cast<const T*>(p.k) + (ks * p.hk + w.h) * p.D;
-                            const T* vr = reinterpret_cast<const T*>(p.v) + (ks * p.hk + w.h) * p.D;
-                            const T* qr = reinterpret_cast<const T*>(p.q) + orow * p.D;
-                            float x = 0.0f;
-                            for (int d = 0; d < p.D; ++d) x = fmaf(to_f(qr[d]), to_f(kr[d]), x);
-                            x = ex2(fmaf(x, p.scale_log2, ref == -INFINITY ? 0.0f : -ref));
-                            x = round_to<T>(x);
-                            if (x == 0.0f) continue;
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) {
-                                if (c * 32 + k < p.D) y[k] = fmaf(x, to_f(vr[c * 32 + k]), y[k]);
-                            }
-                        }
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(y[k]);
-                        __syncwarp();
+                        // the keys that some rows see: before flo, and from fhi on
+                        const int t0 = (w.k0 + w.off + a) * KT, t1 = (w.k0 + w.off + b) * KT;
+                        const int end = mine ? upto : 0;
+                        add_unbounded<T>(p, w, max(w.keys.lo, t0), min(w.keys.flo, t1), from, end, c * 32, o);
+                        add_unbounded<T>(p, w, max(max(w.keys.flo, w.keys.fhi), t0), min(w.keys.hi, t1), from, end, c * 32, o);
                     }
                     if (mine) {
 #pragma unroll

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import paged_ref
+from memory_bound_decode_qk_gb300 import edge_ops
 from test_paged_attention import make, run
 
 gpu = pytest.mark.gpu
@@ -39,3 +40,64 @@ def test_nan_in_queries_and_keys(path, keys):
     assert torch.isnan(lse.cpu()[gone]).all()
     paged_ref.check_rows(out, ref, tol, c["q"].dtype)
     assert ((lse.cpu().double() - rl).abs() <= lt)[~gone].all()
+
+
+def poison(c, b, j, value, what="v"):
+    c[what][int(c["table"][b, j // c["page"]]) * c["page"] + j % c["page"]] = value
+
+
+WIDE = [(8, 2, 128), (4, 4, 64), (2, 1, 80), (8, 2, 256), (3, 1, 192)]
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("hq,hk,D", WIDE)
+@pytest.mark.parametrize("window", [0, 150])
+def test_unseen_values_change_no_bit(dt, hq, hk, D, window):
+    # prompts and a late chunk.  With two query tiles the first ends keys before the second; the values that only
+    # the second sees must not change how the first is summed
+    c = make(dt, hq, hk, D, 16, [(700, 600), (257, 257), (1900, 300)], seed=32)
+    want, lse = run(c, window=window)
+    marks = [(0, 131, math.inf), (0, 400, math.nan), (1, 120, -math.inf), (1, 255, math.nan), (2, 1700, math.inf)]
+    for b, j, bad in marks:
+        poison(c, b, j, bad)
+    sees = torch.zeros(want.shape[0], dtype=torch.bool)
+    for b, j, _ in marks:
+        first, n, at = int(c["starts"][b]), int(c["starts"][b + 1] - c["starts"][b]), int(c["lens"][b])
+        pos = torch.arange(at - n, at)
+        sees[first:first + n] |= (pos >= j) & ((pos - j < window) if window else True)
+    for _ in range(10):
+        out, stats = run(c, window=window)
+        assert torch.equal(out[~sees], want[~sees]) and torch.equal(stats, lse)
+        assert not torch.isfinite(out[sees]).any(), "what a row sees reaches it"
+
+
+@gpu
+@pytest.mark.parametrize("hq,hk,D", [(8, 2, 128), (8, 2, 256)])
+def test_unseen_values_of_a_long_context(hq, hk, D):
+    # infinities that only the last tokens of a chunk see, 32 thousand keys before them: the sum must neither run
+    # into the kernel's limit of two seconds for a wait nor take much longer than without
+    c = make("bf16", hq, hk, D, 64, [(32768, 300), (32768, 300)], seed=33)
+    d = {n: x.cuda() for n, x in c.items() if n != "page"}
+
+    def go():
+        out = edge_ops.paged_attention(d["q"], d["k"], d["v"], d["table"], d["lens"], page_size=64, q_starts=d["starts"])
+        start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        start.record()
+        edge_ops.paged_attention(d["q"], d["k"], d["v"], d["table"], d["lens"], page_size=64, q_starts=d["starts"], out=out)
+        end.record()
+        end.synchronize()
+        return out, start.elapsed_time(end)
+
+    want, clean_ms = go()
+    for b, j in ((0, 32700), (0, 32560), (1, 32767)):
+        poison(c, b, j, math.inf)
+    d["v"] = c["v"].cuda()
+    out, ms = go()
+    print(f"{ms:.3f} ms, {clean_ms:.3f} ms without infinities")
+    sees = torch.zeros(600, dtype=torch.bool)
+    sees[32560 - 32468:300] = True
+    sees[599] = True
+    assert torch.equal(out[~sees], want[~sees])
+    assert (out[sees] == math.inf).all()
+    assert ms < 50, "the row sums of a context of 32768 keys take 70 ms and more one by one"

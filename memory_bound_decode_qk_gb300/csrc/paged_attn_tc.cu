@@ -288,7 +288,8 @@ struct TcSmem {
     uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_full[2];
     uint32_t tmem;
     uint32_t failed;
-    uint32_t careful;  // a bit per unit (its number mod 32): infinities and NaN taken out of its values
+    // the last unit, counted from 1, with infinities or NaN taken out of its values
+    uint32_t taken;
 };
 
 // The tiles [a, b) of the unit's part (relative to its first tile) of which query
@@ -387,7 +388,7 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
             bar_init(smem_addr(&sh.o_full[i]), 1);
         }
         sh.failed = 0;
-        sh.careful = 0;
+        sh.taken = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async_smem();
     }
@@ -584,12 +585,9 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
         } else {
             // ---- values at an edge (warps 2 and 3, half of the rows each): rows
             // that no query sees become zero, and so do infinities and NaN in rows
-            // that some see; those mark the unit
+            // that some see; the unit's number is noted for those
             uint32_t e = 0, phase = 0, unit = 0;
             do {
-                // the mark of a unit long past is cleared for a later one (the
-                // ring holds fewer than 16 units)
-                if (tid == 64) atomicAnd(&sh.careful, ~(1u << ((unit + 16) & 31)));
                 for (int t = 0; t < w.cnt; ++t) {
                     const int j0 = (w.k0 + w.off + t) * KT;
                     if (!is_edge(w, j0, KT)) continue;
@@ -631,7 +629,7 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
                             clean(a, b);
                             clean(c, d);
                         }
-                        if (__any_sync(0xffffffffu, (odd & 0x80008000u) != 0) && lane == 0) atomicOr(&sh.careful, 1u << (unit & 31));
+                        if (__any_sync(0xffffffffu, (odd & 0x80008000u) != 0) && lane == 0) atomicMax(&sh.taken, unit + 1);
                         fence_async_smem();
                         asm volatile("bar.sync 2, 64;" ::: "memory");
                         if (me == 0) bar_arrive(smem_addr(&sh.full[st]));
@@ -894,7 +892,12 @@ attn_tc_kernel(AttnP p, const __grid_constant__ CUtensorMap kmap, const __grid_c
             if (na < nb) give_queries();
             if (rows > 0) {
                 const bool mine = row < rows;
-                const bool again = a < b && ((*(volatile uint32_t*)&sh.careful >> (unit & 31)) & 1u) != 0;
+                // `taken` only grows, and is set before a tile that it speaks of is
+                // given to the products: it has reached this unit's number if
+                // anything was taken out of its tiles.  These warps may be units
+                // ahead or behind the edge warps; if it has passed the number for
+                // the sake of a later unit, the search finds nothing to add
+                const bool again = a < b && *(volatile uint32_t*)&sh.taken > unit;
                 const int slot = walk_slot(w);
                 const float nan = *failed ? NAN : 0.0f;
                 float* part = slot < 0 ? nullptr : part_of<M>(p, w.piece, slot);

@@ -101,3 +101,28 @@ def test_unseen_values_of_a_long_context(hq, hk, D):
     assert torch.equal(out[~sees], want[~sees])
     assert (out[sees] == math.inf).all()
     assert ms < 50, "the row sums of a context of 32768 keys take 70 ms and more one by one"
+
+
+@gpu
+@pytest.mark.parametrize("hq,hk,D", [(128, 32, 64), (64, 16, 256)])
+def test_unseen_values_before_many_units_without_an_edge(hq, hk, D):
+    # chunks with infinities and NaN in their last keys, each followed by sequences of one token over whole tiles of
+    # keys: hundreds of units that have no edge, through which the search of the edges runs ahead of the sums
+    shape = []
+    for i in range(12):
+        shape += [(300 + i, 300 + i)] + [(128 + 128 * (k % 2), 1) for k in range(12)]
+    c = make("bf16", hq, hk, D, 16, shape, seed=34)
+    rows = c["q"].shape[0] * (hq // hk) / len(shape)
+    assert rows > 64, "the call is one for the kernel of wide chunks"
+    want, lse = run(c)
+    sees = torch.zeros(want.shape[0], dtype=torch.bool)
+    for i in range(12):
+        b = 13 * i
+        n = shape[b][0]
+        poison(c, b, n - 1, math.nan)
+        poison(c, b, n - 3, math.inf)
+        sees[int(c["starts"][b]) + n - 3:int(c["starts"][b]) + n] = True
+    for _ in range(20):
+        out, stats = run(c)
+        assert torch.equal(out[~sees], want[~sees]) and torch.equal(stats, lse)
+        assert not torch.isfinite(out[sees]).any()

@@ -368,9 +368,11 @@ def rope(q, k, positions, cos, sin, *, rotary_dim=None, layout=ROTATE_HALF, q_ou
 def _on(device, stream):
     """The context in which a call allocates and launches: the tensors' device,
     and `stream` as torch's current stream, so that memory taken for the call
-    belongs to the stream that uses it."""
+    belongs to the stream that uses it.  A stream of another device is refused."""
     if stream is None:
         return torch.cuda.device(device)
+    if getattr(stream, "device", device) != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     return torch.cuda.stream(stream)

@@ -366,7 +366,9 @@ edge_status edge_qkv_rope_cache_axes(void* q_out, void* k_cache, void* v_cache, 
  *              and holds nothing between calls; calls that may run at the same
  *              time need one each.
  * Scores, maxima, sums and outputs are held in fp32.  16-bit calls round the
- * weights to dt for the product with the values; the output is rounded once.
+ * weights to dt for the product with the values; with at most 16 packed rows
+ * (tokens * q_heads / kv_heads) per sequence on average, sequences of at most 8
+ * keep what that rounding leaves over as well.  The output is rounded once.
  * Results are the same from run to run.
  * EDGE_ERR_SHAPE: q_heads not a multiple of kv_heads, or a workspace that is
  * too small.  EDGE_ERR_UNSUPPORTED: head_dim above 256, or tokens * q_heads or

@@ -14,9 +14,12 @@
 // joined at the ends of units reached 2.7 TB/s on a ragged batch; this form
 // has no such joins.)
 // Measured on GB300: 64 sequences of 64 to 8192 keys, 32/8 heads of 128, 558 MB
-// in 100 us (5.6 TB/s, 82% of the copy bandwidth); three sequences of 30 to 131
-// thousand keys, 24/4 heads of 256, 967 MB in 162 us (6.0 TB/s); blocks of 16
-// tokens, 32/32 heads of 128, 248 MB in 55 us (4.5 TB/s).  16 keys a stage and
+// in 98 us (5.7 TB/s, 84% of the copy bandwidth); three sequences of 30 to 131
+// thousand keys, 24/4 heads of 256, 967 MB in 165 us (5.85 TB/s); blocks of 16
+// tokens, 32/32 heads of 128, 248 MB in 55 us (4.5 TB/s).  Up to 8 rows the
+// weights keep two 16-bit parts, the second in the rows that are free: 0.5% and
+// 2% of the time of the first two, and their error against 64 bits falls from
+// 1.35 times that of the output's rounding alone to 1.0.  16 keys a stage and
 // three stages hold 96 KB of copies in flight per CTA of 128-channel heads, two
 // CTAs to an SM.
 // attn_more_kernel (64 rows): a warp has 16 rows each and the CTA shares the
@@ -86,6 +89,22 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
         __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
         return *reinterpret_cast<uint32_t*>(&h);
     }
+}
+
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+    if constexpr (std::is_same<T, __half>::value) {
+        return __half22float2(*reinterpret_cast<const __half2*>(&w));
+    } else {
+        return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+    }
+}
+// What rounding a and b to the pair `w` left over, rounded in turn.  (A weight
+// that is NaN has NaN here as well.)
+template <typename T>
+__device__ __forceinline__ uint32_t remainder2(float a, float b, uint32_t w) {
+    const float2 r = unpack2<T>(w);
+    return pack2<T>(a - r.x, b - r.y);
 }
 
 // Whether one of the two values in a word is infinite or NaN.
@@ -175,7 +194,7 @@ __device__ void careful_values(const float (&s)[NT][4], float (&o)[NO][4], const
     }
     __syncwarp();
     for (int j = 0; j < KN; ++j) {
-        const float w0 = round_to<T>(ps[g * KN + j]), w1 = round_to<T>(ps[(g + 8) * KN + j]);
+        const float w0 = ps[g * KN + j], w1 = ps[(g + 8) * KN + j];
 #pragma unroll
         for (int n = 0; n < NO; ++n) {
             const T* v = reinterpret_cast<const T*>(vt + chunk_at<DP>(j, n)) + q;
@@ -375,6 +394,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, DP <= 128 ? 2 : 1) attn_few_ke
                 }
             }
         }
+        // with up to 8 rows, rows 8 to 15 of the products are free
+        const bool half = rows <= 8;
         float o[NO][4];
         RowState st;
 #pragma unroll
@@ -434,6 +455,14 @@ __global__ void __launch_bounds__(kFewWarps * 32, DP <= 128 ? 2 : 1) attn_few_ke
                     }
                 }
             }
+            if (half) {
+                // row r + 8 is row r again, for the remainders of its weights
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    s[n][2] = s[n][0];
+                    s[n][3] = s[n][1];
+                }
+            }
             soft_tile<NT, NO>(s, o, st);
             // several tokens: values that only some rows see
             bool odd = false;
@@ -445,17 +474,42 @@ __global__ void __launch_bounds__(kFewWarps * 32, DP <= 128 ? 2 : 1) attn_few_ke
                 odd = __any_sync(0xffffffffu, odd);
             }
             if (odd) {
+                if (half) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) s[n][2] = s[n][3] = 0.0f;
+                }
                 careful_values<T, DP, KT, NT, NO>(s, o, vt, reinterpret_cast<float*>(kt), lane);  // the keys are done with
                 continue;
             }
-            const uint32_t a[4] = {pack2<T>(s[0][0], s[0][1]), pack2<T>(s[0][2], s[0][3]),
-                                   pack2<T>(s[1][0], s[1][1]), pack2<T>(s[1][2], s[1][3])};
+            uint32_t a[4] = {pack2<T>(s[0][0], s[0][1]), pack2<T>(s[0][2], s[0][3]),
+                             pack2<T>(s[1][0], s[1][1]), pack2<T>(s[1][2], s[1][3])};
+            if (half) {
+                // what the rounding of the weights left over, in the free rows: it
+                // does not show in the output then (relative 2^-16 with bf16, 2^-22
+                // with fp16).  With more rows it would take products of its own
+                // (14% of the time of long sequences of 256 channels) and outputs
+                // of its own: in common ones an infinite value would meet
+                // remainders of either sign.
+                a[1] = remainder2<T>(s[0][2], s[0][3], a[1]);
+                a[3] = remainder2<T>(s[1][2], s[1][3], a[3]);
+            }
 #pragma unroll
             for (int n = 0; n < NO; n += 2) {
                 uint32_t b[4];
                 ldsm4t(va + chunk_at<DP>(lane & 15, n + (lane >> 4)), b);
                 mma16816<T>(o[n], a, b[0], b[1]);
                 mma16816<T>(o[n + 1], a, b[2], b[3]);
+            }
+        }
+        if (half) {
+            // an infinity is one in the first part; the second has either sign of
+            // it, or NaN
+#pragma unroll
+            for (int n = 0; n < NO; ++n) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (fabsf(o[n][i]) < INFINITY) o[n][i] += o[n][i + 2];
+                }
             }
         }
 #pragma unroll

@@ -266,9 +266,13 @@ template <int DP>
 struct Tc {
     static constexpr int kNQ = DP <= 128 ? 2 : 1;       // query tiles of a unit
     static constexpr int kM = kNQ * kTile;
-    // a unit's start and end, in key tiles (one query tile: about 10,000 cycles
-    // of edges and output against 3000 of a tile)
-    static constexpr int kUC = kNQ == 2 ? 2 : 3;
+    // A unit's start and end, in key tiles.  Measured on GB300 over 20 batches for
+    // each form (1 to 16 prompts or chunks of 200 to 16,000 keys, with and without
+    // windows, five head shapes): with 2, 3, 4, 5, 6 and 8 the geometric mean of
+    // the times is 1.08, 1.05, 1.03, 1.03, 1.016 and 1.034 of each batch's best
+    // (one query tile), and 1.09, 1.06, 1.03, 1.03, 1.016 and 1.020 (two).  A
+    // single batch moves by up to 20% with where the cuts happen to fall.
+    static constexpr int kUC = 6;
     // a ring entry: 128 keys and CW channels of them.  Wide heads are cut by
     // channels, not by keys: 64-key operands made the pipe read Q twice as often
     // from shared memory, whose bandwidth then bound it (3100 cycles a tile).

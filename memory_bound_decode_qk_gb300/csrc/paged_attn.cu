@@ -465,11 +465,20 @@ cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s) {
     const bool vec = (a.head_dim * es) % 16 == 0 && aligned(a.k_cache) && aligned(a.v_cache);
     AttnShape sh = any_shape();
     if (a.dt != kF32 && vec && aligned(a.q)) {
-        // rows of a unit: packed (token, head of the group) rows of the
-        // average sequence
+        // Packed (token, head of the group) rows of the average sequence: the
+        // lengths are on the device.  Measured on GB300 with every path for the
+        // same batches (21 each: 1 to 256 sequences of 64 to 16,000 keys, three
+        // head shapes), the geometric mean of the times over that of the
+        // tcgen05 kernel: 16-row kernel 0.99 at 16 rows (0.27 to 1.84: many short
+        // sequences want it, few long ones do not), 1.20 at 24, 1.42 at 48 and
+        // 1.59 at 64; 64-row kernel 1.41, 1.43, 1.45 and 1.50.  Of these two,
+        // for what tcgen05 does not serve, the first takes 0.70, 0.84, 0.97 and
+        // 1.06 times the second's time.  A batch of sequences of very different
+        // numbers of new tokens still goes one way: 63 decode tokens with a
+        // chunk of 150 are one for the 16-row kernel.
         const int64_t rows = a.tokens * p.G / a.num_seqs;
-        if (rows > 64 && aligned(a.out) && tc_suits(p)) sh = tc_shape(a.head_dim);
-        else sh = mma_shape(rows <= 16 ? kPathFew : kPathMore, a.dt, a.head_dim);
+        if (rows > 16 && aligned(a.out) && tc_suits(p)) sh = tc_shape(a.head_dim);
+        else sh = mma_shape(rows <= 48 ? kPathFew : kPathMore, a.dt, a.head_dim);
     }
     p.min_per = sh.path == kPathFew ? 2 : 1;
     // no more CTAs than there can be pieces: the table's width bounds the tiles

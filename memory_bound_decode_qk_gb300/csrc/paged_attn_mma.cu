@@ -23,9 +23,10 @@
 // three stages hold 96 KB of copies in flight per CTA of 128-channel heads, two
 // CTAs to an SM.
 // attn_more_kernel (64 rows): a warp has 16 rows each and the CTA shares the
-// tiles, so that a key is read once for 64 rows.  For chunks that fill no wide
-// unit and for pages that TMA boxes do not tile; the products of the 64 rows run
-// at about 160 TFLOP/s, which bounds it beyond them.
+// tiles, so that a key is read once for 64 rows.  For chunks over pages that TMA
+// boxes do not tile; the products run at about 160 TFLOP/s, which bounds it (two
+// chunks of 1024 tokens over 16,384 keys in pages of 13 tokens, 32/8 heads of 128:
+// 3.05 ms, where pages of 16 take 0.41 with tcgen05).
 //
 // Both keep the running maximum lazily: the accumulators are rescaled only when
 // a row's maximum grew by more than 2^8, which leaves the weights at most 256

@@ -12,28 +12,29 @@ from test_paged_attention import make, run
 
 gpu = pytest.mark.gpu
 
-# type, heads, head size, new tokens of a sequence: one for each kernel (any type, and odd heads; 16 rows; 64 rows;
-# two query tiles; one query tile)
-PATHS = {"any": ("f32", 8, 2, 128, 3), "odd": ("bf16", 6, 2, 33, 3), "few": ("bf16", 8, 2, 128, 1),
-         "few wide": ("f16", 16, 2, 256, 1), "more": ("bf16", 8, 2, 128, 9), "many": ("bf16", 8, 2, 128, 40),
-         "many wide": ("f16", 8, 2, 256, 40)}
+# type, heads, head size, new tokens of a sequence, tokens of a page: one for each kernel (any type, and odd heads;
+# 16 rows; 64 rows; two query tiles; one query tile)
+PATHS = {"any": ("f32", 8, 2, 128, 3, 16), "odd": ("bf16", 6, 2, 33, 3, 16), "few": ("bf16", 8, 2, 128, 1, 16),
+         "few wide": ("f16", 16, 2, 256, 1, 16), "more": ("bf16", 8, 2, 128, 13, 13),
+         "more wide": ("f16", 8, 2, 256, 20, 12), "many": ("bf16", 8, 2, 128, 40, 16),
+         "many few": ("bf16", 8, 2, 128, 9, 16), "many wide": ("f16", 8, 2, 256, 40, 16)}
 
 
 @gpu
 @pytest.mark.parametrize("keys", [60, 9000])  # within one part of a unit; over many parts
 @pytest.mark.parametrize("path", PATHS)
 def test_nan_in_queries_and_keys(path, keys):
-    dt, hq, hk, D, new = PATHS[path]
+    dt, hq, hk, D, new, page = PATHS[path]
     # the first sequence has NaN in one query row, in the second every key holds NaN, in the third a run of keys that
     # fills parts of its own; the last is clean
-    c = make(dt, hq, hk, D, 16, [(keys, new), (keys, new), (keys, new), (keys - 9, new)], seed=31)
+    c = make(dt, hq, hk, D, page, [(keys, new), (keys, new), (keys, new), (keys - 9, new)], seed=31)
     c["q"][new - 1, :, 0] = math.nan
     for b, first, behind in ((1, 0, keys), (2, keys // 4, keys // 2)):
         for j in range(first, min(behind, keys)):
-            c["k"][int(c["table"][b, j // 16]) * 16 + j % 16, :, 0] = math.nan
+            c["k"][int(c["table"][b, j // page]) * page + j % page, :, 0] = math.nan
     out, lse = run(c)
     torch.cuda.synchronize()
-    ref, tol, rl, lt = paged_ref.attention(c["q"], c["k"], c["v"], c["table"], c["lens"], c["starts"], 16, D ** -0.5)
+    ref, tol, rl, lt = paged_ref.attention(c["q"], c["k"], c["v"], c["table"], c["lens"], c["starts"], page, D ** -0.5)
     gone = torch.isnan(rl)
     assert gone[new - 1:3 * new].all() and not gone[:new - 1].any() and not gone[3 * new:].any()
     assert torch.isnan(out.cpu()[gone]).all(), "a row of NaN scores became finite"

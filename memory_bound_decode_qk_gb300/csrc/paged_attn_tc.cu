@@ -1034,10 +1034,13 @@ AttnShape tc_shape(int head_dim) {
 
 // 16-byte aligned 16-bit tensors of heads of at least 64 channels (a multiple of
 // 8); pages of 8, 16, 32, 64 or a multiple of 128 tokens, so that a ring entry
-// is made of whole boxes of at least one swizzle atom.
+// is made of whole boxes of at least one swizzle atom; at most 4 million sequences,
+// since a walk over empty ones (100 cycles each at most, while other warps of the
+// CTA wait for this one) has to end well within the waits' limit.
+constexpr int kMaxSeqs = 1 << 22;
 bool tc_suits(const AttnP& p) {
     const bool page = p.page_size % kTile == 0 || (p.page_size >= 8 && p.page_size < kTile && kTile % p.page_size == 0);
-    return page && p.D >= 64 && p.num_pages > 0 &&
+    return page && p.D >= 64 && p.num_pages > 0 && p.num_seqs <= kMaxSeqs &&
            (int64_t)p.num_pages * p.page_size <= (int64_t)INT32_MAX - kTile && encoder() != nullptr;
 }
 

@@ -57,3 +57,23 @@ def test_page_moves_behind_32_bits():
     edge_ops.pages_compact(caches, table, refs)
     assert table.tolist() == [[1], [0]] and int(refs.sum()) == 2
     assert torch.equal(k[:page], last) and torch.equal(k[page:2 * page], last)
+
+
+def test_millions_of_empty_sequences():
+    # one wide chunk between millions of sequences without tokens, which every CTA has to pass over
+    B, G, D, n = 2 ** 22 + 5, 16, 64, 4_300_000
+    at = B // 2
+    g = torch.Generator(device="cuda").manual_seed(3)
+    k, v = (torch.randn(16, 1, D, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    q = torch.randn(n, G, D, generator=g, device="cuda", dtype=torch.float16).to(torch.bfloat16)
+    starts = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    starts[at + 1:] = n
+    lens = torch.full((B,), 11, dtype=torch.int32, device="cuda")
+    out = edge_ops.paged_attention(q, k, v, torch.zeros(B, 1, dtype=torch.int32, device="cuda"), lens, page_size=16,
+                                   q_starts=starts, causal=False)
+    rows = torch.randperm(n, generator=torch.Generator().manual_seed(4))[:50].cuda()
+    ref, tol, _, _ = paged_ref.attention(q[rows], k, v, torch.zeros(1, 1, dtype=torch.int32),
+                                         torch.tensor([11], dtype=torch.int32), torch.tensor([0, 50]), 16, D ** -0.5,
+                                         causal=False)
+    paged_ref.check_rows(out[rows], ref, tol, torch.bfloat16)
+    assert torch.isfinite(out.view(-1, D).sum(1, dtype=torch.float32)).all()

@@ -48,12 +48,12 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool ok) 
 // Any type, head size up to 128 NC and alignment.  Eight warps of two rows each;
 // a tile's keys and values are staged as fp32 in shared memory.  Scores: lane =
 // key, so a key's 16 bytes serve two rows.  Values: four channels per lane, two
-// rows per load.  A key of weight zero (masked, or underflowed) is skipped, so
-// what the cache holds there does not matter.  Bound by the latency of a tile's
-// steps at small sizes and by shared-memory reads at large ones (per key and
-// channel quarter of two rows: one 16-byte read for 8 products).  Measured on
-// GB300: five fp32 chunks of 1 to 37 tokens over up to 999 keys, 8/2 heads of 128,
-// 24 us (36 us with four warps of four rows and one stage).
+// rows per load.  A key that a row does not see (its weight is noted as -1) is
+// skipped, so what the cache holds there does not matter.  Bound by the latency
+// of a tile's steps at small sizes and by shared-memory reads at large ones (per
+// key and channel quarter of two rows: one 16-byte read for 8 products).
+// Measured on GB300: five fp32 chunks of 1 to 37 tokens over up to 999 keys, 8/2
+// heads of 128, 24 us (36 us with four warps of four rows and one stage).
 template <typename T, int NC, bool VEC>
 __global__ void __launch_bounds__(kAnyThreads) attn_any_kernel(AttnP p) {
     constexpr int M = kAnyM, KT = kAnyKT, R = kAnyRows, ST = any_stages<T, VEC>();
@@ -198,7 +198,8 @@ __global__ void __launch_bounds__(kAnyThreads) attn_any_kernel(AttnP p) {
             }
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const float x = in && sees(p, at[r], j0 + lane) ? (s[r][0] + s[r][1]) * p.scale_log2 : -INFINITY;
+                const bool seen = in && sees(p, at[r], j0 + lane);
+                const float x = seen ? (s[r][0] + s[r][1]) * p.scale_log2 : -INFINITY;
                 const float top = fmaxf(m[r], group_max<32>(x));
                 const float ref = top == -INFINITY ? 0.0f : top;
                 const float keep = ex2(m[r] - ref);
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(kAnyThreads) attn_any_kernel(AttnP p) {
                     acc[r][i].z *= keep;
                     acc[r][i].w *= keep;
                 }
-                ps[(wid * R + r) * KT + lane] = e;
+                ps[(wid * R + r) * KT + lane] = seen ? e : -1.0f;
             }
             __syncwarp();
 #pragma unroll 2
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(kAnyThreads) attn_any_kernel(AttnP p) {
 #pragma unroll
                     for (int r = 0; r < R; ++r) {
                         const float x = z == 0 ? e[r].x : z == 1 ? e[r].y : z == 2 ? e[r].z : e[r].w;
-                        if (x != 0.0f) {
+                        if (!(x < 0.0f)) {
 #pragma unroll
                             for (int i = 0; i < NC; ++i) {
                                 acc[r][i].x = fmaf(x, vv[i].x, acc[r][i].x);

@@ -179,8 +179,9 @@ __device__ __forceinline__ void soft_tile(float (&s)[NT][4], float (&o)[NO][4], 
 }
 
 // Weights times values for a tile that holds infinities or NaN where some rows
-// are masked: one key at a time, skipping weights of zero, so a masked value
-// leaves no trace.  ps: this warp's [16][KN] floats.
+// are masked: one key at a time, skipping those that a row does not see (their
+// weights are set to -1), so a masked value leaves no trace, and one whose weight
+// underflowed to zero leaves 0 times it.  ps: this warp's [16][KN] floats.
 template <typename T, int DP, int KN, int NT, int NO>
 __device__ void careful_values(const float (&s)[NT][4], float (&o)[NO][4], const char* vt, float* ps,
                                int lane) {
@@ -200,11 +201,11 @@ __device__ void careful_values(const float (&s)[NT][4], float (&o)[NO][4], const
         for (int n = 0; n < NO; ++n) {
             const T* v = reinterpret_cast<const T*>(vt + chunk_at<DP>(j, n)) + q;
             const float a = to_f(v[0]), b = to_f(v[1]);
-            if (w0 != 0.0f) {
+            if (!(w0 < 0.0f)) {
                 o[n][0] = fmaf(w0, a, o[n][0]);
                 o[n][1] = fmaf(w0, b, o[n][1]);
             }
-            if (w1 != 0.0f) {
+            if (!(w1 < 0.0f)) {
                 o[n][2] = fmaf(w1, a, o[n][2]);
                 o[n][3] = fmaf(w1, b, o[n][3]);
             }
@@ -475,9 +476,13 @@ __global__ void __launch_bounds__(kFewWarps * 32, DP <= 128 ? 2 : 1) attn_few_ke
                 odd = __any_sync(0xffffffffu, odd);
             }
             if (odd) {
-                if (half) {
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) s[n][2] = s[n][3] = 0.0f;
+                for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int c = n * 8 + (lane & 3) * 2 + (i & 1);
+                        if ((half && i > 1) || ((dead >> c) & 1u) || !sees(p, at[i >> 1], j0 + c)) s[n][i] = -1.0f;
+                    }
                 }
                 careful_values<T, DP, KT, NT, NO>(s, o, vt, reinterpret_cast<float*>(kt), lane);  // the keys are done with
                 continue;
@@ -669,9 +674,13 @@ __global__ void __launch_bounds__(128, DP <= 128 ? 2 : 1) attn_more_kernel(AttnP
                 if (odd) {
                     float two[2][4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        two[0][i] = s[2 * k][i];
-                        two[1][i] = s[2 * k + 1][i];
+                    for (int n = 0; n < 2; ++n) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int c = (2 * k + n) * 8 + (lane & 3) * 2 + (i & 1);
+                            const bool gone = ((dead >> c) & 1u) || !sees(p, at[i >> 1], j0 + c);
+                            two[n][i] = gone ? -1.0f : s[2 * k + n][i];
+                        }
                     }
                     careful_values<T, DP, 16, 2, NO>(two, o, vt + k * 16 * DP * 2, ps[wid], lane);
                     continue;

@@ -127,3 +127,23 @@ def test_unseen_values_before_many_units_without_an_edge(hq, hk, D):
         out, stats = run(c)
         assert torch.equal(out[~sees], want[~sees]) and torch.equal(stats, lse)
         assert not torch.isfinite(out[sees]).any()
+
+
+@gpu
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("path", PATHS)
+def test_a_value_whose_weight_underflows_is_seen(path, value):
+    # a weight is small, never nothing: e^-500 of an infinity is one, and NaN stays NaN
+    dt, hq, hk, D, new, page = PATHS[path]
+    c = make(dt, hq, hk, D, page, [(200, new), (90, new)], seed=35)
+    c["q"][:] = 1.0
+    for b, j in ((0, 198), (1, 89)):
+        poison(c, b, j, value)
+        poison(c, b, j, -500.0 / D ** 0.5, "k")
+    out, _ = run(c)
+    sees = torch.zeros(2 * new, dtype=torch.bool)
+    sees[max(0, new - 2):new] = True
+    sees[2 * new - 1] = True
+    out = out.cpu()
+    assert not torch.isfinite(out[sees]).any(), "a value that the row sees was passed over"
+    assert torch.isfinite(out[~sees]).all()

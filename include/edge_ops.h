@@ -302,8 +302,9 @@ typedef enum {
  *            axes behind the first to exist: (sections[a] - 1) * axes + a <
  *            rotary_dim / 2.
  * Otherwise the arguments, results and errors of the forms with one position;
- * equal positions on every axis give the same values.  EDGE_ERR_NULL: sections
- * NULL.  EDGE_ERR_SHAPE: axes or sections that do not fit.  EDGE_ERR_VALUE: an
+ * equal positions on every axis give the same values (up to the rounding of the
+ * normalized head, where the two forms take different kernels).  EDGE_ERR_NULL:
+ * sections NULL.  EDGE_ERR_SHAPE: axes or sections that do not fit.  EDGE_ERR_VALUE: an
  * unknown order.
  */
 edge_status edge_qk_norm_rope_axes(void* q_out, void* k_out, edge_dtype out_dt, const void* q,
@@ -347,7 +348,8 @@ edge_status edge_qkv_rope_cache_axes(void* q_out, void* k_cache, void* v_cache, 
  * [0, num_slots / page_size), and, if causal, j <= its position and (window
  * > 0) position - j < window.  What the cache holds at other keys does not
  * matter.  A query that sees no key, or only keys of score -infinity, gives
- * out 0 and lse -infinity.
+ * out 0 and lse -infinity; NaN and infinities in the query and in the keys and
+ * values that it sees reach its row.
  *
  * q:           [tokens, q_heads, head_dim] of dt.
  * k_cache, v_cache: [num_slots, kv_heads, head_dim] of dt (NULL allowed when
@@ -369,7 +371,11 @@ edge_status edge_qkv_rope_cache_axes(void* q_out, void* k_cache, void* v_cache, 
  * weights to dt for the product with the values; with at most 16 packed rows
  * (tokens * q_heads / kv_heads) per sequence on average, sequences of at most 8
  * keep what that rounding leaves over as well.  The output is rounded once.
- * Results are the same from run to run.
+ * Results are the same from run to run.  Waits inside the kernel are limited to
+ * two seconds; should one run out, which correct operation never does, the rows
+ * that it concerns (out and lse) are NaN.
+ * One kernel serves all sequences of a call, chosen by their average number of
+ * rows; a short chunk among many decode tokens does better in a call of its own.
  * EDGE_ERR_SHAPE: q_heads not a multiple of kv_heads, or a workspace that is
  * too small.  EDGE_ERR_UNSUPPORTED: head_dim above 256, or tokens * q_heads or
  * max_pages * page_size above 2^30.
@@ -411,7 +417,9 @@ int64_t edge_paged_attention_workspace(edge_dtype dt, int32_t q_heads, int32_t k
  * edge_pages_copy copies page src[i] to page dst[i] in every cache, for i < n.
  *   Pairs with a page outside the pool, or with src[i] == dst[i], are passed
  *   over.  Of the other pairs with the same destination the last is carried
- *   out, and a pair whose source is the destination of another is not.
+ *   out, and a pair whose source is the destination of another is not.  Pairs
+ *   are held against each other, which takes n^2 steps: calls of some thousand
+ *   pairs each do better than one of many.
  * EDGE_ERR_UNSUPPORTED: n above 65536.
  */
 edge_status edge_pages_copy(void* const* caches, int32_t num_caches, int64_t page_bytes,

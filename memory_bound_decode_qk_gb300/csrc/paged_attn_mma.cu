@@ -15,13 +15,13 @@
 // has no such joins.)
 // Measured on GB300: 64 sequences of 64 to 8192 keys, 32/8 heads of 128, 558 MB
 // in 98 us (5.7 TB/s, 84% of the copy bandwidth); three sequences of 30 to 131
-// thousand keys, 24/4 heads of 256, 967 MB in 165 us (5.85 TB/s); blocks of 16
+// thousand keys, 24/4 heads of 256, 967 MB in 164 us (5.9 TB/s); blocks of 16
 // tokens, 32/32 heads of 128, 248 MB in 55 us (4.5 TB/s).  Up to 8 rows the
 // weights keep two 16-bit parts, the second in the rows that are free: 0.5% and
-// 2% of the time of the first two, and their error against 64 bits falls from
-// 1.35 times that of the output's rounding alone to 1.0.  16 keys a stage and
-// three stages hold 96 KB of copies in flight per CTA of 128-channel heads, two
-// CTAs to an SM.
+// 1 to 2% of the time of the first two, and their error against 64 bits falls
+// from 1.35 times that of the output's rounding alone to 1.0.  16 keys a stage
+// and three stages hold 96 KB of copies in flight per CTA of 128-channel heads,
+// two CTAs to an SM.
 // attn_more_kernel (64 rows): a warp has 16 rows each and the CTA shares the
 // tiles, so that a key is read once for 64 rows.  For chunks over pages that TMA
 // boxes do not tile; the products run at about 160 TFLOP/s, which bounds it (two

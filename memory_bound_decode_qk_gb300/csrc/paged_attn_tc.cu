@@ -21,11 +21,12 @@
 // second product.
 //
 // Measured on GB300: two chunks of 1024 tokens over 16384 keys, 32/8 heads of 128,
-// 533 GFLOP: 339 us as one launch (1570 TFLOP/s, matrix pipe busy 74%), 441 us back
-// to back (1210 TFLOP/s, the clock lowered to about 1.5 GHz under this load).
-// Four prompts of 1201 to 5003 tokens with a window of 1024, 16/8 heads of 256,
-// 213 GFLOP seen: 323 us (660 TFLOP/s), bound by the fetches of key tiles for 128
-// rows only and by shared-memory operands.
+// 533 GFLOP: 334 us as one launch (1595 TFLOP/s, matrix pipe busy 75%), 436 us back
+// to back (1220 TFLOP/s; the power limit lowers the clock, 1.77 GHz in the middle
+// of four seconds of it against 2.07).  Four prompts of 1201 to 5003 tokens with a
+// window of 1024, 16/8 heads of 256, 213 GFLOP seen: 362 us (588 TFLOP/s at 2.07
+// GHz), bound by the fetches of key tiles for 128 rows only and by shared-memory
+// operands.
 //
 // Pages.  The cache is a 3-d tensor (channel, head, slot) to TMA; a page (or 128
 // rows of it) is one box per 64 channels, stored with the 128-byte swizzle.  A

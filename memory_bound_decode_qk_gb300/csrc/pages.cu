@@ -15,6 +15,10 @@
 // Measured on GB300: 1000 pages of 32 KB in 16 caches (1.05 GB read and written)
 // 174 us, 6.0 TB/s, 89% of the copy bandwidth; compaction of a pool of 4096 such
 // pages (0.77 GB moved) 130 us, 5.9 TB/s.
+// A caller's list of pairs is checked where it is carried out, each pair against
+// all others for every 16 KB that a CTA takes.  That hides up to about a thousand
+// pairs and is the bound beyond: pages of 2 KB in 4 caches, 1000 pairs 10 us,
+// 10,000 293 us, 65,536 11.9 ms.
 // The bookkeeping is integer work on a few KB: one CTA decides it (so that
 // results do not depend on any order of atomics), and the copies follow as a
 // dependent launch that reads the pairs it wrote.

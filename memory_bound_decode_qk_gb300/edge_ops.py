@@ -229,6 +229,8 @@ _AXIS_ORDER = {"blocks": AXES_BLOCKS, "cycled": AXES_CYCLED}
 
 @functools.lru_cache(maxsize=256)
 def _section_array(sections):
+    if any(not -2 ** 31 <= n < 2 ** 31 for n in sections):
+        raise ValueError(f"sections must be 32-bit numbers, not {sections}")
     return (ctypes.c_int32 * max(1, len(sections)))(*sections)
 
 

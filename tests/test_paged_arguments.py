@@ -1,4 +1,5 @@
-"""The stream argument of the paged-cache calls: one of another device than the tensors' is refused."""
+"""Arguments that the binding of the paged-cache calls refuses: a stream of another device than the tensors', and
+sections that no 32-bit number holds."""
 import pytest
 import torch
 
@@ -31,3 +32,10 @@ def test_calls_refuse_a_stream_of_another_device():
         with pytest.raises(ValueError, match="cuda:63"):
             call(Elsewhere())
     assert lens.tolist() == [1, 1] and refs.tolist() == [1] * 4
+
+
+@pytest.mark.parametrize("sections", [(2 ** 32 + 8, 12, 12), (8, 12, 12 - 2 ** 32)])
+def test_sections_past_32_bits_are_refused(sections):
+    # as 32-bit numbers they would be 8, 12 and 12
+    with pytest.raises(ValueError, match="sections"):
+        edge_ops._axis_args(sections, "blocks", None, 4)

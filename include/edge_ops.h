@@ -14,6 +14,9 @@
  *   edge_paged_attention   attention of new tokens over the cache's pages
  *   edge_*_axes            rotary positions with several axes
  *   edge_pages_*           copying, freeing, forking and compacting pages
+ * And linear layers in 8 bits with a scale for each token and output channel:
+ *   edge_*_q8              norm, gate and quantization that find the scale of
+ *                          each row, and the matrix product that reads them
  *
  * Sources, by page and section:
  *   "thox-edge-ops v2: fused decode kernels for small models on THOX edge
@@ -68,7 +71,8 @@ typedef enum {
     EDGE_F32 = 0,
     EDGE_F16 = 1,
     EDGE_BF16 = 2,
-    EDGE_FP8_E4M3 = 3 /* output only: OCP E4M3 "fn", saturating */
+    EDGE_FP8_E4M3 = 3, /* 8-bit results and operands: OCP E4M3 "fn", saturating */
+    EDGE_INT8 = 4      /* 8-bit results and operands of the edge_*_q8 calls */
 } edge_dtype;
 
 typedef enum {
@@ -471,6 +475,68 @@ edge_status edge_pages_compact(void* const* caches, int32_t num_caches, int64_t 
                                int32_t* refs_out, const int32_t* refs, void* workspace,
                                int64_t workspace_bytes, void* stream);
 int64_t edge_pages_compact_workspace(int32_t num_pages);
+
+/*
+ * Rows in 8 bits with a scale for each row (token), found from the row itself: the
+ * inputs of edge_matmul_q8.  code[t, i] * scales[t] stands for the value.
+ *
+ *   edge_rmsnorm_q8, edge_add_rmsnorm_q8:  p_i = s_i (w[i] + weight_offset), s = x or
+ *       the rounded sum x + residual, which replaces residual
+ *   edge_glu_act_q8:   p_i = act(gate_up[t, i]) * gate_up[t, n + i]
+ *   edge_quantize_q8:  p_i = x[t, i]
+ *   m = max_i |p_i|,  Q = 127 (EDGE_INT8) or 448 (EDGE_FP8_E4M3),
+ *   code_i = round(p_i * inv) to nearest even,  inv = min(Q / m, 2^126)  (for E4M3
+ *       the product is rounded to fp32 first, for int8 it is not),
+ *   scales[t] = step, or r_t * step for the norms (r_t as in edge_rmsnorm),
+ *   step = max(m / Q, 2^-126),
+ * all in fp32, the divisions IEEE.  The factor r_t of the norm is common to the
+ * row, so it enters the scale alone; int8 codes lie in -127 .. 127.
+ * A row with a NaN or an infinity among its products has a scale that is NaN or
+ * infinite (the norms: NaN), and codes without a meaning.
+ *
+ * out:    [rows, n] bytes of q_dt (EDGE_INT8 or EDGE_FP8_E4M3).
+ * scales: [rows] fp32.
+ * The other arguments and the errors as in edge_rmsnorm, edge_add_rmsnorm,
+ * edge_glu_act and edge_quantize_fp8; out and scales must not overlap each other
+ * or any other buffer.  EDGE_ERR_UNSUPPORTED: n above 2^24.
+ */
+edge_status edge_rmsnorm_q8(void* out, edge_dtype q_dt, float* scales, const void* x,
+                            const void* w, edge_dtype dt, int64_t rows, int64_t n, float eps,
+                            int weight_offset, void* stream);
+edge_status edge_add_rmsnorm_q8(void* out, edge_dtype q_dt, float* scales, const void* x,
+                                void* residual, const void* w, edge_dtype dt, int64_t rows,
+                                int64_t n, float eps, int weight_offset, void* stream);
+edge_status edge_glu_act_q8(void* out, edge_dtype q_dt, float* scales, const void* gate_up,
+                            edge_dtype dt, int64_t rows, int64_t n, edge_act act, void* stream);
+edge_status edge_quantize_q8(void* out, edge_dtype q_dt, float* scales, const void* x,
+                             edge_dtype dt, int64_t rows, int64_t n, void* stream);
+
+/*
+ * Matrix product of 8-bit operands with a scale for each token and each output
+ * channel (the reader of the calls above).
+ *
+ *   out[t, j] = round((sum_i a[t, i] w[j, i]) * a_scales[t] * w_scales[j] + bias[j])
+ *
+ * a:        [tokens, k] of q_dt (EDGE_INT8 or EDGE_FP8_E4M3).
+ * w:        [n, k] of q_dt, a row for each output channel.
+ * a_scales: [tokens] fp32.   w_scales: [n] fp32.
+ * bias:     [n] of out_dt, or NULL.
+ * out:      [tokens, n] of out_dt (EDGE_F32, EDGE_F16 or EDGE_BF16); it must not
+ *           overlap any other buffer.
+ * int8 sums are exact (every int8 value is allowed, -128 too).  E4M3 sums are
+ * held in fp32; a NaN code makes the sums it enters NaN.  The sum, rounded to fp32, is multiplied by
+ * a_scales[t], then by w_scales[j], and the bias is added, in fp32; then the
+ * output is rounded once.  Results are the same from run to run.
+ * Operands with k a multiple of 16 whose addresses are multiples of 16 take the
+ * tensor-memory and streaming paths; others a slower one.  Waits inside the kernel
+ * are limited to two seconds; should one run out, which correct operation never
+ * does, the outputs that it concerns are NaN.
+ * EDGE_ERR_SHAPE: tokens < 0, n or k < 1.  EDGE_ERR_UNSUPPORTED: k above 131,071
+ * (the largest whose int8 sums fit 32 bits), or tokens or n above 2^24.
+ */
+edge_status edge_matmul_q8(void* out, edge_dtype out_dt, const void* a, const void* w,
+                           edge_dtype q_dt, const float* a_scales, const float* w_scales,
+                           const void* bias, int64_t tokens, int64_t n, int64_t k, void* stream);
 
 /*
  * Plain device copy of `bytes` bytes from src to dst, in the launch form of the

@@ -105,7 +105,9 @@ thread_local int g_last_cuda_error = 0;
 
 bool act_dtype(edge_dtype dt) { return dt == EDGE_F32 || dt == EDGE_F16 || dt == EDGE_BF16; }
 
-int64_t esize(edge_dtype dt) { return dt == EDGE_F32 ? 4 : (dt == EDGE_FP8_E4M3 ? 1 : 2); }
+bool q8_dtype(edge_dtype dt) { return dt == EDGE_INT8 || dt == EDGE_FP8_E4M3; }
+
+int64_t esize(edge_dtype dt) { return dt == EDGE_F32 ? 4 : (q8_dtype(dt) ? 1 : 2); }
 
 bool aligned(const void* p, int64_t n) {
     return p == nullptr || (reinterpret_cast<uintptr_t>(p) % (uintptr_t)n) == 0;
@@ -204,6 +206,52 @@ edge_status rows_entry(void* out, edge_dtype out_dt, const void* x, void* residu
     a.inv_scale = inv_scale;
     a.weight_offset = weight_offset;
     return finish(edge::launch_rows(a, static_cast<cudaStream_t>(stream)));
+}
+
+// Rows in 8 bits with a scale each.  act: -1 without a gate.
+edge_status rows_q8_entry(void* out, edge_dtype q_dt, float* scales, const void* x, void* residual,
+                          bool fused, const void* w, bool norm, edge_dtype dt, int64_t rows,
+                          int64_t n, float eps, int weight_offset, int act, void* stream) {
+    if (!act_dtype(dt) || !q8_dtype(q_dt)) return EDGE_ERR_DTYPE;
+    if (x == nullptr || out == nullptr || scales == nullptr || (fused && residual == nullptr)) {
+        return EDGE_ERR_NULL;
+    }
+    if (rows < 0 || n <= 0) return EDGE_ERR_SHAPE;
+    if (!finite_nonneg(eps) || (weight_offset != 0 && weight_offset != 1)) return EDGE_ERR_VALUE;
+    const int64_t es = esize(dt);
+    int64_t in_bytes = 0, out_bytes = 0, scale_bytes = 0;
+    if (!checked_bytes(rows, n, es * (act >= 0 ? 2 : 1), &in_bytes) ||
+        !checked_bytes(rows, n, 1, &out_bytes) || !checked_bytes(rows, 1, 4, &scale_bytes)) {
+        return EDGE_ERR_SHAPE;
+    }
+    if (n > edge::kMaxHidden) return EDGE_ERR_UNSUPPORTED;
+    if (!aligned(x, es) || !aligned(residual, es) || !aligned(w, es) || !aligned(scales, 4)) {
+        return EDGE_ERR_ALIGN;
+    }
+    const Span so = span(out, out_bytes), ss = span(scales, scale_bytes), sx = span(x, in_bytes);
+    const Span sw = span(w, n * es), sr = span(fused ? residual : nullptr, in_bytes);
+    if (overlap(so, ss)) return EDGE_ERR_ALIAS;
+    for (const Span& written : {so, ss}) {
+        if (overlap(written, sx) || overlap(written, sw) || overlap(written, sr)) return EDGE_ERR_ALIAS;
+    }
+    if (fused && (overlap(sr, sx) || overlap(sr, sw))) return EDGE_ERR_ALIAS;
+    if (rows == 0) return EDGE_OK;
+
+    edge::RowsQ8Args a;
+    a.x = x;
+    a.residual = fused ? residual : nullptr;
+    a.w = w;
+    a.out = out;
+    a.scales = scales;
+    a.rows = rows;
+    a.n = n;
+    a.dt = (int)dt;
+    a.out_dt = (int)q_dt;
+    a.norm = norm ? 1 : 0;
+    a.act = act;
+    a.eps = eps;
+    a.weight_offset = weight_offset;
+    return finish(edge::launch_rows_q8(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace
@@ -858,6 +906,73 @@ edge_status edge_pages_compact(void* const* caches, int32_t num_caches, int64_t 
     const edge::PageRows rows{const_cast<int32_t*>(block_table), nullptr, num_seqs, max_pages};
     return finish(edge::launch_pages_compact(pool, block_table_out, rows, refs_out, refs, workspace,
                                              static_cast<cudaStream_t>(stream)));
+}
+
+edge_status edge_rmsnorm_q8(void* out, edge_dtype q_dt, float* scales, const void* x,
+                            const void* w, edge_dtype dt, int64_t rows, int64_t n, float eps,
+                            int weight_offset, void* stream) {
+    return rows_q8_entry(out, q_dt, scales, x, nullptr, false, w, true, dt, rows, n, eps,
+                         weight_offset, -1, stream);
+}
+
+edge_status edge_add_rmsnorm_q8(void* out, edge_dtype q_dt, float* scales, const void* x,
+                                void* residual, const void* w, edge_dtype dt, int64_t rows,
+                                int64_t n, float eps, int weight_offset, void* stream) {
+    return rows_q8_entry(out, q_dt, scales, x, residual, true, w, true, dt, rows, n, eps,
+                         weight_offset, -1, stream);
+}
+
+edge_status edge_glu_act_q8(void* out, edge_dtype q_dt, float* scales, const void* gate_up,
+                            edge_dtype dt, int64_t rows, int64_t n, edge_act act, void* stream) {
+    if (act != EDGE_ACT_SILU && act != EDGE_ACT_GELU_TANH) return EDGE_ERR_VALUE;
+    return rows_q8_entry(out, q_dt, scales, gate_up, nullptr, false, nullptr, false, dt, rows, n,
+                         0.0f, 0, (int)act, stream);
+}
+
+edge_status edge_quantize_q8(void* out, edge_dtype q_dt, float* scales, const void* x,
+                             edge_dtype dt, int64_t rows, int64_t n, void* stream) {
+    return rows_q8_entry(out, q_dt, scales, x, nullptr, false, nullptr, false, dt, rows, n, 0.0f,
+                         0, -1, stream);
+}
+
+edge_status edge_matmul_q8(void* out, edge_dtype out_dt, const void* a, const void* w,
+                           edge_dtype q_dt, const float* a_scales, const float* w_scales,
+                           const void* bias, int64_t tokens, int64_t n, int64_t k, void* stream) {
+    if (!act_dtype(out_dt) || !q8_dtype(q_dt)) return EDGE_ERR_DTYPE;
+    if (out == nullptr || a == nullptr || w == nullptr || a_scales == nullptr ||
+        w_scales == nullptr) {
+        return EDGE_ERR_NULL;
+    }
+    if (tokens < 0 || n < 1 || k < 1) return EDGE_ERR_SHAPE;
+    if (k > edge::kMaxMatmulK || tokens > edge::kMaxMatmulRows || n > edge::kMaxMatmulRows) {
+        return EDGE_ERR_UNSUPPORTED;
+    }
+    const int64_t es = esize(out_dt);
+    if (!aligned(out, es) || !aligned(bias, es) || !aligned(a_scales, 4) || !aligned(w_scales, 4)) {
+        return EDGE_ERR_ALIGN;
+    }
+    // (at most 2^24 rows of 2^24 elements of 4 bytes: no overflow)
+    const Span so = span(out, tokens * n * es);
+    if (overlap(so, span(a, tokens * k)) || overlap(so, span(w, n * k)) ||
+        overlap(so, span(a_scales, 4 * tokens)) || overlap(so, span(w_scales, 4 * n)) ||
+        overlap(so, span(bias, n * es))) {
+        return EDGE_ERR_ALIAS;
+    }
+    if (tokens == 0) return EDGE_OK;
+
+    edge::MatmulQ8Args m;
+    m.a = a;
+    m.w = w;
+    m.a_scales = a_scales;
+    m.w_scales = w_scales;
+    m.bias = bias;
+    m.out = out;
+    m.tokens = tokens;
+    m.n = n;
+    m.k = k;
+    m.q_dt = (int)q_dt;
+    m.out_dt = (int)out_dt;
+    return finish(edge::launch_matmul_q8(m, static_cast<cudaStream_t>(stream)));
 }
 
 edge_status edge_copy(void* dst, const void* src, int64_t bytes, void* stream) {

@@ -8,7 +8,7 @@
 
 namespace edge {
 
-enum Dt { kF32 = 0, kF16 = 1, kBF16 = 2, kFP8 = 3 };
+enum Dt { kF32 = 0, kF16 = 1, kBF16 = 2, kFP8 = 3, kInt8 = 4 };
 
 // Rotary positions with several axes: pair j of the rotary channels turns by
 // the position of its axis.  n = 0: one position per token.
@@ -98,6 +98,37 @@ struct QuantArgs {
     float inv_scale;
 };
 cudaError_t launch_quant(const QuantArgs& a, cudaStream_t s);
+
+// Rows in 8 bits with a scale each (rows_q8.cu).
+struct RowsQ8Args {
+    const void* x;           // the gate: [rows, 2 n]
+    void* residual;          // nullptr: no residual
+    const void* w;           // norms, nullable
+    void* out;
+    float* scales;
+    int64_t rows, n;
+    int dt, out_dt;
+    int norm;                // 1: RMSNorm
+    int act;                 // -1: no gate
+    float eps;
+    int weight_offset;
+};
+cudaError_t launch_rows_q8(const RowsQ8Args& a, cudaStream_t s);
+
+// Product of 8-bit operands with scales (matmul_q8.cu).
+struct MatmulQ8Args {
+    const void* a;
+    const void* w;
+    const float* a_scales;
+    const float* w_scales;
+    const void* bias;        // nullable
+    void* out;
+    int64_t tokens, n, k;
+    int q_dt, out_dt;
+};
+constexpr int64_t kMaxMatmulK = 131071;   // int8 sums stay below 2^31
+constexpr int64_t kMaxMatmulRows = int64_t(1) << 24;  // tokens, n
+cudaError_t launch_matmul_q8(const MatmulQ8Args& a, cudaStream_t s);
 
 // Attention over a paged KV cache (paged_attn.cu).
 struct AttnArgs {

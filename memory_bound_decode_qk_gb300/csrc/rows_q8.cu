@@ -1,0 +1,394 @@
+// rows_q8.cu -- rows in 8 bits with a scale for each row: RMSNorm with or without
+// the residual's addition, gated activation, and quantization alone (sm_103a).
+//
+// What they compute.  Every row has products p_i:
+//   norm       p_i = s_i (w_i + delta), s = x or round_dt(x + residual)
+//   gate       p_i = act(g_i) u_i
+//   quantize   p_i = x_i
+// and from m = max |p_i|, with Q = 127 (int8) or 448 (E4M3),
+//   code_i = rne(p_i * inv),  inv = min(Q / m, 2^126)  (E4M3: of the product in fp32),
+//   scale  = step (gate, quantize) or r * step (norm),  step = max(m / Q, 2^-126),
+// so that code_i * scale stands for the row's value.  The norm's factor
+// r = 1 / sqrt(mean(s^2) + eps) is common to a row: it leaves the codes as they are
+// and enters the scale alone.  So one reduction (the sum of squares and the
+// maximum together) is enough where norm-then-quantize would take two, and the
+// codes do not depend on the order of any sum.  The bound on the step keeps inv
+// finite: rows whose largest product is below Q 2^-126 (an empty row among them)
+// lose relative precision instead of dividing by zero.
+//
+// NaN and infinities.  The maximum is taken so that NaN stays NaN, so the scale of
+// a row that holds one is NaN or infinite and the row, multiplied back, is NaN
+// wherever its codes are zero.  The codes of such a row mean nothing.
+//
+// GB300 design.  2 (bf16, fp16) to 4 bytes read per element and input, one
+// written: the kernels are bound by HBM, and at few rows by one memory round trip.
+// As in rows.cu a row stays in registers from its load to its store: a CTA is
+// (32 W) x R threads, W warps share a row and every load of a thread is issued
+// before any arithmetic.  The norm forms its products twice (once for the maximum,
+// once for the codes) rather than hold them; the gate holds them in fp32, since
+// its exponentials cost more than the registers.  Rows longer than a CTA holds, or
+// of a length or alignment that 16-byte vectors do not suit, take a two-pass
+// kernel of one CTA per row.
+#include "edge_common.cuh"
+#include "glu_math.cuh"
+#include "launch.h"
+
+namespace edge {
+namespace {
+
+enum RowKind { kQuant = 0, kNorm = 1, kAddNorm = 2, kGateSilu = 3, kGateGelu = 4 };
+
+template <int KIND> constexpr bool kIsNorm = KIND == kNorm || KIND == kAddNorm;
+template <int KIND> constexpr bool kIsGate = KIND == kGateSilu || KIND == kGateGelu;
+
+struct RowsQ8P {
+    const char* x;      // the gate: rows of [gate | up]
+    char* res;
+    const char* w;      // nullable
+    char* out;
+    float* scales;
+    int64_t rows;
+    int n;              // codes per row
+    int nvec;           // 16-byte vectors of them
+    int fp8;
+    float eps, delta, inv_n;
+};
+
+// ---------------------------------------------------------------- maximum and codes
+
+// max(a, |b|) in which NaN stays NaN.
+__device__ __forceinline__ float max_abs(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(fabsf(b)));
+    return y;
+}
+// The maximum of a warp's values, none negative (NaN above all): their bits are
+// ordered as they are.
+__device__ __forceinline__ float warp_max(float v) {
+    uint32_t y;
+    asm volatile("redux.sync.max.u32 %0, %1, 0xffffffff;" : "=r"(y) : "r"(__float_as_uint(v)));
+    return __uint_as_float(y);
+}
+
+constexpr float kStepFloor = 1.1754943508222875e-38f;  // 2^-126
+constexpr float kInvCeiling = 8.507059173023462e37f;   // 2^126
+
+struct Steps {
+    float inv, step;
+};
+// Both quotients are IEEE divisions: a plain evaluation of the formulas gives the
+// same codes.
+__device__ __forceinline__ Steps steps_of(float most, int fp8) {
+    const float top = fp8 ? 448.0f : 127.0f;
+    Steps s;
+    s.inv = fminf(__fdiv_rn(top, most), kInvCeiling);
+    s.step = __fdiv_rn(most, top);
+    if (s.step < kStepFloor) s.step = kStepFloor;  // (NaN stays)
+    return s;
+}
+
+// Four int8 codes of y * inv (at most 127 and a little in size): adding 1.5 * 2^23 in
+// one fused operation rounds the unrounded product to the nearest even integer and
+// leaves it in the low bits.
+__device__ __forceinline__ uint32_t int8x4(float2 a, float2 b, float inv) {
+    const float2 magic = splat2(12582912.0f);
+    a = __ffma2_rn(a, splat2(inv), magic);
+    b = __ffma2_rn(b, splat2(inv), magic);
+    const uint32_t lo = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040);
+    const uint32_t hi = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040);
+    return __byte_perm(lo, hi, 0x5410);
+}
+
+template <int N>
+__device__ __forceinline__ typename Fp8Pack<N>::type codes_of(const float2 (&y)[N / 2], float inv, int fp8) {
+    if (fp8) return quantize_pairs<N>(y, inv);
+    uint32_t w[N / 4];
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+        w[i] = int8x4(y[2 * i], y[2 * i + 1], inv);
+    }
+    if constexpr (N == 4) {
+        return w[0];
+    } else {
+        return make_uint2(w[0], w[1]);
+    }
+}
+__device__ __forceinline__ uint8_t code_of(float y, float inv, int fp8) {
+    if (fp8) return quantize1(y, inv);
+    return (uint8_t)(int8x4(make_float2(y, 0.0f), splat2(0.0f), inv) & 0xFFu);
+}
+
+// ---------------------------------------------------------------- rows in registers
+
+template <typename T, int KIND, int V>
+__global__ void __launch_bounds__(512) rows_q8_kernel(RowsQ8P p) {
+    constexpr int N = vec_elems<T>();
+    constexpr int P = N / 2;
+    constexpr bool NORM = kIsNorm<KIND>, ADD = KIND == kAddNorm, GATE = kIsGate<KIND>;
+    __shared__ float2 red[16];
+    const int tid = threadIdx.x, tpr = blockDim.x;
+    const int64_t row0 = (int64_t)blockIdx.x * blockDim.y;
+    const int64_t row = row0 + threadIdx.y;
+    const bool active = row < p.rows;
+    const int64_t in_row = (int64_t)p.nvec * (GATE ? 32 : 16);
+
+    if (tid == 0 && threadIdx.y == 0) {
+        // this CTA's rows into L2 while the preceding grid drains
+        const int64_t r1 = row0 + blockDim.y < p.rows ? row0 + blockDim.y : p.rows;
+        prefetch_l2(p.x, row0 * in_row, r1 * in_row);
+        if (ADD) prefetch_l2(p.res, row0 * in_row, r1 * in_row);
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+
+    const int64_t rsafe = active ? row : row0;
+    const uint4* xr = reinterpret_cast<const uint4*>(p.x + rsafe * in_row);
+    uint4* rr = ADD ? reinterpret_cast<uint4*>(p.res + rsafe * in_row) : nullptr;
+    const uint4* wv = NORM ? reinterpret_cast<const uint4*>(p.w) : nullptr;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    // xv: the row, or its gate half; yv: the residual, the weight's place is wr, or
+    // the up half
+    uint4 xv[V], yv[ADD || GATE ? V : 1], wr[NORM ? V : 1];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int idx = tid + i * tpr;
+        const bool ok = active && idx < p.nvec;
+        xv[i] = ok ? __ldcs(xr + idx) : zero;
+        if constexpr (ADD) yv[i] = ok ? __ldcs(rr + idx) : zero;
+        if constexpr (GATE) yv[i] = ok ? __ldcs(xr + p.nvec + idx) : zero;
+        if constexpr (NORM) wr[i] = ok && wv != nullptr ? __ldg(wv + idx) : zero;
+    }
+
+    // products of vector i (the norm's sums, or the gate's values where they are held)
+    float2 held[GATE ? V : 1][P];
+    const float2 delta = splat2(p.delta);
+    auto products = [&](int i, float2 (&y)[P]) {
+        if constexpr (GATE) {
+#pragma unroll
+            for (int j = 0; j < P; ++j) y[j] = held[i][j];
+        } else {
+            unpack_pairs<T, N>(xv[i], y);
+            if constexpr (NORM) {
+                if (wv != nullptr) {
+                    float2 w[P];
+                    unpack_pairs<T, N>(wr[i], w);
+#pragma unroll
+                    for (int j = 0; j < P; ++j) y[j] = __fmul2_rn(y[j], __fadd2_rn(w[j], delta));
+                }
+            }
+        }
+    };
+
+    // the sum of squares runs in the two lanes of a pair, and beyond 32 terms per
+    // thread in two pairs alternating by vector
+    constexpr bool kSplit = V * N > 32;
+    float2 ss[2] = {splat2(0.0f), splat2(0.0f)};
+    float2 most = splat2(0.0f);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        float2 a[P];
+        if constexpr (ADD) {
+            // eager semantics: widen, add in fp32, round once to the dtype
+            float2 b[P];
+            unpack_pairs<T, N>(xv[i], a);
+            unpack_pairs<T, N>(yv[i], b);
+#pragma unroll
+            for (int j = 0; j < P; ++j) a[j] = __fadd2_rn(a[j], b[j]);
+            xv[i] = pack_pairs<T, N>(a);
+            const int idx = tid + i * tpr;
+            if (active && idx < p.nvec) rr[idx] = xv[i];
+        }
+        if constexpr (NORM) {
+            unpack_pairs<T, N>(xv[i], a);
+#pragma unroll
+            for (int j = 0; j < P; ++j) ss[kSplit ? (i & 1) : 0] = __ffma2_rn(a[j], a[j], ss[kSplit ? (i & 1) : 0]);
+        }
+        if constexpr (GATE) {
+            float2 u[P];
+            unpack_pairs<T, N>(xv[i], a);
+            unpack_pairs<T, N>(yv[i], u);
+#pragma unroll
+            for (int j = 0; j < P; ++j) held[i][j] = gate_fast2<KIND == kGateSilu ? kSilu : kGelu>(a[j], u[j]);
+        }
+        products(i, a);
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            most.x = max_abs(most.x, a[j].x);
+            most.y = max_abs(most.y, a[j].y);
+        }
+    }
+    // over the warps that share the row: sum and maximum with one barrier
+    float sum = 0.0f;
+    if constexpr (NORM) {
+        const float2 s2 = kSplit ? __fadd2_rn(ss[0], ss[1]) : ss[0];
+        sum = group_sum<32>(__fadd_rn(s2.x, s2.y));
+    }
+    float top = warp_max(max_abs(most.x, most.y));
+    const int W = tpr >> 5;
+    if ((tid & 31) == 0) red[(threadIdx.y * tpr + tid) >> 5] = make_float2(sum, top);
+    __syncthreads();
+    sum = top = 0.0f;
+    for (int k = 0; k < W; ++k) {
+        const float2 v = red[threadIdx.y * W + k];
+        if constexpr (NORM) sum = __fadd_rn(sum, v.x);
+        top = max_abs(top, v.y);
+    }
+    const Steps st = steps_of(top, p.fp8);
+    if (tid == 0 && active) {
+        p.scales[row] = NORM ? __fmul_rn(inv_rms(sum, p.inv_n, p.eps), st.step) : st.step;
+    }
+
+    char* orow = p.out + rsafe * p.n;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int idx = tid + i * tpr;
+        if (!(active && idx < p.nvec)) continue;
+        float2 y[P];
+        products(i, y);
+        auto c = codes_of<N>(y, st.inv, p.fp8);
+        reinterpret_cast<decltype(c)*>(orow)[idx] = c;
+    }
+}
+
+// ---------------------------------------------------------------- any row
+
+// Any length and alignment: one CTA per row, two passes (the second hits L1/L2).
+// The sum of squares is accumulated in fp64, as in the scalar RMSNorm kernel: a
+// thread sums up to 65,536 terms here.
+template <typename T, int KIND>
+__global__ void __launch_bounds__(256) rows_q8_any_kernel(RowsQ8P p) {
+    constexpr bool NORM = kIsNorm<KIND>, ADD = KIND == kAddNorm, GATE = kIsGate<KIND>;
+    __shared__ double red[8];
+    __shared__ float red_top[8];
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nw = blockDim.x >> 5;
+
+    pdl_wait();
+    pdl_launch_dependents();
+
+    const T* w = reinterpret_cast<const T*>(p.w);
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        const T* x = reinterpret_cast<const T*>(p.x) + row * p.n * (GATE ? 2 : 1);
+        T* res = ADD ? reinterpret_cast<T*>(p.res) + row * p.n : nullptr;
+        // s: the value that the norm squares
+        auto product = [&](int i, float s) {
+            if constexpr (GATE) {
+                return gate_fast<KIND == kGateSilu ? kSilu : kGelu>(s, to_f(x[(int64_t)p.n + i]));
+            } else if constexpr (NORM) {
+                return w != nullptr ? __fmul_rn(s, __fadd_rn(to_f(w[i]), p.delta)) : s;
+            } else {
+                return s;
+            }
+        };
+        double ss = 0.0;
+        float top = 0.0f;
+        for (int i = threadIdx.x; i < p.n; i += blockDim.x) {
+            float a = to_f(x[i]);
+            if constexpr (ADD) {
+                a = round_to<T>(__fadd_rn(a, to_f(res[i])));
+                res[i] = from_f<T>(a);
+            }
+            if constexpr (NORM) ss = __fma_rn((double)a, (double)a, ss);
+            top = max_abs(top, product(i, a));
+        }
+        if constexpr (NORM) ss = group_sum<32>(ss);
+        top = warp_max(top);
+        if (lane == 0) {
+            red[wid] = ss;
+            red_top[wid] = top;
+        }
+        __syncthreads();
+        ss = 0.0;
+        top = 0.0f;
+        for (int k = 0; k < nw; ++k) {
+            ss = __dadd_rn(ss, red[k]);
+            top = max_abs(top, red_top[k]);
+        }
+        __syncthreads();
+        const Steps st = steps_of(top, p.fp8);
+        if (threadIdx.x == 0) {
+            p.scales[row] = NORM ? __fmul_rn(inv_rms((float)ss, p.inv_n, p.eps), st.step) : st.step;
+        }
+        uint8_t* out = reinterpret_cast<uint8_t*>(p.out) + row * p.n;
+        for (int i = threadIdx.x; i < p.n; i += blockDim.x) {
+            out[i] = code_of(product(i, ADD ? to_f(res[i]) : to_f(x[i])), st.inv, p.fp8);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- launch
+
+template <typename T, int KIND>
+cudaError_t launch_kind(const RowsQ8Args& a, RowsQ8P& p, cudaStream_t s) {
+    constexpr int N = vec_elems<T>();
+    const int sms = sm_count();
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 1 : 0;
+
+    auto aligned = [](const void* ptr, uintptr_t n) { return (reinterpret_cast<uintptr_t>(ptr) % n) == 0; };
+    const int64_t nvec = a.n / N;
+    const bool vec = a.n % N == 0 && aligned(a.x, 16) && aligned(a.residual, 16) && aligned(a.w, 16) &&
+                     aligned(a.out, N) && nvec <= 16 * 32 * 8;
+    if (vec) {
+        const int vt = a.rows >= 2 * sms ? 2 : 1;
+        int W = (int)((nvec + 32 * vt - 1) / (32 * vt));
+        if (W > 16) W = 16;
+        const int64_t per = (nvec + 32 * W - 1) / (32 * W);
+        const int R = 256 / (32 * W) > 1 ? 256 / (32 * W) : 1;
+        const int64_t blocks = (a.rows + R - 1) / R;
+        if (blocks <= (int64_t)INT32_MAX) {
+            p.nvec = (int)nvec;
+            cfg.gridDim = dim3((unsigned)blocks);
+            cfg.blockDim = dim3(32 * W, R);
+            switch (per <= 1 ? 1 : per <= 2 ? 2 : per <= 4 ? 4 : 8) {
+                case 1: return cudaLaunchKernelEx(&cfg, rows_q8_kernel<T, KIND, 1>, p);
+                case 2: return cudaLaunchKernelEx(&cfg, rows_q8_kernel<T, KIND, 2>, p);
+                case 4: return cudaLaunchKernelEx(&cfg, rows_q8_kernel<T, KIND, 4>, p);
+                default: return cudaLaunchKernelEx(&cfg, rows_q8_kernel<T, KIND, 8>, p);
+            }
+        }
+    }
+    int64_t blocks = a.rows;
+    const int64_t cap = (int64_t)sms * 16;
+    if (blocks > cap) blocks = cap;
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(256);
+    return cudaLaunchKernelEx(&cfg, rows_q8_any_kernel<T, KIND>, p);
+}
+
+template <typename T>
+cudaError_t launch_dt(const RowsQ8Args& a, RowsQ8P& p, cudaStream_t s) {
+    if (a.act == kSilu) return launch_kind<T, kGateSilu>(a, p, s);
+    if (a.act == kGelu) return launch_kind<T, kGateGelu>(a, p, s);
+    if (a.residual != nullptr) return launch_kind<T, kAddNorm>(a, p, s);
+    return a.norm ? launch_kind<T, kNorm>(a, p, s) : launch_kind<T, kQuant>(a, p, s);
+}
+
+}  // namespace
+
+cudaError_t launch_rows_q8(const RowsQ8Args& a, cudaStream_t s) {
+    RowsQ8P p;
+    p.x = static_cast<const char*>(a.x);
+    p.res = static_cast<char*>(a.residual);
+    p.w = static_cast<const char*>(a.w);
+    p.out = static_cast<char*>(a.out);
+    p.scales = a.scales;
+    p.rows = a.rows;
+    p.n = (int)a.n;
+    p.nvec = 0;
+    p.fp8 = a.out_dt == kFP8;
+    p.eps = a.eps;
+    p.delta = (float)a.weight_offset;
+    p.inv_n = 1.0f / (float)a.n;
+    switch (a.dt) {
+        case kF32: return launch_dt<float>(a, p, s);
+        case kF16: return launch_dt<__half>(a, p, s);
+        default: return launch_dt<__nv_bfloat16>(a, p, s);
+    }
+}
+
+}  // namespace edge

@@ -16,7 +16,7 @@ import torch
 
 from . import _build
 
-F32, F16, BF16, FP8_E4M3 = 0, 1, 2, 3
+F32, F16, BF16, FP8_E4M3, INT8 = 0, 1, 2, 3, 4
 ROTATE_HALF, INTERLEAVED = 0, 1
 SILU, GELU_TANH = 0, 1
 AXES_BLOCKS, AXES_CYCLED = 0, 1
@@ -33,9 +33,12 @@ EXPORTS = ("edge_rmsnorm", "edge_add_rmsnorm", "edge_glu_act", "edge_qk_norm_rop
            "edge_paged_attention", "edge_paged_attention_workspace",
            "edge_pages_copy", "edge_pages_free", "edge_pages_fork", "edge_pages_compact",
            "edge_pages_compact_workspace",
+           "edge_rmsnorm_q8", "edge_add_rmsnorm_q8", "edge_glu_act_q8", "edge_quantize_q8",
+           "edge_matmul_q8",
            "edge_status_str", "edge_last_cuda_error", "edge_version")
 QK_ROTATE_UNROUNDED = 1
 
+_ACTS = {"silu": SILU, "gelu_tanh": GELU_TANH}
 _DT = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 _LIB = None
 
@@ -107,6 +110,14 @@ def lib(build_if_missing: bool = False) -> ctypes.CDLL:
         getattr(L, name).restype = I
     L.edge_pages_compact_workspace.argtypes = [I32]
     L.edge_pages_compact_workspace.restype = I64
+    L.edge_rmsnorm_q8.argtypes = [P, I, P, P, P, I, I64, I64, F, I, P]
+    L.edge_add_rmsnorm_q8.argtypes = [P, I, P, P, P, P, I, I64, I64, F, I, P]
+    L.edge_glu_act_q8.argtypes = [P, I, P, P, I, I64, I64, I, P]
+    L.edge_quantize_q8.argtypes = [P, I, P, P, I, I64, I64, P]
+    L.edge_matmul_q8.argtypes = [P, I, P, P, I, P, P, P, I64, I64, I64, P]
+    for name in ("edge_rmsnorm_q8", "edge_add_rmsnorm_q8", "edge_glu_act_q8", "edge_quantize_q8",
+                 "edge_matmul_q8"):
+        getattr(L, name).restype = I
     L.edge_status_str.argtypes = [I]
     L.edge_status_str.restype = ctypes.c_char_p
     L.edge_last_cuda_error.restype = I
@@ -286,7 +297,7 @@ def glu_act(gate_up, act=SILU, *, out=None, fp8=False, inv_scale=1.0, stream=Non
     d = two_d // 2
     rows = gate_up.numel() // two_d if two_d else 0
     if isinstance(act, str):
-        act = {"silu": SILU, "gelu_tanh": GELU_TANH}[act]
+        act = _ACTS[act]
     if out is None:
         out = _alloc(gate_up, tuple(gate_up.shape[:-1]) + (d,), fp8)
     dt = _dt(gate_up)
@@ -644,3 +655,206 @@ def pages_compact(caches, block_table, refs, *, table_out=None, refs_out=None, w
                                     workspace.data_ptr(), workspace.numel(), _stream(None)),
            "edge_pages_compact")
     return workspace[:4 * caches.num_pages].view(torch.int32)
+
+
+# ---------------------------------------------------------------- 8 bits, a scale per token
+
+# dtypes of a tensor of codes, by fp8; the first is the one that the binding allocates
+_CODES = {False: (torch.int8,), True: (torch.uint8, torch.float8_e4m3fn)}
+_CODE_KIND = {torch.int8: INT8, torch.uint8: FP8_E4M3, torch.float8_e4m3fn: FP8_E4M3}
+
+
+def _q8_fits(at, x, n, shape, fp8, out, scales):
+    """Whether x, and out and scales where given, suit a call that turns the rows of x
+    into n codes each, of shape `shape` in all."""
+    return (at >= 0 and n > 0 and x.is_contiguous() and
+            (out is None or (out.shape == shape and out.dtype in _CODES[fp8] and
+                             out.get_device() == at and out.is_contiguous())) and
+            (scales is None or (scales.shape == shape[:-1] and
+                                _fits(at, torch.float32, scales))))
+
+
+def _explain_q8(x, name, shape, fp8, out, scales):
+    """Raises for the first tensor of a row call in 8 bits that does not fit."""
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor, not on {dev}")
+    if shape[-1] < 1:
+        raise ValueError(f"{name} must have rows of at least one code, not shape {tuple(x.shape)}")
+    _want(x, name, x.dtype, tuple(x.shape), dev)
+    if out is not None:
+        kind = out.dtype if out.dtype in _CODES[fp8] else _CODES[fp8][0]
+        _want(out, "out", kind, tuple(shape), dev)
+    if scales is not None:
+        _want(scales, "scales", torch.float32, tuple(shape[:-1]), dev)
+
+
+def _q8_results(x, shape, fp8, out, scales):
+    if out is None:
+        out = torch.empty(shape, dtype=_CODES[fp8][0], device=x.device)
+    if scales is None:
+        scales = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
+    return out, scales
+
+
+def rmsnorm_q8(x, w=None, *, eps=1e-6, weight_offset=0, fp8=False, out=None, scales=None,
+               stream=None):
+    """RMSNorm over the last dim of x ([..., n]) in 8 bits: int8 codes, or E4M3
+    codes (uint8) with fp8=True, and an fp32 scale for each row.  w: [n].
+    Returns (out, scales), out * scales[..., None] being the norm."""
+    at, shape = x.get_device(), x.shape
+    n = shape[-1]
+    if not (_q8_fits(at, x, n, shape, fp8, out, scales) and
+            (w is None or (w.shape == (n,) and _fits(at, x.dtype, w)))):
+        _explain_q8(x, "x", shape, fp8, out, scales)
+        if w is not None:
+            _want(w, "w", x.dtype, (n,), x.device)
+    if not _here(at, stream):
+        with _on(x.device, stream):
+            return rmsnorm_q8(x, w, eps=eps, weight_offset=weight_offset, fp8=fp8, out=out,
+                              scales=scales)
+    dt = _dt(x)
+    out, scales = _q8_results(x, shape, fp8, out, scales)
+    rows = scales.numel()
+    if rows == 0:
+        return out, scales  # (an empty tensor has no address to pass on)
+    st = lib().edge_rmsnorm_q8(out.data_ptr(), FP8_E4M3 if fp8 else INT8, scales.data_ptr(),
+                               x.data_ptr(), _ptr(w), dt, rows, n, eps, weight_offset,
+                               _stream(None))
+    if st:
+        raise EdgeError(st, "edge_rmsnorm_q8")
+    return out, scales
+
+
+def add_rmsnorm_q8(x, residual, w=None, *, eps=1e-6, weight_offset=0, fp8=False, out=None,
+                   scales=None, stream=None):
+    """residual <- x + residual (rounded to the dtype); returns rmsnorm_q8 of it."""
+    at, shape = x.get_device(), x.shape
+    n = shape[-1]
+    if not (_q8_fits(at, x, n, shape, fp8, out, scales) and residual.shape == shape and
+            _fits(at, x.dtype, residual) and
+            (w is None or (w.shape == (n,) and _fits(at, x.dtype, w)))):
+        _explain_q8(x, "x", shape, fp8, out, scales)
+        _want(residual, "residual", x.dtype, tuple(shape), x.device)
+        if w is not None:
+            _want(w, "w", x.dtype, (n,), x.device)
+    if not _here(at, stream):
+        with _on(x.device, stream):
+            return add_rmsnorm_q8(x, residual, w, eps=eps, weight_offset=weight_offset, fp8=fp8,
+                                  out=out, scales=scales)
+    dt = _dt(x)
+    out, scales = _q8_results(x, shape, fp8, out, scales)
+    rows = scales.numel()
+    if rows == 0:
+        return out, scales
+    st = lib().edge_add_rmsnorm_q8(out.data_ptr(), FP8_E4M3 if fp8 else INT8, scales.data_ptr(),
+                                   x.data_ptr(), residual.data_ptr(), _ptr(w), dt, rows, n, eps,
+                                   weight_offset, _stream(None))
+    if st:
+        raise EdgeError(st, "edge_add_rmsnorm_q8")
+    return out, scales
+
+
+def glu_act_q8(gate_up, act=SILU, *, fp8=False, out=None, scales=None, stream=None):
+    """act(gate) * up for gate_up = [..., 2d] (gate first) in 8 bits, as rmsnorm_q8
+    returns them: ([..., d], [...])."""
+    if isinstance(act, str):
+        act = _ACTS[act]
+    at, two_d = gate_up.get_device(), gate_up.shape[-1]
+    shape = gate_up.shape[:-1] + (two_d // 2,)
+    if not (_q8_fits(at, gate_up, two_d // 2, shape, fp8, out, scales) and two_d % 2 == 0):
+        _explain_q8(gate_up, "gate_up", shape, fp8, out, scales)
+        raise ValueError(f"gate_up must have rows of an even length, not {two_d}")
+    if not _here(at, stream):
+        with _on(gate_up.device, stream):
+            return glu_act_q8(gate_up, act, fp8=fp8, out=out, scales=scales)
+    dt = _dt(gate_up)
+    out, scales = _q8_results(gate_up, shape, fp8, out, scales)
+    rows = scales.numel()
+    if rows == 0:
+        return out, scales
+    st = lib().edge_glu_act_q8(out.data_ptr(), FP8_E4M3 if fp8 else INT8, scales.data_ptr(),
+                               gate_up.data_ptr(), dt, rows, two_d // 2, act, _stream(None))
+    if st:
+        raise EdgeError(st, "edge_glu_act_q8")
+    return out, scales
+
+
+def quantize_q8(x, *, fp8=False, out=None, scales=None, stream=None):
+    """The rows of x ([..., n]) in 8 bits, as rmsnorm_q8 returns them."""
+    at, shape = x.get_device(), x.shape
+    n = shape[-1]
+    if not _q8_fits(at, x, n, shape, fp8, out, scales):
+        _explain_q8(x, "x", shape, fp8, out, scales)
+    if not _here(at, stream):
+        with _on(x.device, stream):
+            return quantize_q8(x, fp8=fp8, out=out, scales=scales)
+    dt = _dt(x)
+    out, scales = _q8_results(x, shape, fp8, out, scales)
+    rows = scales.numel()
+    if rows == 0:
+        return out, scales
+    st = lib().edge_quantize_q8(out.data_ptr(), FP8_E4M3 if fp8 else INT8, scales.data_ptr(),
+                                x.data_ptr(), dt, rows, n, _stream(None))
+    if st:
+        raise EdgeError(st, "edge_quantize_q8")
+    return out, scales
+
+
+def matmul_q8(a, w, a_scales, w_scales, *, bias=None, dtype=None, out=None, stream=None):
+    """a w^T of 8-bit operands with a scale for each token and output channel.
+    a: [..., k] and w: [n, k], both int8 or both E4M3 codes (uint8 or
+    float8_e4m3fn); a_scales: [...], w_scales: [n] fp32; bias: [n].  The result
+    ([..., n]) and bias have dtype `dtype` (out's, or bf16)."""
+    at, k, n = a.get_device(), a.shape[-1], w.shape[0]
+    kind = _CODE_KIND.get(a.dtype)
+    if dtype is None:
+        dtype = torch.bfloat16 if out is None else out.dtype
+    shape = a.shape[:-1] + (n,)
+    if not (at >= 0 and kind is not None and k > 0 and w.shape == (n, k) and a.is_contiguous() and
+            _CODE_KIND.get(w.dtype) == kind and w.get_device() == at and w.is_contiguous() and
+            a_scales.shape == shape[:-1] and w_scales.shape == (n,) and
+            _fits(at, torch.float32, a_scales, w_scales) and
+            (bias is None or (bias.shape == (n,) and _fits(at, dtype, bias))) and
+            (out is None or (out.shape == shape and _fits(at, dtype, out)))):
+        _explain_matmul(a, w, a_scales, w_scales, bias, dtype, out)
+    if not _here(at, stream):
+        with _on(a.device, stream):
+            return matmul_q8(a, w, a_scales, w_scales, bias=bias, dtype=dtype, out=out)
+    try:
+        dt = _DT[dtype]
+    except KeyError:
+        raise TypeError(f"unsupported dtype {dtype}") from None
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=a.device)
+    tokens = a_scales.numel()
+    if tokens == 0:
+        return out
+    st = lib().edge_matmul_q8(out.data_ptr(), dt, a.data_ptr(), w.data_ptr(), kind,
+                              a_scales.data_ptr(), w_scales.data_ptr(), _ptr(bias), tokens, n, k,
+                              _stream(None))
+    if st:
+        raise EdgeError(st, "edge_matmul_q8")
+    return out
+
+
+def _explain_matmul(a, w, a_scales, w_scales, bias, dtype, out):
+    """Raises for the first tensor of a matmul_q8 call that does not fit."""
+    dev = a.device
+    if dev.type != "cuda":
+        raise ValueError(f"a must be a CUDA tensor, not on {dev}")
+    if a.dtype not in _CODE_KIND:
+        raise TypeError(f"a must hold int8 or E4M3 codes, not {a.dtype}")
+    if w.dim() != 2 or a.shape[-1] < 1:
+        raise ValueError(f"a and w must be [..., k] and [n, k], not {tuple(a.shape)} and "
+                         f"{tuple(w.shape)}")
+    n, k = w.shape[0], a.shape[-1]
+    same = w.dtype if _CODE_KIND.get(w.dtype) == _CODE_KIND[a.dtype] else a.dtype
+    _want(a, "a", a.dtype, tuple(a.shape), dev)
+    _want(w, "w", same, (n, k), dev)
+    _want(a_scales, "a_scales", torch.float32, tuple(a.shape[:-1]), dev)
+    _want(w_scales, "w_scales", torch.float32, (n,), dev)
+    if bias is not None:
+        _want(bias, "bias", dtype, (n,), dev)
+    if out is not None:
+        _want(out, "out", dtype, tuple(a.shape[:-1]) + (n,), dev)

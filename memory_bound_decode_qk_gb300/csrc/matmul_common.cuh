@@ -37,4 +37,8 @@ __device__ __forceinline__ float scaled(float sum, float sa, float sw, float bia
     return __fadd_rn(__fmul_rn(__fmul_rn(sum, sa), sw), bias);
 }
 
+// On the tensor memory (matmul_q8_tc.cu).  cfg has room for one more attribute.
+bool matmul_tc_suits(const MatmulP& m);
+cudaError_t launch_matmul_tc(const MatmulP& m, int q_dt, cudaLaunchConfig_t cfg);
+
 }  // namespace edge

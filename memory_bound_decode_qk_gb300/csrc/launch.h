@@ -188,6 +188,10 @@ int sm_count();
 // shared memory (the occupancy calculator, cached per kernel and device).
 int resident_ctas(const void* fn, int threads);
 
+// Clusters of `n` CTAs of kernel `fn` resident at the same time, launched as `cfg`
+// says (the occupancy calculator, cached per kernel, size and device).
+int resident_clusters(const void* fn, const cudaLaunchConfig_t& cfg, int n);
+
 // Lets kernel `fn` use `bytes` of dynamic shared memory (asked of the runtime
 // once per kernel and device).
 cudaError_t allow_smem(const void* fn, int bytes);

@@ -37,6 +37,22 @@ __device__ __forceinline__ float scaled(float sum, float sa, float sw, float bia
     return __fadd_rn(__fmul_rn(__fmul_rn(sum, sa), sw), bias);
 }
 
+// Four int8 to four fp16 numbers: a byte with its sign bit turned, in the low bits of
+// an fp16 number of exponent 2^10, is 1024 + 128 + the value.
+__device__ __forceinline__ void widen4(uint32_t v, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = v ^ 0x80808080u;
+    const __half2 bias = __floats2half2_rn(-1152.0f, -1152.0f);
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 x = __hadd2(*reinterpret_cast<const __half2*>(&a), bias);
+    const __half2 y = __hadd2(*reinterpret_cast<const __half2*>(&b), bias);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+
+// A few tokens (matmul_q8_few.cu).
+bool matmul_few_suits(const MatmulP& m);
+cudaError_t launch_matmul_few(const MatmulP& m, int q_dt, cudaLaunchConfig_t cfg);
+
 // On the tensor memory (matmul_q8_tc.cu).  cfg has room for one more attribute.
 bool matmul_tc_suits(const MatmulP& m);
 cudaError_t launch_matmul_tc(const MatmulP& m, int q_dt, cudaLaunchConfig_t cfg);

@@ -183,6 +183,7 @@ cudaError_t launch_matmul_q8(const MatmulQ8Args& a, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 1 : 0;
+    if (matmul_few_suits(p)) return launch_matmul_few(p, a.q_dt, cfg);
     if (matmul_tc_suits(p)) return launch_matmul_tc(p, a.q_dt, cfg);
     return a.q_dt == kInt8 ? launch_any<true>(p, cfg) : launch_any<false>(p, cfg);
 }

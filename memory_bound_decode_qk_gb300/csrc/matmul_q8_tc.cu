@@ -1,11 +1,18 @@
 // matmul_q8_tc.cu -- the 8-bit product on the 5th-generation tensor cores (sm_103a).
 //
 // A tile is 128 output channels (the rows of the accumulator, so that a thread's
-// channel scale is one register) by NT tokens (its columns).  Roles of the warps:
-//   warp 0        copies both operands by TMA into a ring in shared memory
-//   warp 1        issues tcgen05.mma (one thread)
-//   warps 4-11    scales and stores, a thread per channel and half of the tokens
-//   warps 12-19   int8 only: widen the ring's bytes to fp16
+// channel scale is one register) by nt tokens (its columns).  Two forms:
+//   one CTA     nt of 16, 32 or 64, for few tokens: E4M3 keeps two CTAs on an SM.  Few
+//               tiles are cut along the sum over the CTAs of a cluster, which add
+//               their parts through distributed shared memory in a fixed order.
+//   a pair      256 channels by up to 256 tokens (int8: 192), each CTA of the pair with
+//               128 of the channels and half of the tokens (tcgen05 .cta_group::2):
+//               a byte of either operand is fetched for twice as many products.
+// Roles of the warps:
+//   warp 0      copies both operands by TMA into a ring in shared memory
+//   warp 1      issues tcgen05.mma (one thread; of a pair, the first CTA's)
+//   warps 4..   scale and store, a thread per channel and all or half of the tokens
+//   the last    int8 only: widen the ring's bytes to fp16
 // The accumulator is held twice, so the tile that is stored does not stop the next
 // one's products.  CTAs are persistent over the tiles.
 //
@@ -14,49 +21,66 @@
 // product (148 TOPS measured).  But every int8 is an fp16 number, a product of two is
 // at most 2^14 in size, and fp32 sums of whole numbers are exact up to 2^24: so int8
 // operands go through kind::f16 exactly, 1024 terms at a time.  Every 1024 terms the
-// accumulator is emptied into int32 registers.
-//
-// Few tiles are cut along the summed dimension over the CTAs of a cluster (SPLIT),
-// which then add their parts through distributed shared memory in a fixed order.
+// accumulator is emptied into int32 registers.  The widened weights go to TMEM, where
+// the unit reads them without taking bandwidth from shared memory (which a product of
+// few tokens needs whole: 128 rows of 32 bytes took 64 cycles whatever nt was), the
+// tokens back to shared memory.
 //
 // Every wait has a limit of two seconds.  A wait that runs out (which correct
 // operation never does) ends all later waits of the CTA at once and makes its
 // outputs NaN.
+#include <cmath>
+
 #include "matmul_common.cuh"
 #include "tc_common.cuh"
 
 namespace edge {
 namespace {
 
-constexpr int kRows = 128;  // channels of a tile
+constexpr int kRows = 128;  // channels of a CTA's tile
+constexpr int kStep = 128;  // terms of a ring entry, the bytes of a swizzled row
 
-template <bool INT8, int NT>
+// NT: tokens of a tile, for a pair the most.
+template <bool INT8, int NT, bool PAIR>
 struct Mm {
-    static constexpr int kStep = INT8 ? 64 : 128;                 // terms of a ring entry
-    static constexpr int kRaw = (kRows + NT) * kStep;             // bytes that TMA writes
-    static constexpr int kWide = (kRows + NT) * 128;              // fp16 bytes of an int8 entry
-    static constexpr int kWides = INT8 ? (NT >= 128 ? 3 : 4) : 0;
-    static constexpr int kLeft = 220 * 1024 - kWides * kWide;
-    static constexpr int kStages = kLeft / kRaw < 10 ? kLeft / kRaw : 10;
+    static constexpr int kCtas = PAIR || INT8 ? 1 : 2;            // on an SM
+    static constexpr int kRoom = (kCtas == 2 ? 110 : 222) * 1024 - 1024;
+    static constexpr int kTokens = PAIR ? NT / 2 : NT;            // of this CTA's part of the operand
+    static constexpr int kRaw = (kRows + kTokens) * kStep;        // bytes of a ring entry
+    // int8: half an entry (64 terms) widened, the weights in TMEM, the tokens here
+    static constexpr int kWides = !INT8 ? 0 : PAIR ? 4 : 8;
+    static constexpr int kWide = kTokens * 128;
+    static constexpr int kFit = (kRoom - kWides * kWide) / kRaw;
+    static constexpr int kStages = kFit < 10 ? kFit : 10;
     static constexpr int kSmem = kStages * kRaw + kWides * kWide + 1024;
-    static constexpr int kThreads = INT8 ? 640 : 384;
-    static constexpr int kColumns = 2 * NT;                       // of TMEM
-    static constexpr int kUnit = INT8 ? 1024 / kStep : 1 << 30;   // entries until the sum is emptied
-    static_assert(kStages >= 3 && kSmem <= 227 * 1024, "the ring does not fit");
-    static_assert(NT * kRows * 4 <= kSmem - 1024, "a part of a cut tile does not fit");
+    static constexpr int kUnit = INT8 ? 1024 / kStep : 1 << 30;   // entries until a sum is emptied
+    // columns of TMEM: two sums, and the widened weights (32 for 64 terms)
+    static constexpr int kNeed = 2 * NT + 32 * kWides;
+    static constexpr int kColumns = kNeed <= 32 ? 32 : kNeed <= 64 ? 64 : kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
+    // warps: 4 for copies and products, those of the sums, groups of 4 that widen
+    static constexpr int kSumWarps = PAIR ? 8 : 4;
+    static constexpr int kGroups = !INT8 ? 0 : PAIR ? 3 : 4;
+    static constexpr int kThreads = 128 + 32 * kSumWarps + 128 * kGroups;
+    // int8: registers of the three kinds of warps; together at most the launch's, 768
+    // threads at 80
+    enum : int { kRegsFew = 40, kRegsSums = PAIR ? 144 : 152, kRegsWide = PAIR ? 48 : 72 };
+    static_assert(kStages >= 3 && kStages <= 10 && kNeed <= 512, "the ring or the accumulators do not fit");
+    static_assert(PAIR || NT * kRows * 4 <= kSmem - 1024, "a part of a cut tile does not fit");
 };
 
 struct MmSmem {
     uint64_t full[10], empty[10];      // the ring
-    uint64_t wide[4], narrow[4];       // widened entries: full, empty
+    uint64_t wide[8], narrow[8];       // widened halves of entries: full, empty
     uint64_t sum[2], taken[2];         // accumulators: full, empty
     uint32_t tmem, failed;
 };
 
 struct TcP {
     MatmulP m;
+    int nt;          // tokens of a tile
     int tiles_n, tiles_t;
-    int split;       // CTAs of a cluster that share a tile
+    int split;       // one CTA: CTAs of a cluster that share a tile
+    int pairs;       // 16-bit outputs whose channel pairs start on 4 bytes
 };
 
 // Tiles in groups of 16 token tiles, the token tile running fastest: a wave's
@@ -68,12 +92,27 @@ __device__ __forceinline__ void tile_at(const TcP& p, int i, int& tn, int& tt) {
     tt = first + at - tn * wide;
 }
 
-template <bool INT8>
-__device__ __forceinline__ void mma_8bit(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t lead) {
-    if constexpr (INT8) {
+// ---------------------------------------------------------------- instructions
+
+// d (+)= A B: E4M3 with A in shared memory, fp16 with A in TMEM.
+template <bool INT8, bool PAIR>
+__device__ __forceinline__ void mma_8bit(uint32_t d, uint64_t a, uint32_t ta, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t lead) {
+    if constexpr (INT8 && PAIR) {
         asm volatile(
             "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+            "r"(ta), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
+            : "memory");
+    } else if constexpr (INT8) {
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+            "r"(ta), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
+            : "memory");
+    } else if constexpr (PAIR) {
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
             "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
             : "memory");
     } else {
@@ -84,11 +123,33 @@ __device__ __forceinline__ void mma_8bit(uint32_t d, uint64_t a, uint64_t b, uin
             : "memory");
     }
 }
+// Arrives, once every product issued before is complete, on the barrier: of a pair, on
+// that of both CTAs.
+template <bool PAIR>
+__device__ __forceinline__ void mma_commit(uint32_t bar, uint32_t lead) {
+    if constexpr (PAIR) {
+        asm volatile(
+            "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+            "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}" ::"r"(bar),
+            "r"(lead), "h"((uint16_t)3)
+            : "memory");
+    } else {
+        tc_commit(bar, lead);
+    }
+}
 
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar, uint32_t lead) {
     asm volatile(
         "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t"
         "@q cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar), "r"(lead)
+        : "memory");
+}
+// The same to this CTA's shared memory, with the barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_2d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(bar), "r"(lead)
         : "memory");
 }
@@ -99,45 +160,67 @@ __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, i
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// A 32-bit word of shared memory of CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t peer_word(uint32_t addr, int rank) {
-    uint32_t at, v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
+// This CTA's shared-memory address as CTA `rank` of the cluster has it.
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, int rank) {
+    uint32_t at;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
+    return at;
+}
+__device__ __forceinline__ uint32_t peer_word(uint32_t at) {
+    uint32_t v;
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
     return v;
 }
-
-// Four int8 to four fp16 numbers: a byte with its sign bit turned, in the low bits of
-// an fp16 number of exponent 2^10, is 1024 + 128 + the value.
-__device__ __forceinline__ void widen4(uint32_t v, uint32_t& lo, uint32_t& hi) {
-    const uint32_t u = v ^ 0x80808080u;
-    const __half2 bias = __floats2half2_rn(-1152.0f, -1152.0f);
-    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-    const __half2 x = __hadd2(*reinterpret_cast<const __half2*>(&a), bias);
-    const __half2 y = __hadd2(*reinterpret_cast<const __half2*>(&b), bias);
-    lo = *reinterpret_cast<const uint32_t*>(&x);
-    hi = *reinterpret_cast<const uint32_t*>(&y);
+__device__ __forceinline__ uint4 peer_vector(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+// Arrives on a barrier of any CTA of the cluster.
+__device__ __forceinline__ void cluster_bar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-template <bool INT8, int NT>
-__global__ void __launch_bounds__(Mm<INT8, NT>::kThreads, 1)
+__device__ __forceinline__ uint4 lds_vector(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts_vector(uint32_t at, const uint4& v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// ---------------------------------------------------------------- the kernel
+
+template <bool INT8, int NT, bool PAIR>
+__global__ void __launch_bounds__(Mm<INT8, NT, PAIR>::kThreads, Mm<INT8, NT, PAIR>::kCtas)
 matmul_tc_kernel(TcP p, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap amap) {
-    using C = Mm<INT8, NT>;
-    constexpr int ST = C::kStages, WD = C::kWides > 0 ? C::kWides : 1;
+    using C = Mm<INT8, NT, PAIR>;
+    constexpr int ST = C::kStages, WD = C::kWides > 0 ? C::kWides : 1, SW = C::kSumWarps;
+    constexpr int TILE = PAIR ? 2 * kRows : kRows;
     extern __shared__ char raw[];
     __shared__ MmSmem sh;
     const int tid = threadIdx.x, lane = tid & 31, wid = uniform(tid >> 5);
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;  // the swizzle works on address bits
     const uint32_t wides = base, ring = base + C::kWides * C::kWide;
-    const int split = p.split, rank = split > 1 ? (int)(blockIdx.x % split) : 0;
+    const int nt = PAIR ? p.nt : NT, part = PAIR ? nt / 2 : NT;  // tokens of the tile, and this CTA's
+    const int split = PAIR ? 1 : p.split, cluster = PAIR ? 2 : split;
+    const int rank = cluster > 1 ? (int)(blockIdx.x % cluster) : 0;
     const int tiles = p.tiles_n * p.tiles_t;
-    const int first = blockIdx.x / split, step = gridDim.x / split;
-    const int entries = (p.m.k + C::kStep - 1) / C::kStep;
-    const int e0 = (int)((int64_t)entries * rank / split), e1 = (int)((int64_t)entries * (rank + 1) / split);
+    const int first = blockIdx.x / cluster, step = gridDim.x / cluster;
+    const int entries = (p.m.k + kStep - 1) / kStep;
+    const int e0 = PAIR ? 0 : (int)((int64_t)entries * rank / split);
+    const int e1 = PAIR ? entries : (int)((int64_t)entries * (rank + 1) / split);
+    const int mine_n = PAIR ? rank * kRows : 0;  // this CTA's channels in the tile
 
     if (wid == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh.tmem)), "n"(C::kColumns) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        if constexpr (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh.tmem)), "n"(C::kColumns) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh.tmem)), "n"(C::kColumns) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
     }
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
@@ -145,12 +228,12 @@ matmul_tc_kernel(TcP p, const __grid_constant__ CUtensorMap wmap, const __grid_c
             bar_init(smem_addr(&sh.empty[i]), INT8 ? 8 : 1);
         }
         for (int i = 0; i < WD; ++i) {
-            bar_init(smem_addr(&sh.wide[i]), 8);
+            bar_init(smem_addr(&sh.wide[i]), PAIR ? 8 : 4);
             bar_init(smem_addr(&sh.narrow[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(smem_addr(&sh.sum[i]), 1);
-            bar_init(smem_addr(&sh.taken[i]), 8);
+            bar_init(smem_addr(&sh.taken[i]), PAIR ? 2 * SW : SW);
         }
         sh.failed = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -158,103 +241,168 @@ matmul_tc_kernel(TcP p, const __grid_constant__ CUtensorMap wmap, const __grid_c
         // the first weights into L2 while the preceding grid drains
         int tn, tt;
         tile_at(p, first, tn, tt);
-        for (int e = e0; e < e1 && e < e0 + ST; ++e) tma_prefetch_2d(&wmap, e * C::kStep, tn * kRows);
+        for (int e = e0; e < e1 && e < e0 + ST; ++e) tma_prefetch_2d(&wmap, e * kStep, tn * TILE + mine_n);
     }
     tc_before();
-    __syncthreads();
+    if constexpr (PAIR) {
+        __syncwarp();
+        cluster_sync();  // both CTAs' barriers are there
+    } else {
+        __syncthreads();
+    }
     tc_after();
     pdl_wait();
     pdl_launch_dependents();
     const uint32_t tmem = (uint32_t)uniform((int)sh.tmem);
+    const uint32_t tmem_w = tmem + 2 * NT;  // widened weights
     volatile uint32_t* failed = &sh.failed;
 
     if (wid < 4) {
-        if constexpr (INT8) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if constexpr (INT8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"((int)C::kRegsFew));
         if (wid == 0) {
             // ---- copies
             const uint32_t lead = elect_lane();
-            uint32_t n = 0;
+            const uint32_t bytes = (uint32_t)(kRows + part) * kStep;
+            uint32_t st = 0, phase = 1;
             for (int i = first; i < tiles; i += step) {
                 int tn, tt;
                 tile_at(p, i, tn, tt);
-                for (int e = e0; e < e1; ++e, ++n) {
-                    const uint32_t st = n % ST, dst = ring + st * C::kRaw, bar = smem_addr(&sh.full[st]);
-                    bar_wait(smem_addr(&sh.empty[st]), ((n / ST) & 1) ^ 1, failed);
-                    bar_expect(bar, C::kRaw, lead);
-                    tma_2d(dst, &wmap, e * C::kStep, tn * kRows, bar, lead);
-                    tma_2d(dst + kRows * C::kStep, &amap, e * C::kStep, tt * NT, bar, lead);
+                const int y = tn * TILE + mine_n, t = tt * nt + (PAIR ? rank * part : 0);
+                for (int e = e0; e < e1; ++e) {
+                    const uint32_t dst = ring + st * C::kRaw, bar = smem_addr(&sh.full[st]);
+                    bar_wait(smem_addr(&sh.empty[st]), phase, failed);
+                    if constexpr (PAIR && !INT8) {
+                        // the products wait for both CTAs' operands on the first one's barrier
+                        if (rank == 0) bar_expect(bar, 2 * bytes, lead);
+                        const uint32_t at = peer_addr(bar, 0);
+                        tma_2d_pair(dst, &wmap, e * kStep, y, at, lead);
+                        tma_2d_pair(dst + kRows * kStep, &amap, e * kStep, t, at, lead);
+                    } else {
+                        bar_expect(bar, bytes, lead);
+                        tma_2d(dst, &wmap, e * kStep, y, bar, lead);
+                        tma_2d(dst + kRows * kStep, &amap, e * kStep, t, bar, lead);
+                    }
+                    if (++st == ST) {
+                        st = 0;
+                        phase ^= 1;
+                    }
                 }
             }
-        } else if (wid == 1) {
+            if constexpr (PAIR && !INT8) {
+                // the other CTA's last arrivals on this one's barriers
+                for (int i = 0; i < ST; ++i) {
+                    bar_wait(smem_addr(&sh.empty[st]), phase, failed);
+                    if (++st == ST) {
+                        st = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+        } else if (wid == 1 && (!PAIR || rank == 0)) {
             // ---- products
             const uint32_t lead = elect_lane();
-            constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(NT / 8) << 17) | ((uint32_t)(kRows / 16) << 24);
-            constexpr int DEPTH = INT8 ? WD : ST;
-            constexpr int BYTES = INT8 ? C::kWide : C::kRaw;
-            const uint64_t dw = smem_desc(INT8 ? wides : ring, 16);
-            const uint64_t da = dw + ((kRows * 128) >> 4);
-            uint32_t n = 0, unit = 0;
+            const uint32_t idesc = (1u << 4) | ((uint32_t)(nt / 8) << 17) | ((uint32_t)(TILE / 16) << 24);
+            constexpr int DEPTH = INT8 ? WD : ST, HALVES = INT8 ? 2 : 1;
+            const uint64_t dw = smem_desc(ring, 16), dt = smem_desc(INT8 ? wides : ring + kRows * kStep, 16);
+            constexpr uint32_t BYTES = INT8 ? C::kWide : C::kRaw;
+            uint32_t st = 0, phase = 0, unit = 0;
             for (int i = first; i < tiles; i += step) {
                 for (int e = e0; e < e1; ++unit) {
                     const uint32_t buf = unit & 1, d = tmem + buf * NT;
                     bar_wait(smem_addr(&sh.taken[buf]), ((unit >> 1) & 1) ^ 1, failed);
                     tc_after();
-                    const int end = min(e1, e + C::kUnit), begin = e;
-                    for (; e < end; ++e, ++n) {
-                        const uint32_t st = n % DEPTH;
-                        bar_wait(smem_addr(INT8 ? &sh.wide[st] : &sh.full[st]), (n / DEPTH) & 1, failed);
+                    const int end = min(e1, e + C::kUnit);
+                    uint32_t more = 0;
+                    for (int count = (end - e) * HALVES; count > 0; --count) {
+                        bar_wait(smem_addr(INT8 ? &sh.wide[st] : &sh.full[st]), phase, failed);
                         tc_after();
-                        const uint64_t at = st * (uint32_t)(BYTES >> 4);
+                        const uint64_t at = st * (uint64_t)(BYTES >> 4);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            mma_8bit<INT8>(d, dw + (at + k * 2), da + (at + k * 2), idesc, k > 0 ? 1u : (uint32_t)(e > begin), lead);
+                            mma_8bit<INT8, PAIR>(d, dw + (at + k * 2), tmem_w + st * 32 + k * 8, dt + (at + k * 2), idesc, k > 0 ? 1u : more, lead);
                         }
-                        tc_commit(smem_addr(INT8 ? &sh.narrow[st] : &sh.empty[st]), lead);
+                        more = 1;
+                        mma_commit<PAIR>(smem_addr(INT8 ? &sh.narrow[st] : &sh.empty[st]), lead);
+                        if (++st == DEPTH) {
+                            st = 0;
+                            phase ^= 1;
+                        }
                     }
-                    tc_commit(smem_addr(&sh.sum[buf]), lead);
+                    e = end;
+                    mma_commit<PAIR>(smem_addr(&sh.sum[buf]), lead);
                 }
             }
         }
-    } else if (wid < 12) {
-        if constexpr (INT8) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
-        // ---- sums: this thread's channel, and half of the tokens
-        constexpr int H = NT / 2, CH = H < 32 ? H : 32;
+    } else if (wid < 4 + SW) {
+        if constexpr (INT8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"((int)C::kRegsSums));
+        // ---- sums: this thread's channel, and all or half of the tokens
+        constexpr int H = NT / (SW / 4), CH = 16;
+        const int h = nt / (SW / 4);
         const int quad = wid & 3, half = (wid - 4) >> 2;
         const int row = quad * 32 + lane;
-        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + half * H;
-        auto load = [&](uint32_t at, uint32_t (&v)[CH]) {
-            if constexpr (CH == 32) {
-                tc_ld32(at, v);
+        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + half * h;
+        auto release = [&](uint32_t buf) {
+            tc_before();
+            __syncwarp();
+            if (lane != 0) return;
+            if constexpr (PAIR) {
+                cluster_bar_arrive(peer_addr(smem_addr(&sh.taken[buf]), 0));
             } else {
-                tc_ld16(at, v);
+                bar_arrive(smem_addr(&sh.taken[buf]));
             }
-            tc_wait_ld();
         };
         uint32_t unit = 0;
         for (int i = first; i < tiles; i += step) {
             int tn, tt;
             tile_at(p, i, tn, tt);
-            const int ch = tn * kRows + row, t0 = tt * NT + half * H;
+            const int ch = tn * TILE + mine_n + row, t0 = tt * nt + half * h;
             const bool mine = ch < p.m.n;
             const float sw = mine ? __ldg(p.m.sw + ch) : 0.0f;
             const float bias = mine && p.m.bias != nullptr ? load_out(p.m.bias, ch, p.m.out_dt) : 0.0f;
-            // CH sums of tokens t0 + c ..: to the output, or to this CTA's part of the tile
+            // the sums of tokens t0 + c ..: to the output, or to this CTA's part of the tile
             auto give = [&](int c, const uint32_t (&v)[CH]) {
                 if (split > 1) {
 #pragma unroll
                     for (int j = 0; j < CH; ++j) {
-                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(base + (uint32_t)(((half * H + c + j) * kRows + row) * 4)), "r"(v[j]) : "memory");
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(base + (uint32_t)(((half * h + c + j) * kRows + row) * 4)), "r"(v[j]) : "memory");
                     }
                     return;
                 }
-                if (!mine) return;
                 const float nan = *failed ? NAN : 0.0f;
+                // lane j holds the scale of token c + j
+                const float scales = lane < CH && t0 + c + lane < p.m.tokens ? __ldg(p.m.sa + t0 + c + lane) : 0.0f;
+                char* dst = p.m.out + ((int64_t)(t0 + c) * p.m.n + ch) * (p.m.out_dt == kF32 ? 4 : 2);
+                const int64_t next = (int64_t)p.m.n * (p.m.out_dt == kF32 ? 4 : 2);
+                const int count = min(CH, p.m.tokens - t0 - c);
+                auto value = [&](int j) {
+                    const float sum = (INT8 ? __int2float_rn((int)v[j]) : __uint_as_float(v[j])) + nan;
+                    return scaled(sum, __shfl_sync(0xffffffffu, scales, j), sw, bias);
+                };
+                if (p.pairs) {
+                    // even lanes store token j of their and their neighbour's channel, odd
+                    // lanes token j + 1: 4 bytes (16-bit outputs) of two rows at a time
+                    dst += (lane & 1) ? next - 2 : 0;
+#pragma unroll
+                    for (int j = 0; j < CH; j += 2) {
+                        const float x = value(j), y = value(j + 1);
+                        const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? x : y, 1);
+                        const float lo = (lane & 1) ? other : x, hi = (lane & 1) ? y : other;
+                        if (mine && j + (lane & 1) < count) {
+                            if (p.m.out_dt == kF16) {
+                                *reinterpret_cast<__half2*>(dst) = __floats2half2_rn(lo, hi);
+                            } else {
+                                *reinterpret_cast<__nv_bfloat162*>(dst) = __floats2bfloat162_rn(lo, hi);
+                            }
+                        }
+                        dst += 2 * next;
+                    }
+                    return;
+                }
 #pragma unroll
                 for (int j = 0; j < CH; ++j) {
-                    const int t = t0 + c + j;
-                    if (t >= p.m.tokens) break;
-                    const float sum = (INT8 ? __int2float_rn((int)v[j]) : __uint_as_float(v[j])) + nan;
-                    store_out(p.m.out, (int64_t)t * p.m.n + ch, scaled(sum, __ldg(p.m.sa + t), sw, bias), p.m.out_dt);
+                    const float y = value(j);
+                    if (mine && j < count) store_out(dst, 0, y, p.m.out_dt);
+                    dst += next;
                 }
             };
             if constexpr (INT8) {
@@ -267,17 +415,18 @@ matmul_tc_kernel(TcP p, const __grid_constant__ CUtensorMap wmap, const __grid_c
                     tc_after();
 #pragma unroll
                     for (int c = 0; c < H; c += CH) {
+                        if (c >= h) continue;
                         uint32_t v[CH];
-                        load(lanes + buf * NT + c, v);
+                        tc_ld16(lanes + buf * NT + c, v);
+                        tc_wait_ld();
 #pragma unroll
                         for (int j = 0; j < CH; ++j) acc[c + j] += (uint32_t)__float2int_rn(__uint_as_float(v[j]));
                     }
-                    tc_before();
-                    __syncwarp();
-                    if (lane == 0) bar_arrive(smem_addr(&sh.taken[buf]));
+                    release(buf);
                 }
 #pragma unroll
                 for (int c = 0; c < H; c += CH) {
+                    if (c >= h) continue;
                     uint32_t v[CH];
 #pragma unroll
                     for (int j = 0; j < CH; ++j) v[j] = acc[c + j];
@@ -288,52 +437,96 @@ matmul_tc_kernel(TcP p, const __grid_constant__ CUtensorMap wmap, const __grid_c
                 bar_wait(smem_addr(&sh.sum[buf]), (unit >> 1) & 1, failed);
                 tc_after();
 #pragma unroll 1
-                for (int c = 0; c < H; c += CH) {
+                for (int c = 0; c < h; c += CH) {
                     uint32_t v[CH];
-                    load(lanes + buf * NT + c, v);
+                    tc_ld16(lanes + buf * NT + c, v);
+                    tc_wait_ld();
                     give(c, v);
                 }
-                tc_before();
-                __syncwarp();
-                if (lane == 0) bar_arrive(smem_addr(&sh.taken[buf]));
+                release(buf);
                 ++unit;
             }
         }
     } else if constexpr (INT8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-        // ---- widening: a 16-byte piece of a row to two of fp16, stored with the 128-byte
-        // swizzle that the products read
-        const int mine = tid - 384;
-        uint32_t n = 0;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"((int)C::kRegsWide));
+        // ---- widening.  Groups of four warps take the halves of the entries in turn.
+        // Weights: a thread's row to its lane of TMEM, two numbers to a column.  Tokens: a
+        // 16-byte piece of half a row to two of fp16, both with the 128-byte swizzle; eight
+        // threads take four pieces of rows r and r + 4, and those of r + 4 store their
+        // second piece first, so that loads and stores are free of bank conflicts.
+        const int group = (wid - 4 - SW) >> 2, quad = wid & 3, mine = tid & 127;
+        const uint32_t wrow = ring + mine * 128, wx = (uint32_t)(mine & 7);
+        const uint32_t wlane = tmem_w + ((uint32_t)(quad * 32) << 16);
+        const int odd = (mine >> 2) & 1, r = odd * 4 + ((mine >> 3) & 3) + (mine >> 5) * 8, c = mine & 3;
+        const uint32_t from = ring + kRows * kStep + r * 128 + ((c ^ (r & 7)) << 4);
+        const uint32_t to = wides + r * 128 + (((c * 2 + odd) ^ (r & 7)) << 4);
+        const int pieces = part * 4;
+        uint32_t n = 0, st = 0, full = 0;
         for (int i = first; i < tiles; i += step) {
-            for (int e = e0; e < e1; ++e, ++n) {
-                const uint32_t st = n % ST, wd = n % WD;
-                bar_wait(smem_addr(&sh.full[st]), (n / ST) & 1, failed);
-                bar_wait(smem_addr(&sh.narrow[wd]), ((n / WD) & 1) ^ 1, failed);
-                const uint32_t src = ring + st * C::kRaw, dst = wides + wd * C::kWide;
-#pragma unroll 2
-                for (int q = mine; q < (kRows + NT) * 4; q += 256) {
-                    uint4 v;
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(src + q * 16) : "memory");
-                    const int r = q >> 2, c = (q & 3) * 2;
-                    uint32_t o[8];
-                    widen4(v.x, o[0], o[1]);
-                    widen4(v.y, o[2], o[3]);
-                    widen4(v.z, o[4], o[5]);
-                    widen4(v.w, o[6], o[7]);
+            for (int e = 2 * e0; e < 2 * e1; ++e, ++n) {
+                if ((int)(n % C::kGroups) == group) {
+                    const uint32_t wd = n % WD;
+                    bar_wait(smem_addr(&sh.full[st]), full, failed);
+                    bar_wait(smem_addr(&sh.narrow[wd]), ((n / WD) & 1) ^ 1, failed);
+                    tc_after();
+                    const uint32_t entry = st * C::kRaw, half = n & 1;
+                    const uint32_t src = (from + entry) ^ (half << 6), dst = to + wd * C::kWide;
+                    // every load before the first number is turned
+                    constexpr int EACH = C::kTokens * 4 / 128 > 0 ? C::kTokens * 4 / 128 : 1;
+                    uint4 x[4], v[EACH];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t at = dst + r * 128 + (((c + h) ^ (r & 7)) << 4);
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(o[4 * h]), "r"(o[4 * h + 1]), "r"(o[4 * h + 2]), "r"(o[4 * h + 3]) : "memory");
+                    for (int b = 0; b < 4; ++b) x[b] = lds_vector(wrow + entry + (((half * 4 + b) ^ wx) << 4));
+#pragma unroll
+                    for (int u = 0; u < EACH; ++u) {
+                        if (mine + 128 * u < pieces) v[u] = lds_vector(src + u * 4096);
+                    }
+#pragma unroll
+                    for (int b = 0; b < 4; b += 2) {
+                        uint32_t o[16];
+                        widen4(x[b].x, o[0], o[1]);
+                        widen4(x[b].y, o[2], o[3]);
+                        widen4(x[b].z, o[4], o[5]);
+                        widen4(x[b].w, o[6], o[7]);
+                        widen4(x[b + 1].x, o[8], o[9]);
+                        widen4(x[b + 1].y, o[10], o[11]);
+                        widen4(x[b + 1].z, o[12], o[13]);
+                        widen4(x[b + 1].w, o[14], o[15]);
+                        tc_st16(wlane + wd * 32 + b * 8, o);
+                    }
+#pragma unroll
+                    for (int u = 0; u < EACH; ++u) {
+                        if (mine + 128 * u < pieces) {
+                            uint4 lo, hi;
+                            widen4(odd ? v[u].z : v[u].x, lo.x, lo.y);
+                            widen4(odd ? v[u].w : v[u].y, lo.z, lo.w);
+                            widen4(odd ? v[u].x : v[u].z, hi.x, hi.y);
+                            widen4(odd ? v[u].y : v[u].w, hi.z, hi.w);
+                            sts_vector(dst + u * 4096, lo);
+                            sts_vector((dst + u * 4096) ^ 16, hi);
+                        }
+                    }
+                    tc_wait_st();
+                    tc_before();
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (PAIR) {
+                            cluster_bar_arrive(peer_addr(smem_addr(&sh.wide[wd]), 0));
+                        } else {
+                            bar_arrive(smem_addr(&sh.wide[wd]));
+                        }
+                        bar_arrive(smem_addr(&sh.empty[st]));
                     }
                 }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    bar_arrive(smem_addr(&sh.empty[st]));
-                    bar_arrive(smem_addr(&sh.wide[wd]));
+                if ((n & 1) && ++st == ST) {
+                    st = 0;
+                    full ^= 1;
                 }
             }
+        }
+        if constexpr (PAIR) {
+            // the other CTA's last arrivals on this one's barriers
+            for (int i = 0; i < WD; ++i, ++n) bar_wait(smem_addr(&sh.narrow[n % WD]), ((n / WD) & 1) ^ 1, failed);
         }
     }
     tc_before();
@@ -344,39 +537,51 @@ matmul_tc_kernel(TcP p, const __grid_constant__ CUtensorMap wmap, const __grid_c
         }
         __syncthreads();
     }
+    if constexpr (PAIR) cluster_sync();  // products read both CTAs' memory until here
     if (wid == 1) {
         tc_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::kColumns) : "memory");
+        if constexpr (PAIR) {
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::kColumns) : "memory");
+        } else {
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::kColumns) : "memory");
+        }
     }
-    if (split > 1) {
+    if (!PAIR && split > 1) {
+        // the parts lie where the ring was, [token][channel]; every product is done
+        __syncwarp();
         cluster_sync();
-        if (wid >= 4 && wid < 12) {
-            // this CTA's share of the tile's tokens, summed over the parts in rank order
-            // (on the warps that have the registers)
+        if (wid >= 4 && wid < 4 + SW) {
+            // this CTA's share of the tile's tokens, the parts added in rank order (on the
+            // warps that have the registers); a lane has four channels of a token, a warp
+            // all
             int tn, tt;
             tile_at(p, first, tn, tt);
-            const int row = tid & 127, ch = tn * kRows + row;
-            const int c0 = NT * rank / split, c1 = NT * (rank + 1) / split;
+            const int c0 = NT * rank / split, c1 = min(NT * (rank + 1) / split, p.m.tokens - tt * NT);
+            const int ch = tn * kRows + lane * 4;
             float nan = 0.0f;
-            for (int r = 0; r < split; ++r) nan = peer_word(smem_addr(&sh.failed), r) ? NAN : nan;
-            const bool mine = ch < p.m.n;
-            const float sw = mine ? __ldg(p.m.sw + ch) : 0.0f;
-            const float bias = mine && p.m.bias != nullptr ? load_out(p.m.bias, ch, p.m.out_dt) : 0.0f;
-            for (int c = c0 + ((wid - 4) >> 2); c < c1; c += 2) {
-                const int t = tt * NT + c;
-                if (!mine || t >= p.m.tokens) break;
-                float sum = 0.0f;
-                int whole = 0;
-                for (int r = 0; r < split; ++r) {
-                    const uint32_t v = peer_word(base + (uint32_t)((c * kRows + row) * 4), r);
-                    if constexpr (INT8) {
-                        whole += (int)v;
-                    } else {
-                        sum = __fadd_rn(sum, __uint_as_float(v));
-                    }
+            for (int r = 0; r < split; ++r) nan = peer_word(peer_addr(smem_addr(&sh.failed), r)) ? NAN : nan;
+            for (int c = c0 + (wid - 4); c < c1; c += SW) {
+                uint4 v[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    v[r] = make_uint4(0u, 0u, 0u, 0u);
+                    if (r < split) v[r] = peer_vector(peer_addr(base + (uint32_t)((c * kRows + lane * 4) * 4), r));
                 }
-                if constexpr (INT8) sum = __int2float_rn(whole);
-                store_out(p.m.out, (int64_t)t * p.m.n + ch, scaled(sum + nan, __ldg(p.m.sa + t), sw, bias), p.m.out_dt);
+                const float sa = __ldg(p.m.sa + tt * NT + c);
+                char* dst = p.m.out + ((int64_t)(tt * NT + c) * p.m.n + ch) * (p.m.out_dt == kF32 ? 4 : 2);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t sum = 0u;
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                        const uint32_t x = reinterpret_cast<const uint32_t*>(&v[r])[j];
+                        sum = INT8 ? sum + x : __float_as_uint(__fadd_rn(__uint_as_float(sum), __uint_as_float(x)));
+                    }
+                    if (ch + j >= p.m.n) continue;
+                    const float y = INT8 ? __int2float_rn((int)sum) : __uint_as_float(sum);
+                    const float bias = p.m.bias != nullptr ? load_out(p.m.bias, ch + j, p.m.out_dt) : 0.0f;
+                    store_out(dst, j, scaled(y + nan, sa, __ldg(p.m.sw + ch + j), bias), p.m.out_dt);
+                }
             }
         }
         cluster_sync();  // peers read this CTA's shared memory until here
@@ -385,59 +590,129 @@ matmul_tc_kernel(TcP p, const __grid_constant__ CUtensorMap wmap, const __grid_c
 
 // ---------------------------------------------------------------- launch
 
-bool operand_map(CUtensorMap* map, const char* base, int rows, int k, int box_rows, int box_k, bool swizzle) {
+bool operand_map(CUtensorMap* map, const char* base, int rows, int k, int box_rows) {
     const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)k};
-    const cuuint32_t box[2] = {(cuuint32_t)box_k, (cuuint32_t)box_rows};
+    const cuuint32_t box[2] = {kStep, (cuuint32_t)box_rows};
     const cuuint32_t ones[2] = {1, 1};
     return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<char*>(base), dims, strides, box, ones,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool INT8, int NT>
-cudaError_t launch_tile(const MatmulP& m, int split, cudaLaunchConfig_t cfg) {
-    using C = Mm<INT8, NT>;
+// How a call is cut: tiles of nt tokens by one CTA (split over a cluster) or a pair.
+struct Cut {
+    bool pair;
+    int nt, split;
+};
+
+template <bool INT8, int NT, bool PAIR>
+cudaError_t launch_tile(const MatmulP& m, const Cut& cut, cudaLaunchConfig_t cfg) {
+    using C = Mm<INT8, NT, PAIR>;
+    const void* fn = (const void*)matmul_tc_kernel<INT8, NT, PAIR>;
+    constexpr int TILE = PAIR ? 2 * kRows : kRows;
+    const int nt = cut.nt;
     TcP p;
     p.m = m;
-    p.tiles_n = (m.n + kRows - 1) / kRows;
-    p.tiles_t = (m.tokens + NT - 1) / NT;
-    p.split = split;
+    p.nt = nt;
+    p.tiles_n = (m.n + TILE - 1) / TILE;
+    p.tiles_t = (m.tokens + nt - 1) / nt;
+    p.pairs = m.out_dt != kF32 && m.n % 2 == 0 && reinterpret_cast<uintptr_t>(m.out) % 4 == 0;
     CUtensorMap wmap, amap;
-    if (!operand_map(&wmap, m.w, m.n, m.k, kRows, C::kStep, !INT8) ||
-        !operand_map(&amap, m.a, m.tokens, m.k, NT, C::kStep, !INT8)) {
+    if (!operand_map(&wmap, m.w, m.n, m.k, kRows) || !operand_map(&amap, m.a, m.tokens, m.k, PAIR ? nt / 2 : nt)) {
         return cudaErrorInvalidValue;
     }
-    const cudaError_t e = allow_smem((const void*)matmul_tc_kernel<INT8, NT>, C::kSmem);
+    const cudaError_t e = allow_smem(fn, C::kSmem);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = (int64_t)p.tiles_n * p.tiles_t;
-    const int sms = sm_count();
-    cfg.gridDim = dim3((unsigned)(split > 1 ? tiles * split : tiles < sms ? tiles : sms));
     cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kSmem;
-    if (split > 1) {
+    const int64_t tiles = (int64_t)p.tiles_n * p.tiles_t;
+    int cluster = 2;
+    int64_t slots = (int64_t)sm_count() * C::kCtas;
+    if constexpr (PAIR) {
+        slots = resident_clusters(fn, cfg, 2);
+        if (slots < 1) return cudaErrorInvalidConfiguration;
+    } else {
+        cluster = cut.split;
+        while (cluster > 1 && tiles > resident_clusters(fn, cfg, cluster)) --cluster;
+    }
+    p.split = PAIR ? 1 : cluster;
+    cfg.gridDim = dim3((unsigned)(cluster * (p.split > 1 || tiles < slots ? tiles : slots)));
+    if (cluster > 1) {
         cfg.attrs[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-        cfg.attrs[cfg.numAttrs].val.clusterDim.x = (unsigned)split;
+        cfg.attrs[cfg.numAttrs].val.clusterDim.x = (unsigned)cluster;
         cfg.attrs[cfg.numAttrs].val.clusterDim.y = 1;
         cfg.attrs[cfg.numAttrs].val.clusterDim.z = 1;
         ++cfg.numAttrs;
     }
-    return cudaLaunchKernelEx(&cfg, matmul_tc_kernel<INT8, NT>, p, wmap, amap);
+    return cudaLaunchKernelEx(&cfg, matmul_tc_kernel<INT8, NT, PAIR>, p, wmap, amap);
+}
+
+// The quickest cut by a model of the times in us, whose numbers are fits to
+// measurements on GB300 (back-to-back launches, weights from memory; 1 to 4096 tokens,
+// 1024 to 19,456 channels, sums of 1024 to 9728 terms):
+//   a ring entry (128 terms)
+//     E4M3: the bytes that an SM takes in, 110 GB/s; a pair's products need 1.25 ns a
+//     token
+//     int8: widening, 0.35 us (one CTA, 64 tokens 0.44) and 0.47 to 0.55 us (pair)
+//   a launch with its first fetch and last store: 2.4 to 5 us and some ns a token
+//   the sum over a cluster: 2 us and 30 ns a token
+// The time that memory takes for the weights (5.5 TB/s) runs beside the entries, the
+// longer of the two and a quarter of the other count.  Over 32 drawn calls its choices took
+// 0.97 (E4M3) and 0.98 (int8) of the best of a sweep of 18 cuts each in the geometric mean,
+// at worst 1.06.  Measured around them: 2560 x 9728 in E4M3, 64 tokens, 11.1 us split over six CTAs against
+// 21.4 unsplit and 17.5 by pairs of 96 tokens; 1024 tokens, 21.5 us with pairs of 160
+// tokens (70 tiles on 76 pairs) against 27.4 with 256 (40 tiles) and 29.4 with 128 (80).
+template <bool INT8>
+Cut choose(const MatmulP& m) {
+    const double sms = sm_count();
+    const int entries = (m.k + kStep - 1) / kStep;
+    const double memory = ((double)m.n * m.k + (double)m.tokens * m.k) / 5.5e6;
+    Cut best = {false, 16, 1};
+    double least = 1e30;
+    auto consider = [&](const Cut& c) {
+        const double tile = c.pair ? 2 * kRows : kRows;
+        const double tiles = std::ceil(m.n / tile) * std::ceil((double)m.tokens / c.nt);
+        const double rounds = std::ceil(tiles * (c.pair ? 2 : c.split) / sms);
+        double entry, ends;
+        if (INT8) {
+            entry = c.pair ? 0.45 + 0.0005 * c.nt : c.nt <= 32 ? 0.35 : 0.44;
+            ends = c.pair ? 5.0 + 0.01 * c.nt : 3.6 + 0.02 * c.nt;
+        } else {
+            entry = c.pair ? std::fmax((kRows + c.nt / 2) * 0.00117, c.nt * 0.00125) : (kRows + c.nt) * 0.00117;
+            ends = c.pair ? 3.0 + 0.008 * c.nt : 2.4 + 0.01 * c.nt;
+        }
+        if (c.split > 1) ends += 2.0 + 0.03 * c.nt;
+        const double work = rounds * std::ceil((double)entries / c.split) * entry;
+        const double t = ends + std::fmax(work, memory) + 0.25 * std::fmin(work, memory);
+        if (t < least) {
+            least = t;
+            best = c;
+        }
+    };
+    for (int nt = 16; nt <= 64; nt *= 2) {
+        if (nt > 16 && m.tokens <= nt / 2) break;
+        const int64_t tiles = (int64_t)((m.n + kRows - 1) / kRows) * ((m.tokens + nt - 1) / nt);
+        for (int split = 1; split <= 8; ++split) {
+            // at least 4 entries for each CTA, and all CTAs at once
+            if (split > 1 && (split * 4 > entries || tiles * split > (int64_t)sms)) break;
+            consider(Cut{false, nt, split});
+        }
+    }
+    for (int nt = 32; nt <= (INT8 ? 192 : 256); nt += 32) {
+        if (m.tokens <= 32 || (nt > 32 && m.tokens <= nt - 32)) break;
+        consider(Cut{true, nt, 1});
+    }
+    return best;
 }
 
 template <bool INT8>
 cudaError_t launch_kind(const MatmulP& m, cudaLaunchConfig_t cfg) {
-    const int sms = sm_count();
-    const int nt = m.tokens <= 32 ? 32 : m.tokens <= 64 ? 64 : m.tokens <= 128 ? 128 : 256;
-    const int64_t tiles = (int64_t)((m.n + kRows - 1) / kRows) * ((m.tokens + nt - 1) / nt);
-    const int entries = (m.k + (INT8 ? 63 : 127)) / (INT8 ? 64 : 128);
-    int split = 1;
-    while (split < 8 && tiles * (split + 1) <= sms && (split + 1) * 4 <= entries) ++split;
-    if (split == 7 || split == 5) --split;
-    if (nt == 32) return launch_tile<INT8, 32>(m, split, cfg);
-    if (nt == 64) return launch_tile<INT8, 64>(m, split, cfg);
-    if (nt == 128) return launch_tile<INT8, 128>(m, split, cfg);
-    return launch_tile<INT8, 256>(m, split, cfg);
+    const Cut cut = choose<INT8>(m);
+    if (cut.pair) return launch_tile<INT8, INT8 ? 192 : 256, true>(m, cut, cfg);
+    if (cut.nt == 16) return launch_tile<INT8, 16, false>(m, cut, cfg);
+    if (cut.nt == 32) return launch_tile<INT8, 32, false>(m, cut, cfg);
+    return launch_tile<INT8, 64, false>(m, cut, cfg);
 }
 
 }  // namespace

@@ -13,7 +13,14 @@ SHAPES = [(1, 1, 1), (3, 5, 7), (2, 33, 20), (65, 70, 33), (130, 129, 100), (17,
           (1, 16, 16), (1, 2560, 2560), (2, 4100, 1040), (4, 512, 9728), (7, 1000, 48), (8, 128, 128),
           (9, 640, 2048), (16, 272, 4096), (17, 128, 1024), (33, 2560, 9728), (64, 1152, 1040), (65, 384, 144),
           (100, 257, 2064), (128, 130, 1024), (129, 512, 1200), (200, 6144, 2560), (256, 128, 4112), (257, 640, 512),
-          (1000, 1024, 1040), (1201, 5120, 2048), (300, 131, 16), (2048, 2304, 1536)]
+          (1000, 1024, 1040), (1201, 5120, 2048), (300, 131, 16), (2048, 2304, 1536),
+          # the cuts of the tensor-memory kernel: 16, 32 and 64 tokens by one CTA, unsplit and over clusters of 2 to
+          # 8, and pairs with 32 to 256 tokens in steps of 32
+          (1243, 131, 144), (546, 5450, 32), (17, 3661, 3872), (9, 64, 1488), (9, 69, 1968), (9, 64, 2592),
+          (9, 74, 2960), (9, 66, 3856), (9, 68, 4000), (609, 138, 3824), (246, 131, 4672), (862, 132, 4752),
+          (1248, 135, 2992), (834, 132, 2592), (65, 3853, 4736), (1230, 136, 3968), (1242, 391, 1568), (1409, 5014, 32),
+          (588, 2592, 528), (985, 5335, 144), (500, 4957, 672), (582, 5635, 544), (677, 5029, 928), (1424, 5915, 32),
+          (521, 4906, 272)]
 
 
 def operands(t, n, k, fp8, seed=0):

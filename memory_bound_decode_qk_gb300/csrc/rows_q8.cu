@@ -24,9 +24,8 @@
 // written: the kernels are bound by HBM, and at few rows by one memory round trip.
 // As in rows.cu a row stays in registers from its load to its store: a CTA is
 // (32 W) x R threads, W warps share a row and every load of a thread is issued
-// before any arithmetic.  The norm forms its products twice (once for the maximum,
-// once for the codes) rather than hold them; the gate holds them in fp32, since
-// its exponentials cost more than the registers.  Rows longer than a CTA holds, or
+// before any arithmetic.  The products are held in fp32 from the maximum to the
+// codes.  Rows longer than a CTA holds, or
 // of a length or alignment that 16-byte vectors do not suit, take a two-pass
 // kernel of one CTA per row.
 #include "edge_common.cuh"
@@ -56,7 +55,12 @@ struct RowsQ8P {
 
 // ---------------------------------------------------------------- maximum and codes
 
-// max(a, |b|) in which NaN stays NaN.
+// max(a, |b|, |c|) in which NaN stays NaN.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+    float y;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
 __device__ __forceinline__ float max_abs(float a, float b) {
     float y;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(fabsf(b)));
@@ -73,18 +77,14 @@ __device__ __forceinline__ float warp_max(float v) {
 constexpr float kStepFloor = 1.1754943508222875e-38f;  // 2^-126
 constexpr float kInvCeiling = 8.507059173023462e37f;   // 2^126
 
-struct Steps {
-    float inv, step;
-};
 // Both quotients are IEEE divisions: a plain evaluation of the formulas gives the
 // same codes.
-__device__ __forceinline__ Steps steps_of(float most, int fp8) {
-    const float top = fp8 ? 448.0f : 127.0f;
-    Steps s;
-    s.inv = fminf(__fdiv_rn(top, most), kInvCeiling);
-    s.step = __fdiv_rn(most, top);
-    if (s.step < kStepFloor) s.step = kStepFloor;  // (NaN stays)
-    return s;
+__device__ __forceinline__ float inverse_of(float most, int fp8) {
+    return fminf(__fdiv_rn(fp8 ? 448.0f : 127.0f, most), kInvCeiling);
+}
+__device__ __forceinline__ float step_of(float most, int fp8) {
+    const float step = __fdiv_rn(most, fp8 ? 448.0f : 127.0f);
+    return step < kStepFloor ? kStepFloor : step;  // (NaN stays)
 }
 
 // Four int8 codes of y * inv (at most 127 and a little in size): adding 1.5 * 2^23 in
@@ -159,63 +159,47 @@ __global__ void __launch_bounds__(512) rows_q8_kernel(RowsQ8P p) {
         if constexpr (NORM) wr[i] = ok && wv != nullptr ? __ldg(wv + idx) : zero;
     }
 
-    // products of vector i (the norm's sums, or the gate's values where they are held)
-    float2 held[GATE ? V : 1][P];
-    const float2 delta = splat2(p.delta);
-    auto products = [&](int i, float2 (&y)[P]) {
-        if constexpr (GATE) {
-#pragma unroll
-            for (int j = 0; j < P; ++j) y[j] = held[i][j];
-        } else {
-            unpack_pairs<T, N>(xv[i], y);
-            if constexpr (NORM) {
-                if (wv != nullptr) {
-                    float2 w[P];
-                    unpack_pairs<T, N>(wr[i], w);
-#pragma unroll
-                    for (int j = 0; j < P; ++j) y[j] = __fmul2_rn(y[j], __fadd2_rn(w[j], delta));
-                }
-            }
-        }
-    };
-
-    // the sum of squares runs in the two lanes of a pair, and beyond 32 terms per
-    // thread in two pairs alternating by vector
+    // the products are held from here to the codes.  The sum of squares runs in the two
+    // lanes of a pair, and beyond 32 terms per thread in two pairs alternating by vector
     constexpr bool kSplit = V * N > 32;
+    const float2 delta = splat2(p.delta);
+    float2 y[V][P];
     float2 ss[2] = {splat2(0.0f), splat2(0.0f)};
-    float2 most = splat2(0.0f);
+    float most = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        float2 a[P];
+        unpack_pairs<T, N>(xv[i], y[i]);
         if constexpr (ADD) {
             // eager semantics: widen, add in fp32, round once to the dtype
             float2 b[P];
-            unpack_pairs<T, N>(xv[i], a);
             unpack_pairs<T, N>(yv[i], b);
 #pragma unroll
-            for (int j = 0; j < P; ++j) a[j] = __fadd2_rn(a[j], b[j]);
-            xv[i] = pack_pairs<T, N>(a);
+            for (int j = 0; j < P; ++j) y[i][j] = __fadd2_rn(y[i][j], b[j]);
+            const uint4 sum = pack_pairs<T, N>(y[i]);
             const int idx = tid + i * tpr;
-            if (active && idx < p.nvec) rr[idx] = xv[i];
+            if (active && idx < p.nvec) rr[idx] = sum;
+            unpack_pairs<T, N>(sum, y[i]);
         }
         if constexpr (NORM) {
-            unpack_pairs<T, N>(xv[i], a);
 #pragma unroll
-            for (int j = 0; j < P; ++j) ss[kSplit ? (i & 1) : 0] = __ffma2_rn(a[j], a[j], ss[kSplit ? (i & 1) : 0]);
+            for (int j = 0; j < P; ++j) {
+                ss[kSplit ? (i & 1) : 0] = __ffma2_rn(y[i][j], y[i][j], ss[kSplit ? (i & 1) : 0]);
+            }
+            if (wv != nullptr) {
+                float2 w[P];
+                unpack_pairs<T, N>(wr[i], w);
+#pragma unroll
+                for (int j = 0; j < P; ++j) y[i][j] = __fmul2_rn(y[i][j], __fadd2_rn(w[j], delta));
+            }
         }
         if constexpr (GATE) {
             float2 u[P];
-            unpack_pairs<T, N>(xv[i], a);
             unpack_pairs<T, N>(yv[i], u);
 #pragma unroll
-            for (int j = 0; j < P; ++j) held[i][j] = gate_fast2<KIND == kGateSilu ? kSilu : kGelu>(a[j], u[j]);
+            for (int j = 0; j < P; ++j) y[i][j] = gate_fast2<KIND == kGateSilu ? kSilu : kGelu>(y[i][j], u[j]);
         }
-        products(i, a);
 #pragma unroll
-        for (int j = 0; j < P; ++j) {
-            most.x = max_abs(most.x, a[j].x);
-            most.y = max_abs(most.y, a[j].y);
-        }
+        for (int j = 0; j < P; ++j) most = max_abs(most, y[i][j].x, y[i][j].y);
     }
     // over the warps that share the row: sum and maximum with one barrier
     float sum = 0.0f;
@@ -223,7 +207,7 @@ __global__ void __launch_bounds__(512) rows_q8_kernel(RowsQ8P p) {
         const float2 s2 = kSplit ? __fadd2_rn(ss[0], ss[1]) : ss[0];
         sum = group_sum<32>(__fadd_rn(s2.x, s2.y));
     }
-    float top = warp_max(max_abs(most.x, most.y));
+    float top = warp_max(most);
     const int W = tpr >> 5;
     if ((tid & 31) == 0) red[(threadIdx.y * tpr + tid) >> 5] = make_float2(sum, top);
     __syncthreads();
@@ -233,19 +217,17 @@ __global__ void __launch_bounds__(512) rows_q8_kernel(RowsQ8P p) {
         if constexpr (NORM) sum = __fadd_rn(sum, v.x);
         top = max_abs(top, v.y);
     }
-    const Steps st = steps_of(top, p.fp8);
     if (tid == 0 && active) {
-        p.scales[row] = NORM ? __fmul_rn(inv_rms(sum, p.inv_n, p.eps), st.step) : st.step;
+        const float step = step_of(top, p.fp8);
+        p.scales[row] = NORM ? __fmul_rn(inv_rms(sum, p.inv_n, p.eps), step) : step;
     }
-
+    const float inv = inverse_of(top, p.fp8);
     char* orow = p.out + rsafe * p.n;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int idx = tid + i * tpr;
         if (!(active && idx < p.nvec)) continue;
-        float2 y[P];
-        products(i, y);
-        auto c = codes_of<N>(y, st.inv, p.fp8);
+        auto c = codes_of<N>(y[i], inv, p.fp8);
         reinterpret_cast<decltype(c)*>(orow)[idx] = c;
     }
 }
@@ -304,13 +286,14 @@ __global__ void __launch_bounds__(256) rows_q8_any_kernel(RowsQ8P p) {
             top = max_abs(top, red_top[k]);
         }
         __syncthreads();
-        const Steps st = steps_of(top, p.fp8);
         if (threadIdx.x == 0) {
-            p.scales[row] = NORM ? __fmul_rn(inv_rms((float)ss, p.inv_n, p.eps), st.step) : st.step;
+            const float step = step_of(top, p.fp8);
+            p.scales[row] = NORM ? __fmul_rn(inv_rms((float)ss, p.inv_n, p.eps), step) : step;
         }
+        const float inv = inverse_of(top, p.fp8);
         uint8_t* out = reinterpret_cast<uint8_t*>(p.out) + row * p.n;
         for (int i = threadIdx.x; i < p.n; i += blockDim.x) {
-            out[i] = code_of(product(i, ADD ? to_f(res[i]) : to_f(x[i])), st.inv, p.fp8);
+            out[i] = code_of(product(i, ADD ? to_f(res[i]) : to_f(x[i])), inv, p.fp8);
         }
     }
 }
@@ -334,19 +317,38 @@ cudaError_t launch_kind(const RowsQ8Args& a, RowsQ8P& p, cudaStream_t s) {
     const bool vec = a.n % N == 0 && aligned(a.x, 16) && aligned(a.residual, 16) && aligned(a.w, 16) &&
                      aligned(a.out, N) && nvec <= 16 * 32 * 8;
     if (vec) {
-        const int vt = a.rows >= 2 * sms ? 2 : 1;
-        int W = (int)((nvec + 32 * vt - 1) / (32 * vt));
-        if (W > 16) W = 16;
-        const int64_t per = (nvec + 32 * W - 1) / (32 * W);
-        const int R = 256 / (32 * W) > 1 ? 256 / (32 * W) : 1;
+        // Vectors per thread.  With few rows, or few vectors in all, as many warps to a row
+        // as it fills (one vector each); else the number with the least cost for a vector: a
+        // warp's reduction and divisions count for 0.88 of the work on one vector, spread
+        // over V, and lanes behind the row's end are lost (8, for the longest rows, leaves two
+        // CTAs of 16 warps on an SM).  Measured on GB300: the norm of
+        // 4096 rows of 4096 bf16 takes 11.0 us with V = 4, 12.9 with 2 and 17.0 with 1, of
+        // 1024 rows of 2560 (320 vectors, a sixth of the lanes lost with 3 or 4) 2.9 with 2 and
+        // 3.4 with 4; the gate of 512 rows of 2048 2.4 with 1 and 3.0 with 4, of 4096 rows of
+        // 9728 34.7 with 4, 39.9 with 3 and 47.4 with rows of 16 warps.
+        int V = 8, W = 16;
+        double least = 1e30;
+        const bool few = a.rows < 2 * (int64_t)sms || a.rows * nvec < 1024 * (int64_t)sms;
+        for (int v = 1; v <= 4; ++v) {
+            const int w = (int)((nvec + 32 * v - 1) / (32 * v));
+            if (w > 16) continue;
+            const double cost = few ? v : (1.0 + 0.88 / v) * w * v;
+            if (cost < least) {
+                least = cost;
+                V = v;
+                W = w;
+            }
+        }
+        const int R = 128 / (32 * W) > 1 ? 128 / (32 * W) : 1;
         const int64_t blocks = (a.rows + R - 1) / R;
         if (blocks <= (int64_t)INT32_MAX) {
             p.nvec = (int)nvec;
             cfg.gridDim = dim3((unsigned)blocks);
             cfg.blockDim = dim3(32 * W, R);
-            switch (per <= 1 ? 1 : per <= 2 ? 2 : per <= 4 ? 4 : 8) {
+            switch (V) {
                 case 1: return cudaLaunchKernelEx(&cfg, rows_q8_kernel<T, KIND, 1>, p);
                 case 2: return cudaLaunchKernelEx(&cfg, rows_q8_kernel<T, KIND, 2>, p);
+                case 3: return cudaLaunchKernelEx(&cfg, rows_q8_kernel<T, KIND, 3>, p);
                 case 4: return cudaLaunchKernelEx(&cfg, rows_q8_kernel<T, KIND, 4>, p);
                 default: return cudaLaunchKernelEx(&cfg, rows_q8_kernel<T, KIND, 8>, p);
             }

@@ -664,6 +664,11 @@ _CODES = {False: (torch.int8,), True: (torch.uint8, torch.float8_e4m3fn)}
 _CODE_KIND = {torch.int8: INT8, torch.uint8: FP8_E4M3, torch.float8_e4m3fn: FP8_E4M3}
 
 
+def _stream_of(index):
+    """The current stream's raw handle on device `index`, the current one."""
+    return _RAW_STREAM(index) if _RAW_STREAM is not None else torch.cuda.current_stream().cuda_stream
+
+
 def _q8_fits(at, x, n, shape, fp8, out, scales):
     """Whether x, and out and scales where given, suit a call that turns the rows of x
     into n codes each, of shape `shape` in all."""
@@ -718,9 +723,9 @@ def rmsnorm_q8(x, w=None, *, eps=1e-6, weight_offset=0, fp8=False, out=None, sca
     rows = scales.numel()
     if rows == 0:
         return out, scales  # (an empty tensor has no address to pass on)
-    st = lib().edge_rmsnorm_q8(out.data_ptr(), FP8_E4M3 if fp8 else INT8, scales.data_ptr(),
+    st = (_LIB or lib()).edge_rmsnorm_q8(out.data_ptr(), FP8_E4M3 if fp8 else INT8, scales.data_ptr(),
                                x.data_ptr(), _ptr(w), dt, rows, n, eps, weight_offset,
-                               _stream(None))
+                               _stream_of(at))
     if st:
         raise EdgeError(st, "edge_rmsnorm_q8")
     return out, scales
@@ -747,9 +752,9 @@ def add_rmsnorm_q8(x, residual, w=None, *, eps=1e-6, weight_offset=0, fp8=False,
     rows = scales.numel()
     if rows == 0:
         return out, scales
-    st = lib().edge_add_rmsnorm_q8(out.data_ptr(), FP8_E4M3 if fp8 else INT8, scales.data_ptr(),
+    st = (_LIB or lib()).edge_add_rmsnorm_q8(out.data_ptr(), FP8_E4M3 if fp8 else INT8, scales.data_ptr(),
                                    x.data_ptr(), residual.data_ptr(), _ptr(w), dt, rows, n, eps,
-                                   weight_offset, _stream(None))
+                                   weight_offset, _stream_of(at))
     if st:
         raise EdgeError(st, "edge_add_rmsnorm_q8")
     return out, scales
@@ -773,8 +778,8 @@ def glu_act_q8(gate_up, act=SILU, *, fp8=False, out=None, scales=None, stream=No
     rows = scales.numel()
     if rows == 0:
         return out, scales
-    st = lib().edge_glu_act_q8(out.data_ptr(), FP8_E4M3 if fp8 else INT8, scales.data_ptr(),
-                               gate_up.data_ptr(), dt, rows, two_d // 2, act, _stream(None))
+    st = (_LIB or lib()).edge_glu_act_q8(out.data_ptr(), FP8_E4M3 if fp8 else INT8, scales.data_ptr(),
+                               gate_up.data_ptr(), dt, rows, two_d // 2, act, _stream_of(at))
     if st:
         raise EdgeError(st, "edge_glu_act_q8")
     return out, scales
@@ -794,8 +799,8 @@ def quantize_q8(x, *, fp8=False, out=None, scales=None, stream=None):
     rows = scales.numel()
     if rows == 0:
         return out, scales
-    st = lib().edge_quantize_q8(out.data_ptr(), FP8_E4M3 if fp8 else INT8, scales.data_ptr(),
-                                x.data_ptr(), dt, rows, n, _stream(None))
+    st = (_LIB or lib()).edge_quantize_q8(out.data_ptr(), FP8_E4M3 if fp8 else INT8, scales.data_ptr(),
+                                x.data_ptr(), dt, rows, n, _stream_of(at))
     if st:
         raise EdgeError(st, "edge_quantize_q8")
     return out, scales
@@ -830,9 +835,9 @@ def matmul_q8(a, w, a_scales, w_scales, *, bias=None, dtype=None, out=None, stre
     tokens = a_scales.numel()
     if tokens == 0:
         return out
-    st = lib().edge_matmul_q8(out.data_ptr(), dt, a.data_ptr(), w.data_ptr(), kind,
+    st = (_LIB or lib()).edge_matmul_q8(out.data_ptr(), dt, a.data_ptr(), w.data_ptr(), kind,
                               a_scales.data_ptr(), w_scales.data_ptr(), _ptr(bias), tokens, n, k,
-                              _stream(None))
+                              _stream_of(at))
     if st:
         raise EdgeError(st, "edge_matmul_q8")
     return out

@@ -2,6 +2,10 @@
 // channel (sm_103a): the choice of a kernel, and the kernel for any size.
 //
 //   out[t, j] = round((sum_i a[t, i] w[j, i]) sa[t] sw[j] + bias[j])
+//
+// Rows and addresses on 16 bytes take the stream of weights (matmul_q8_few.cu: up to 8
+// tokens and 16 MB of weights) or the tensor memory (matmul_q8_tc.cu); the rest the
+// kernel here.
 #include "matmul_common.cuh"
 
 namespace edge {
@@ -34,7 +38,7 @@ __device__ __forceinline__ float sum_of(uint32_t v) {
 // Tiles of 64 tokens x 64 channels, 64 bytes of the summed dimension at a time, on
 // the warp-level matrix instructions: 2 x 2 warps of 32 x 32 each.  The next bytes
 // are fetched into registers while the tile in shared memory is multiplied.  VW:
-// bytes of one load, which divide the row length and both addresses.
+// bytes of one load, 4 where they divide the row length and both addresses, else 1.
 constexpr int kTileAny = 64;
 constexpr int kRowAny = 80;  // bytes of a row in shared memory: fragments without bank conflicts
 
@@ -51,17 +55,7 @@ __global__ void __launch_bounds__(128) matmul_any_kernel(MatmulP p) {
     auto fetch = [&](const char* base, int r, int rows, int k0, uint32_t (&v)[8]) {
         const char* src = base + (int64_t)r * p.k;
         const bool ok = r < rows;
-        if constexpr (VW == 16) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int k = k0 + half + 16 * i;
-                const uint4 x = ok && k < p.k ? __ldg(reinterpret_cast<const uint4*>(src + k)) : make_uint4(0u, 0u, 0u, 0u);
-                v[4 * i] = x.x;
-                v[4 * i + 1] = x.y;
-                v[4 * i + 2] = x.z;
-                v[4 * i + 3] = x.w;
-            }
-        } else if constexpr (VW == 4) {
+        if constexpr (VW == 4) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int k = k0 + half + 4 * i;
@@ -157,7 +151,6 @@ cudaError_t launch_any(const MatmulP& p, cudaLaunchConfig_t cfg) {
     if (tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
     cfg.gridDim = dim3((unsigned)tiles);
     cfg.blockDim = dim3(128);
-    if (fits(16)) return cudaLaunchKernelEx(&cfg, matmul_any_kernel<INT8, 16>, p);
     if (fits(4)) return cudaLaunchKernelEx(&cfg, matmul_any_kernel<INT8, 4>, p);
     return cudaLaunchKernelEx(&cfg, matmul_any_kernel<INT8, 1>, p);
 }

@@ -624,6 +624,15 @@ cudaError_t launch_tile(const MatmulP& m, const Cut& cut, cudaLaunchConfig_t cfg
     }
     const cudaError_t e = allow_smem(fn, C::kSmem);
     if (e != cudaSuccess) return e;
+    if constexpr (INT8) {
+        // the registers that the warps ask for have to be there, or they would wait for ever
+        static const bool there = [&] {
+            cudaFuncAttributes f;
+            constexpr int need = 4 * C::kRegsFew + C::kSumWarps * C::kRegsSums + 4 * C::kGroups * C::kRegsWide;
+            return cudaFuncGetAttributes(&f, fn) == cudaSuccess && f.numRegs * (C::kThreads / 32) >= need;
+        }();
+        if (!there) return cudaErrorInvalidConfiguration;
+    }
     cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kSmem;
     const int64_t tiles = (int64_t)p.tiles_n * p.tiles_t;

@@ -1,4 +1,8 @@
 """The 8-bit matrix product: int8 bit for bit against exact sums, E4M3 against 64 bits within the derived bound."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -59,14 +63,15 @@ def test_sizes(t, n, k, fp8):
         check(out, a, w, sa, sw, b, dtype, fp8)
 
 
-@pytest.mark.parametrize("t,n,k", [(1, 48, 131056), (3, 130, 131071), (70, 130, 131056), (300, 40, 131056)])
+@pytest.mark.parametrize("t,n,k", [(1, 48, 131056), (3, 130, 131071), (70, 130, 131056), (300, 40, 131056),
+                                   (1300, 2560, 131056)])
 @pytest.mark.parametrize("value", [(-128, -128), (-128, 127), (127, 127)])
 def test_the_largest_int8_sums(t, n, k, value):
     a = torch.full((t, k), value[0], dtype=torch.int8, device="cuda")
     w = torch.full((n, k), value[1], dtype=torch.int8, device="cuda")
     # channel j drops its last j terms, so that sums differ in their low bits
-    for j in range(n):
-        w[j, k - j % 7:] = 0
+    for j in range(7):
+        w[j::7, k - j:] = 0
     one_t, one_n = torch.ones(t, device="cuda"), torch.ones(n, device="cuda")
     out = edge_ops.matmul_q8(a, w, one_t, one_n, dtype=torch.float32)
     terms = torch.tensor([k - j % 7 for j in range(n)], dtype=torch.float64)
@@ -74,9 +79,9 @@ def test_the_largest_int8_sums(t, n, k, value):
     assert torch.equal(out, want)
 
 
-@pytest.mark.parametrize("t", [1, 5, 40, 90, 300])
-def test_e4m3_extremes_and_nan(t):
-    n, k = 200, 512
+@pytest.mark.parametrize("t,n", [(1, 200), (5, 200), (40, 200), (90, 200), (300, 200), (677, 5029)])
+def test_e4m3_extremes_and_nan(t, n):
+    k = 512
     a, w, sa, sw, _ = operands(t, n, k, True, 3)
     a[:, ::2] = 0x7E   # 448
     w[:, ::2] = 0xFE   # -448
@@ -93,9 +98,9 @@ def test_e4m3_extremes_and_nan(t):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
-@pytest.mark.parametrize("t", [1, 3, 30, 150])
-def test_scales_of_nothing_infinities_and_nan(t, fp8):
-    a, w, sa, sw, _ = operands(t, 70, 64, fp8, 4)
+@pytest.mark.parametrize("t,n", [(1, 70), (3, 70), (30, 70), (150, 70), (677, 5029)])
+def test_scales_of_nothing_infinities_and_nan(t, n, fp8):
+    a, w, sa, sw, _ = operands(t, n, 64, fp8, 4)
     sums, _ = ref.product_sums(a, w, fp8)
     sa[0], sw[1], sw[2] = 0.0, float("inf"), float("nan")
     out = edge_ops.matmul_q8(a, w, sa, sw, dtype=torch.float32)
@@ -107,11 +112,11 @@ def test_scales_of_nothing_infinities_and_nan(t, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
-@pytest.mark.parametrize("t", [1, 6, 40, 300])
-@pytest.mark.parametrize("off", [1, 4, 16])
-def test_addresses_and_neighbours(t, off, fp8):
+@pytest.mark.parametrize("t,n", [(1, 136), (6, 136), (40, 136), (300, 136), (677, 5030)])
+@pytest.mark.parametrize("off", [1, 2, 4, 16])
+def test_addresses_and_neighbours(t, n, off, fp8):
     """Operands that start off the vector; values behind and before the output stay as they were."""
-    n, k = 136, 176
+    k = 176
     a, w, sa, sw, _ = operands(t, n, k, fp8, 5)
     at = torch.zeros(t * k + 32, dtype=a.dtype, device="cuda")[off:off + t * k].view(t, k).copy_(a)
     wt = torch.zeros(n * k + 32, dtype=a.dtype, device="cuda")[off:off + n * k].view(n, k).copy_(w)
@@ -146,6 +151,45 @@ def test_runs_streams_and_graphs_give_the_same_bits(t, n, k, fp8):
     a.copy_(b)  # the graph reads its operands when it runs
     graph.replay()
     assert torch.equal(outs[2], edge_ops.matmul_q8(b, w, sa, sw))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_two_streams_at_once(fp8):
+    """Calls that share the GPU: pairs of CTAs, clusters and streams of weights beside each other."""
+    calls = [operands(t, n, k, fp8, 20) for t, n, k in ((700, 2560, 2048), (48, 512, 9728), (4, 2560, 2560), (200, 6144, 1024))]
+    want = [edge_ops.matmul_q8(*c[:4]) for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = [[] for _ in calls]
+    for _ in range(20):
+        for i, (c, s) in enumerate(zip(calls, streams)):
+            got[i].append(edge_ops.matmul_q8(*c[:4], stream=s))
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(w, x) for x in g)
+
+
+def test_first_calls_of_a_process_in_a_graph():
+    """What a call asks of the runtime once (shared memory, resident clusters) can be asked during a capture."""
+    code = """
+import sys
+sys.path[:0] = [{root!r}, {here!r}]
+import torch, test_q8_matmul as m
+from memory_bound_decode_qk_gb300 import edge_ops
+sets = [m.operands(t, n, k, q, 21) for t, n, k in ((4, 640, 512), (48, 512, 9728), (700, 2560, 2048)) for q in (True, False)]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    outs = [edge_ops.matmul_q8(*s[:4]) for s in sets]
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(o, edge_ops.matmul_q8(*s[:4])) for o, s in zip(outs, sets))
+print("same")
+"""
+    here = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, "-c", code.format(root=os.path.dirname(here), here=here)], capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stdout[-2000:] + r.stderr[-2000:]
 
 
 def test_leading_dimensions_and_empty_batches():

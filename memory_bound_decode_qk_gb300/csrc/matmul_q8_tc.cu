@@ -63,7 +63,7 @@ struct Mm {
     static constexpr int kThreads = 128 + 32 * kSumWarps + 128 * kGroups;
     // int8: registers of the three kinds of warps; together at most the launch's, 768
     // threads at 80
-    enum : int { kRegsFew = 40, kRegsSums = PAIR ? 144 : 152, kRegsWide = PAIR ? 48 : 72 };
+    enum : int { kRegsFew = 40, kRegsSums = PAIR ? 144 : 120, kRegsWide = PAIR ? 48 : 80 };
     static_assert(kStages >= 3 && kStages <= 10 && kNeed <= 512, "the ring or the accumulators do not fit");
     static_assert(PAIR || NT * kRows * 4 <= kSmem - 1024, "a part of a cut tile does not fit");
 };
@@ -200,6 +200,7 @@ matmul_tc_kernel(TcP p, const __grid_constant__ CUtensorMap wmap, const __grid_c
     constexpr int TILE = PAIR ? 2 * kRows : kRows;
     extern __shared__ char raw[];
     __shared__ MmSmem sh;
+    __shared__ __align__(16) float scales[SW][NT / (SW / 4)];  // of a warp's tokens
     const int tid = threadIdx.x, lane = tid & 31, wid = uniform(tid >> 5);
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;  // the swizzle works on address bits
     const uint32_t wides = base, ring = base + C::kWides * C::kWide;
@@ -359,6 +360,8 @@ matmul_tc_kernel(TcP p, const __grid_constant__ CUtensorMap wmap, const __grid_c
             const bool mine = ch < p.m.n;
             const float sw = mine ? __ldg(p.m.sw + ch) : 0.0f;
             const float bias = mine && p.m.bias != nullptr ? load_out(p.m.bias, ch, p.m.out_dt) : 0.0f;
+            for (int c = lane; c < h; c += 32) scales[wid - 4][c] = t0 + c < p.m.tokens ? __ldg(p.m.sa + t0 + c) : 0.0f;
+            __syncwarp();
             // the sums of tokens t0 + c ..: to the output, or to this CTA's part of the tile
             auto give = [&](int c, const uint32_t (&v)[CH]) {
                 if (split > 1) {
@@ -368,15 +371,21 @@ matmul_tc_kernel(TcP p, const __grid_constant__ CUtensorMap wmap, const __grid_c
                     }
                     return;
                 }
-                const float nan = *failed ? NAN : 0.0f;
-                // lane j holds the scale of token c + j
-                const float scales = lane < CH && t0 + c + lane < p.m.tokens ? __ldg(p.m.sa + t0 + c + lane) : 0.0f;
+                const float nsw = *failed ? NAN : sw;
                 char* dst = p.m.out + ((int64_t)(t0 + c) * p.m.n + ch) * (p.m.out_dt == kF32 ? 4 : 2);
                 const int64_t next = (int64_t)p.m.n * (p.m.out_dt == kF32 ? 4 : 2);
                 const int count = min(CH, p.m.tokens - t0 - c);
+                float sa[CH];
+#pragma unroll
+                for (int j = 0; j < CH; j += 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(&scales[wid - 4][c + j]);
+                    sa[j] = x.x;
+                    sa[j + 1] = x.y;
+                    sa[j + 2] = x.z;
+                    sa[j + 3] = x.w;
+                }
                 auto value = [&](int j) {
-                    const float sum = (INT8 ? __int2float_rn((int)v[j]) : __uint_as_float(v[j])) + nan;
-                    return scaled(sum, __shfl_sync(0xffffffffu, scales, j), sw, bias);
+                    return scaled(INT8 ? __int2float_rn((int)v[j]) : __uint_as_float(v[j]), sa[j], nsw, bias);
                 };
                 if (p.pairs) {
                     // even lanes store token j of their and their neighbour's channel, odd
@@ -448,7 +457,7 @@ matmul_tc_kernel(TcP p, const __grid_constant__ CUtensorMap wmap, const __grid_c
             }
         }
     } else if constexpr (INT8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"((int)C::kRegsWide));
+        if constexpr (C::kRegsWide < 80) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"((int)C::kRegsWide));
         // ---- widening.  Groups of four warps take the halves of the entries in turn.
         // Weights: a thread's row to its lane of TMEM, two numbers to a column.  Tokens: a
         // 16-byte piece of half a row to two of fp16, both with the 128-byte swizzle; eight
@@ -461,71 +470,66 @@ matmul_tc_kernel(TcP p, const __grid_constant__ CUtensorMap wmap, const __grid_c
         const uint32_t from = ring + kRows * kStep + r * 128 + ((c ^ (r & 7)) << 4);
         const uint32_t to = wides + r * 128 + (((c * 2 + odd) ^ (r & 7)) << 4);
         const int pieces = part * 4;
-        uint32_t n = 0, st = 0, full = 0;
-        for (int i = first; i < tiles; i += step) {
-            for (int e = 2 * e0; e < 2 * e1; ++e, ++n) {
-                if ((int)(n % C::kGroups) == group) {
-                    const uint32_t wd = n % WD;
-                    bar_wait(smem_addr(&sh.full[st]), full, failed);
-                    bar_wait(smem_addr(&sh.narrow[wd]), ((n / WD) & 1) ^ 1, failed);
-                    tc_after();
-                    const uint32_t entry = st * C::kRaw, half = n & 1;
-                    const uint32_t src = (from + entry) ^ (half << 6), dst = to + wd * C::kWide;
-                    // every load before the first number is turned
-                    constexpr int EACH = C::kTokens * 4 / 128 > 0 ? C::kTokens * 4 / 128 : 1;
-                    uint4 x[4], v[EACH];
+        const uint32_t mine_of = first < tiles ? (uint32_t)((tiles - 1 - first) / step + 1) : 0u;  // tiles
+        const uint32_t halves = mine_of * 2u * (uint32_t)(e1 - e0);
+        uint32_t n = group;
+        for (; n < halves; n += C::kGroups) {
+            const uint32_t st = (n >> 1) % ST, wd = n % WD;
+            bar_wait(smem_addr(&sh.full[st]), ((n >> 1) / ST) & 1, failed);
+            bar_wait(smem_addr(&sh.narrow[wd]), ((n / WD) & 1) ^ 1, failed);
+            tc_after();
+            const uint32_t entry = st * C::kRaw, half = n & 1;
+            const uint32_t src = (from + entry) ^ (half << 6), dst = to + wd * C::kWide;
+            // every load before the first number is turned
+            constexpr int EACH = C::kTokens * 4 / 128 > 0 ? C::kTokens * 4 / 128 : 1;
+            uint4 x[4], v[EACH];
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) x[b] = lds_vector(wrow + entry + (((half * 4 + b) ^ wx) << 4));
+            for (int b = 0; b < 4; ++b) x[b] = lds_vector(wrow + entry + (((half * 4 + b) ^ wx) << 4));
 #pragma unroll
-                    for (int u = 0; u < EACH; ++u) {
-                        if (mine + 128 * u < pieces) v[u] = lds_vector(src + u * 4096);
-                    }
+            for (int u = 0; u < EACH; ++u) {
+                if (mine + 128 * u < pieces) v[u] = lds_vector(src + u * 4096);
+            }
 #pragma unroll
-                    for (int b = 0; b < 4; b += 2) {
-                        uint32_t o[16];
-                        widen4(x[b].x, o[0], o[1]);
-                        widen4(x[b].y, o[2], o[3]);
-                        widen4(x[b].z, o[4], o[5]);
-                        widen4(x[b].w, o[6], o[7]);
-                        widen4(x[b + 1].x, o[8], o[9]);
-                        widen4(x[b + 1].y, o[10], o[11]);
-                        widen4(x[b + 1].z, o[12], o[13]);
-                        widen4(x[b + 1].w, o[14], o[15]);
-                        tc_st16(wlane + wd * 32 + b * 8, o);
-                    }
+            for (int b = 0; b < 4; b += 2) {
+                uint32_t o[16];
+                widen4(x[b].x, o[0], o[1]);
+                widen4(x[b].y, o[2], o[3]);
+                widen4(x[b].z, o[4], o[5]);
+                widen4(x[b].w, o[6], o[7]);
+                widen4(x[b + 1].x, o[8], o[9]);
+                widen4(x[b + 1].y, o[10], o[11]);
+                widen4(x[b + 1].z, o[12], o[13]);
+                widen4(x[b + 1].w, o[14], o[15]);
+                tc_st16(wlane + wd * 32 + b * 8, o);
+            }
 #pragma unroll
-                    for (int u = 0; u < EACH; ++u) {
-                        if (mine + 128 * u < pieces) {
-                            uint4 lo, hi;
-                            widen4(odd ? v[u].z : v[u].x, lo.x, lo.y);
-                            widen4(odd ? v[u].w : v[u].y, lo.z, lo.w);
-                            widen4(odd ? v[u].x : v[u].z, hi.x, hi.y);
-                            widen4(odd ? v[u].y : v[u].w, hi.z, hi.w);
-                            sts_vector(dst + u * 4096, lo);
-                            sts_vector((dst + u * 4096) ^ 16, hi);
-                        }
-                    }
-                    tc_wait_st();
-                    tc_before();
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if constexpr (PAIR) {
-                            cluster_bar_arrive(peer_addr(smem_addr(&sh.wide[wd]), 0));
-                        } else {
-                            bar_arrive(smem_addr(&sh.wide[wd]));
-                        }
-                        bar_arrive(smem_addr(&sh.empty[st]));
-                    }
+            for (int u = 0; u < EACH; ++u) {
+                if (mine + 128 * u < pieces) {
+                    uint4 lo, hi;
+                    widen4(odd ? v[u].z : v[u].x, lo.x, lo.y);
+                    widen4(odd ? v[u].w : v[u].y, lo.z, lo.w);
+                    widen4(odd ? v[u].x : v[u].z, hi.x, hi.y);
+                    widen4(odd ? v[u].y : v[u].w, hi.z, hi.w);
+                    sts_vector(dst + u * 4096, lo);
+                    sts_vector((dst + u * 4096) ^ 16, hi);
                 }
-                if ((n & 1) && ++st == ST) {
-                    st = 0;
-                    full ^= 1;
+            }
+            tc_wait_st();
+            tc_before();
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (PAIR) {
+                    cluster_bar_arrive(peer_addr(smem_addr(&sh.wide[wd]), 0));
+                } else {
+                    bar_arrive(smem_addr(&sh.wide[wd]));
                 }
+                bar_arrive(smem_addr(&sh.empty[st]));
             }
         }
         if constexpr (PAIR) {
             // the other CTA's last arrivals on this one's barriers
+            n = halves;
             for (int i = 0; i < WD; ++i, ++n) bar_wait(smem_addr(&sh.narrow[n % WD]), ((n / WD) & 1) ^ 1, failed);
         }
     }
@@ -550,17 +554,17 @@ matmul_tc_kernel(TcP p, const __grid_constant__ CUtensorMap wmap, const __grid_c
         // the parts lie where the ring was, [token][channel]; every product is done
         __syncwarp();
         cluster_sync();
-        if (wid >= 4 && wid < 4 + SW) {
-            // this CTA's share of the tile's tokens, the parts added in rank order (on the
-            // warps that have the registers); a lane has four channels of a token, a warp
-            // all
+        constexpr int FROM = INT8 ? 4 : 0;  // the warps that have the launch's registers
+        if (wid >= FROM) {
+            // this CTA's share of the tile's tokens, the parts added in rank order; a lane has
+            // four channels of a token, a warp all
             int tn, tt;
             tile_at(p, first, tn, tt);
             const int c0 = NT * rank / split, c1 = min(NT * (rank + 1) / split, p.m.tokens - tt * NT);
             const int ch = tn * kRows + lane * 4;
             float nan = 0.0f;
             for (int r = 0; r < split; ++r) nan = peer_word(peer_addr(smem_addr(&sh.failed), r)) ? NAN : nan;
-            for (int c = c0 + (wid - 4); c < c1; c += SW) {
+            for (int c = c0 + (wid - FROM); c < c1; c += C::kThreads / 32 - FROM) {
                 uint4 v[8];
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
@@ -661,16 +665,18 @@ cudaError_t launch_tile(const MatmulP& m, const Cut& cut, cudaLaunchConfig_t cfg
 // measurements on GB300 (back-to-back launches, weights from memory; 1 to 4096 tokens,
 // 1024 to 19,456 channels, sums of 1024 to 9728 terms):
 //   a ring entry (128 terms)
-//     E4M3: the bytes that an SM takes in, 110 GB/s; a pair's products need 1.25 ns a
-//     token
+//     E4M3: the bytes that an SM takes in, 110 to 120 GB/s; a pair's products need 1.13 ns
+//     a token
 //     int8: widening, 0.35 us (one CTA, 64 tokens 0.44) and 0.47 to 0.55 us (pair)
 //   a launch with its first fetch and last store: 2.4 to 5 us and some ns a token
 //   the sum over a cluster: 2 us and 30 ns a token
+//   a tile among others: no less than its store, 0.4 us and 9 ns a token (one CTA), 1.3 us
+//   and 6 ns (pair)
 // The time that memory takes for the weights (5.5 TB/s) runs beside the entries, the
-// longer of the two and a quarter of the other count.  Over 32 drawn calls its choices took
-// 0.97 (E4M3) and 0.98 (int8) of the best of a sweep of 18 cuts each in the geometric mean,
-// at worst 1.06.  Measured around them: 2560 x 9728 in E4M3, 64 tokens, 11.1 us split over six CTAs against
-// 21.4 unsplit and 17.5 by pairs of 96 tokens; 1024 tokens, 21.5 us with pairs of 160
+// longer of the two and a quarter of the other count.  Over 22 drawn calls of each type its
+// choices took 1.02 (E4M3) and 0.99 (int8) times the best of a sweep of up to 20 cuts in
+// the geometric mean, at worst 1.16.  Measured around them: 2560 x 9728 in E4M3, 64 tokens, 11.1 us split over six CTAs against
+// 21.4 unsplit and 17.5 by pairs of 96 tokens; 1024 tokens, 20.7 us with pairs of 160
 // tokens (70 tiles on 76 pairs) against 27.4 with 256 (40 tiles) and 29.4 with 128 (80).
 template <bool INT8>
 Cut choose(const MatmulP& m) {
@@ -688,11 +694,13 @@ Cut choose(const MatmulP& m) {
             entry = c.pair ? 0.45 + 0.0005 * c.nt : c.nt <= 32 ? 0.35 : 0.44;
             ends = c.pair ? 5.0 + 0.01 * c.nt : 3.6 + 0.02 * c.nt;
         } else {
-            entry = c.pair ? std::fmax((kRows + c.nt / 2) * 0.00117, c.nt * 0.00125) : (kRows + c.nt) * 0.00117;
+            entry = c.pair ? std::fmax((kRows + c.nt / 2) * 0.00105, c.nt * 0.00113) : (kRows + c.nt) * 0.00117;
             ends = c.pair ? 3.0 + 0.008 * c.nt : 2.4 + 0.01 * c.nt;
         }
         if (c.split > 1) ends += 2.0 + 0.03 * c.nt;
-        const double work = rounds * std::ceil((double)entries / c.split) * entry;
+        double tile_time = std::ceil((double)entries / c.split) * entry;
+        if (rounds > 1) tile_time = std::fmax(tile_time, c.pair ? 1.3 + 0.006 * c.nt : 0.4 + 0.009 * c.nt);
+        const double work = rounds * tile_time;
         const double t = ends + std::fmax(work, memory) + 0.25 * std::fmin(work, memory);
         if (t < least) {
             least = t;

@@ -24,7 +24,9 @@ SHAPES = [(1, 1, 1), (3, 5, 7), (2, 33, 20), (65, 70, 33), (130, 129, 100), (17,
           (9, 74, 2960), (9, 66, 3856), (9, 68, 4000), (609, 138, 3824), (246, 131, 4672), (862, 132, 4752),
           (1248, 135, 2992), (834, 132, 2592), (65, 3853, 4736), (1230, 136, 3968), (1242, 391, 1568), (1409, 5014, 32),
           (588, 2592, 528), (985, 5335, 144), (500, 4957, 672), (582, 5635, 544), (677, 5029, 928), (1424, 5915, 32),
-          (521, 4906, 272)]
+          (521, 4906, 272), (197, 4923, 32), (296, 4891, 32), (392, 4872, 32), (418, 5545, 32), (587, 4907, 32),
+          (676, 4871, 32), (975, 133, 2480), (429, 132, 1936), (679, 69, 3472), (319, 136, 3520), (514, 65, 2480),
+          (1000, 141, 3376)]
 
 
 def operands(t, n, k, fp8, seed=0):

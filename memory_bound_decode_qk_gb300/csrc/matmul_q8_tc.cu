@@ -422,14 +422,23 @@ matmul_tc_kernel(TcP p, const __grid_constant__ CUtensorMap wmap, const __grid_c
                     const uint32_t buf = unit & 1;
                     bar_wait(smem_addr(&sh.sum[buf]), (unit >> 1) & 1, failed);
                     tc_after();
+                    if constexpr (H >= 32) {
+                        // (h is a multiple of 16: the last columns may be those of nobody)
 #pragma unroll
-                    for (int c = 0; c < H; c += CH) {
-                        if (c >= h) continue;
+                        for (int c = 0; c < H; c += 32) {
+                            if (c >= h) continue;
+                            uint32_t v[32];
+                            tc_ld32(lanes + buf * NT + c, v);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) acc[c + j] += (uint32_t)__float2int_rn(__uint_as_float(v[j]));
+                        }
+                    } else {
                         uint32_t v[CH];
-                        tc_ld16(lanes + buf * NT + c, v);
+                        tc_ld16(lanes + buf * NT, v);
                         tc_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < CH; ++j) acc[c + j] += (uint32_t)__float2int_rn(__uint_as_float(v[j]));
+                        for (int j = 0; j < CH; ++j) acc[j] += (uint32_t)__float2int_rn(__uint_as_float(v[j]));
                     }
                     release(buf);
                 }

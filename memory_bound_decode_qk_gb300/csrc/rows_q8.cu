@@ -28,7 +28,7 @@
 // codes.  Measured with E4M3 codes: norm of 4096 x 4096 bf16 11.0 us (4.6 TB/s), with the
 // residual 19.5 (6.0), tanh-GELU gate of 4001 x 10,240 36.0 (5.7), 2500 x 4096 fp32
 // quantized 8.3 (6.1).  Rows longer than a CTA holds, or of a length or alignment that
-// 16-byte vectors do not suit, take a two-pass kernel of one CTA per row.
+// 16-byte vectors do not suit, take a kernel of one CTA per row.
 #include "edge_common.cuh"
 #include "glu_math.cuh"
 #include "launch.h"
@@ -235,15 +235,21 @@ __global__ void __launch_bounds__(512) rows_q8_kernel(RowsQ8P p) {
 
 // ---------------------------------------------------------------- any row
 
-// Any length and alignment: one CTA per row, two passes (the second hits L1/L2).
-// The sum of squares is accumulated in fp64, as in the scalar RMSNorm kernel: a
-// thread sums up to 65,536 terms here.
+// Any length and alignment: one CTA per row, an element per load.  A thread issues the
+// loads of 8 elements before it uses one and holds the products of its first 16; a
+// longer row's are loaded and computed again for the codes.  8 squares are summed in fp32
+// and those sums in fp64 (a thread has up to 32,768 terms, and this GPU is slow in fp64:
+// with every square added there, 4096 rows of 4095 bf16 took 93 us, now 41).  Measured too:
+// tanh-GELU gate of 4001 rows of 10,239 84 us, 2500 rows of 4095 fp32 quantized 14.5.  An
+// element per load is the bound: 2 or 4 bytes where the aligned kernel has 16.
 template <typename T, int KIND>
-__global__ void __launch_bounds__(256) rows_q8_any_kernel(RowsQ8P p) {
+__global__ void __launch_bounds__(512, 2) rows_q8_any_kernel(RowsQ8P p) {
     constexpr bool NORM = kIsNorm<KIND>, ADD = KIND == kAddNorm, GATE = kIsGate<KIND>;
-    __shared__ double red[8];
-    __shared__ float red_top[8];
+    constexpr int U = 8, HELD = 2;
+    __shared__ double red[16];
+    __shared__ float red_top[16];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    const int stride = U * blockDim.x;
 
     pdl_wait();
     pdl_launch_dependents();
@@ -252,26 +258,64 @@ __global__ void __launch_bounds__(256) rows_q8_any_kernel(RowsQ8P p) {
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
         const T* x = reinterpret_cast<const T*>(p.x) + row * p.n * (GATE ? 2 : 1);
         T* res = ADD ? reinterpret_cast<T*>(p.res) + row * p.n : nullptr;
-        // s: the value that the norm squares
-        auto product = [&](int i, float s) {
-            if constexpr (GATE) {
-                return gate_fast<KIND == kGateSilu ? kSilu : kGelu>(s, to_f(x[(int64_t)p.n + i]));
-            } else if constexpr (NORM) {
-                return w != nullptr ? __fmul_rn(s, __fadd_rn(to_f(w[i]), p.delta)) : s;
-            } else {
-                return s;
-            }
-        };
+        uint8_t* out = reinterpret_cast<uint8_t*>(p.out) + row * p.n;
         double ss = 0.0;
         float top = 0.0f;
-        for (int i = threadIdx.x; i < p.n; i += blockDim.x) {
-            float a = to_f(x[i]);
-            if constexpr (ADD) {
-                a = round_to<T>(__fadd_rn(a, to_f(res[i])));
-                res[i] = from_f<T>(a);
+        // the products of 8 elements from i0 on, zeros behind the row; `again`: of a row whose
+        // sum and maximum are known (and stored)
+        auto products = [&](int i0, bool again, float (&y)[U]) {
+            T a[U], b[U], c[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * blockDim.x + threadIdx.x;
+                const bool ok = i < p.n;
+                if (!ADD || !again) a[u] = ok ? __ldg(x + i) : from_f<T>(0.0f);
+                if constexpr (ADD) b[u] = ok ? res[i] : from_f<T>(0.0f);
+                if constexpr (GATE) b[u] = ok ? __ldg(x + (int64_t)p.n + i) : from_f<T>(0.0f);
+                if constexpr (NORM) c[u] = ok && w != nullptr ? __ldg(w + i) : from_f<T>(0.0f);
             }
-            if constexpr (NORM) ss = __fma_rn((double)a, (double)a, ss);
-            top = max_abs(top, product(i, a));
+            float part = 0.0f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * blockDim.x + threadIdx.x;
+                if constexpr (ADD) {
+                    if (again) {
+                        y[u] = to_f(b[u]);
+                    } else {
+                        const T sum = from_f<T>(__fadd_rn(to_f(a[u]), to_f(b[u])));
+                        if (i < p.n) res[i] = sum;
+                        y[u] = to_f(sum);
+                    }
+                } else {
+                    y[u] = to_f(a[u]);
+                }
+                if constexpr (NORM) {
+                    part = __fmaf_rn(y[u], y[u], part);
+                    if (w != nullptr) y[u] = __fmul_rn(y[u], __fadd_rn(to_f(c[u]), p.delta));
+                }
+                if constexpr (GATE) {
+                    if (u % 2 == 1) {
+                        const float2 v = gate_fast2<KIND == kGateSilu ? kSilu : kGelu>(
+                            make_float2(y[u - 1], y[u]), make_float2(to_f(b[u - 1]), to_f(b[u])));
+                        y[u - 1] = v.x;
+                        y[u] = v.y;
+                        if (!again) top = max_abs(top, v.x, v.y);
+                    }
+                    continue;
+                }
+                if (i >= p.n) y[u] = 0.0f;
+                if (!again) top = max_abs(top, y[u]);
+            }
+            if (NORM && !again) ss = __dadd_rn(ss, (double)part);
+        };
+        float held[HELD][U];
+#pragma unroll
+        for (int h = 0; h < HELD; ++h) {
+            if (h * stride < p.n) products(h * stride, false, held[h]);
+        }
+        for (int i0 = HELD * stride; i0 < p.n; i0 += stride) {
+            float y[U];
+            products(i0, false, y);
         }
         if constexpr (NORM) ss = group_sum<32>(ss);
         top = warp_max(top);
@@ -283,7 +327,7 @@ __global__ void __launch_bounds__(256) rows_q8_any_kernel(RowsQ8P p) {
         ss = 0.0;
         top = 0.0f;
         for (int k = 0; k < nw; ++k) {
-            ss = __dadd_rn(ss, red[k]);
+            if constexpr (NORM) ss = __dadd_rn(ss, red[k]);
             top = max_abs(top, red_top[k]);
         }
         __syncthreads();
@@ -292,9 +336,21 @@ __global__ void __launch_bounds__(256) rows_q8_any_kernel(RowsQ8P p) {
             p.scales[row] = NORM ? __fmul_rn(inv_rms((float)ss, p.inv_n, p.eps), step) : step;
         }
         const float inv = inverse_of(top, p.fp8);
-        uint8_t* out = reinterpret_cast<uint8_t*>(p.out) + row * p.n;
-        for (int i = threadIdx.x; i < p.n; i += blockDim.x) {
-            out[i] = code_of(product(i, ADD ? to_f(res[i]) : to_f(x[i])), inv, p.fp8);
+        auto codes = [&](int i0, const float (&y)[U]) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * blockDim.x + threadIdx.x;
+                if (i < p.n) out[i] = code_of(y[u], inv, p.fp8);
+            }
+        };
+#pragma unroll
+        for (int h = 0; h < HELD; ++h) {
+            if (h * stride < p.n) codes(h * stride, held[h]);
+        }
+        for (int i0 = HELD * stride; i0 < p.n; i0 += stride) {
+            float y[U];
+            products(i0, true, y);
+            codes(i0, y);
         }
     }
 }
@@ -355,11 +411,12 @@ cudaError_t launch_kind(const RowsQ8Args& a, RowsQ8P& p, cudaStream_t s) {
             }
         }
     }
-    int64_t blocks = a.rows;
-    const int64_t cap = (int64_t)sms * 16;
-    if (blocks > cap) blocks = cap;
-    cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(256);
+    // 16 elements per thread, in 2 to 16 warps
+    int64_t warps = (a.n + 32 * 16 - 1) / (32 * 16);
+    warps = warps < 2 ? 2 : warps > 16 ? 16 : warps;
+    const int64_t cap = (int64_t)sms * 32;
+    cfg.gridDim = dim3((unsigned)(a.rows < cap ? a.rows : cap));
+    cfg.blockDim = dim3((unsigned)(32 * warps));
     return cudaLaunchKernelEx(&cfg, rows_q8_any_kernel<T, KIND>, p);
 }
 

@@ -11,7 +11,9 @@ DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
 # rows x codes: single values, odd lengths, a vector more or less than a warp or a CTA holds, the longest row in
 # registers (16-bit types: 32,768) and one that is longer
 SHAPES = [(1, 1), (3, 7), (5, 48), (2, 100), (1, 2560), (67, 2048), (9, 2056), (700, 128), (400, 1152), (310, 4096),
-          (2, 9728), (305, 9728), (2, 32768), (3, 32776), (2, 40001)]
+          (2, 9728), (305, 9728), (2, 32768), (3, 32776), (2, 40001),
+          # an element per load: one and two groups of 8 held, the rest computed again, rows for a second round
+          (300, 511), (65, 2561), (9, 4095), (3, 8193), (5, 10239), (5000, 33)]
 
 
 def rows_of(dt, rows, n, seed=0, spread=12.0):

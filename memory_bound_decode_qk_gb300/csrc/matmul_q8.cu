@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kThreadsAny, 3) matmul_any_kernel(MatmulP p, i
 template <bool INT8>
 cudaError_t launch_any(const MatmulP& p, cudaLaunchConfig_t cfg) {
     const int64_t tiles = (int64_t)((p.tokens + kTile - 1) / kTile) * ((p.n + kTile - 1) / kTile);
-    if (tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
+    if (tiles > INT32_MAX / 8) return cudaErrorInvalidConfiguration;
     const void* fn = reinterpret_cast<const void*>(matmul_any_kernel<INT8>);
     cfg.blockDim = dim3(kThreadsAny);
     // The cut with the least time in units of a step: the rounds of CTAs times the steps of a

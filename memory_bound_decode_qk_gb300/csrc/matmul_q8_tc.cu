@@ -710,9 +710,10 @@ cudaError_t launch_tile(const MatmulP& m, const Cut& cut, cudaLaunchConfig_t cfg
 // The time that memory takes for the weights (5.5 TB/s) runs beside the entries, the
 // longer of the two and a quarter of the other count.  Over 22 drawn calls of each type its
 // choices took 1.02 (E4M3) and 0.99 (int8) times the best of a sweep of up to 20 cuts in
-// the geometric mean, at worst 1.16.  Measured around them: 2560 x 9728 in E4M3, 64 tokens, 11.1 us split over six CTAs against
-// 21.4 unsplit and 17.5 by pairs of 96 tokens; 1024 tokens, 20.7 us with pairs of 160
-// tokens (70 tiles on 76 pairs) against 27.4 with 256 (40 tiles) and 29.4 with 128 (80).
+// the geometric mean, at worst 1.16.  Measured around them: 2560 x 9728 in E4M3, 64
+// tokens, 11.1 us split over six CTAs against 21.4 unsplit and 17.5 by pairs of 96 tokens;
+// 1024 tokens, 20.7 us with pairs of 160 tokens (70 tiles on 76 pairs) against 27.4 with
+// 256 (40 tiles) and 29.4 with 128 (80).
 template <bool INT8>
 Cut choose(const MatmulP& m) {
     const double sms = sm_count();

@@ -201,7 +201,7 @@ import sys
 sys.path[:0] = [{root!r}, {here!r}]
 import torch, test_q8_matmul as m
 from memory_bound_decode_qk_gb300 import edge_ops
-sets = [m.operands(t, n, k, q, 21) for t, n, k in ((4, 640, 512), (48, 512, 9728), (700, 2560, 2048)) for q in (True, False)]
+sets = [m.operands(t, n, k, q, 21) for t, n, k in ((4, 640, 512), (48, 512, 9728), (700, 2560, 2048), (5, 90, 2047)) for q in (True, False)]
 torch.cuda.synchronize()
 graph = torch.cuda.CUDAGraph()
 with torch.cuda.graph(graph):

@@ -485,11 +485,13 @@ int64_t edge_pages_compact_workspace(int32_t num_pages);
  *   edge_glu_act_q8:   p_i = act(gate_up[t, i]) * gate_up[t, n + i]
  *   edge_quantize_q8:  p_i = x[t, i]
  *   m = max_i |p_i|,  Q = 127 (EDGE_INT8) or 448 (EDGE_FP8_E4M3),
- *   code_i = round(p_i * inv) to nearest even,  inv = min(Q / m, 2^126)  (for E4M3
- *       the product is rounded to fp32 first, for int8 it is not),
+ *   code_i = round(p_i * inv) to nearest even,  inv = min(Q / m, 2^126)  (the product
+ *       is rounded to fp32 first; inv is an fp32 number for E4M3, and for int8 is held
+ *       to 2^-44 of itself, so that a value halfway between two codes takes the even
+ *       one),
  *   scales[t] = step, or r_t * step for the norms (r_t as in edge_rmsnorm),
  *   step = max(m / Q, 2^-126),
- * all in fp32, the divisions IEEE.  The factor r_t of the norm is common to the
+ * all in fp32 but for that, the divisions IEEE.  The factor r_t of the norm is common to the
  * row, so it enters the scale alone; int8 codes lie in -127 .. 127.
  * A row with a NaN or an infinity among its products has a scale that is NaN or
  * infinite (the norms: NaN), and codes without a meaning.

@@ -67,12 +67,14 @@ def check_codes(codes, y, fp8, err=0.0):
 
 
 def plain_codes(p, fp8):
-    """The codes of fp32 products p on the CPU, by the formula with IEEE operations (a product of two fp32 numbers is
-    exact in 64 bits): what the kernels have to give bit for bit."""
+    """The codes of fp32 products p on the CPU, by the formula with IEEE operations: what the kernels have to give bit
+    for bit.  int8: p Q / m rounded to fp32 and then to the nearest even code, the quotient in 64 bits (p Q is exact
+    there)."""
     m = p.abs().amax(-1, keepdim=True)
     inv = torch.minimum(torch.full_like(m, TOP[fp8]) / m, torch.tensor(2.0 ** 126))
     if not fp8:
-        return (p.double() * inv.double()).round().to(torch.int8)
+        y = torch.where(inv < 2.0 ** 126, p.double() * TOP[fp8] / m.double(), p.double() * 2.0 ** 126)
+        return y.float().round().to(torch.int8)
     return (p * inv).clamp(-448.0, 448.0).to(torch.float8_e4m3fn).view(torch.uint8)
 
 

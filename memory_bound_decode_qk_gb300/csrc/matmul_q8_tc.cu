@@ -360,6 +360,7 @@ matmul_tc_kernel(TcP p, const __grid_constant__ CUtensorMap wmap, const __grid_c
             const bool mine = ch < p.m.n;
             const float sw = mine ? __ldg(p.m.sw + ch) : 0.0f;
             const float bias = mine && p.m.bias != nullptr ? load_out(p.m.bias, ch, p.m.out_dt) : 0.0f;
+            __syncwarp();  // every lane has read the last tile's scales
             for (int c = lane; c < h; c += 32) scales[wid - 4][c] = t0 + c < p.m.tokens ? __ldg(p.m.sa + t0 + c) : 0.0f;
             __syncwarp();
             // the sums of tokens t0 + c ..: to the output, or to this CTA's part of the tile

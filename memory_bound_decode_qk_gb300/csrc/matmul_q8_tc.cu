@@ -246,7 +246,6 @@ matmul_tc_kernel(TcP p, const __grid_constant__ CUtensorMap wmap, const __grid_c
     }
     tc_before();
     if constexpr (PAIR) {
-        __syncwarp();
         cluster_sync();  // both CTAs' barriers are there
     } else {
         __syncthreads();
@@ -587,7 +586,6 @@ matmul_tc_kernel(TcP p, const __grid_constant__ CUtensorMap wmap, const __grid_c
     }
     if (!PAIR && split > 1) {
         // the parts lie where the ring was, [token][channel]; every product is done
-        __syncwarp();
         cluster_sync();
         constexpr int FROM = INT8 ? 4 : 0;  // the warps that have the launch's registers
         if (wid >= FROM) {

@@ -22,3 +22,16 @@ def test_every_tile_has_its_own_scales(t, n, k, dtype, fp8):
     check(first, a, w, sa, sw, bias.to(dtype), dtype, fp8)
     for _ in range(5):
         assert torch.equal(edge_ops.matmul_q8(a, w, sa, sw, bias=bias.to(dtype), dtype=dtype), first)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+# sums cut over a cluster: 1 to 63 channels or tokens more than a tile, so that some lanes and warps store nothing
+@pytest.mark.parametrize("t,n,k", [(9, 1, 2592), (9, 65, 1968), (17, 131, 3872), (33, 129, 9728), (64, 193, 9728), (2, 70, 321),
+                                   (9, 201, 9727), (65, 65, 2049), (20, 131, 579)])
+def test_ragged_ends_of_a_cut_sum(t, n, k, fp8):
+    a, w, sa, sw, bias = operands(t, n, k, fp8, 32)
+    for dtype in (torch.float32, torch.bfloat16):
+        first = edge_ops.matmul_q8(a, w, sa, sw, bias=bias.to(dtype), dtype=dtype)
+        check(first, a, w, sa, sw, bias.to(dtype), dtype, fp8)
+        for _ in range(20):
+            assert torch.equal(edge_ops.matmul_q8(a, w, sa, sw, bias=bias.to(dtype), dtype=dtype), first)

@@ -32,8 +32,8 @@
 // TB/s), bound by the launch's beginning, the join and the bytes a CTA has in flight.
 //
 // Every wait has a limit of two seconds.  A wait that runs out (which correct
-// operation never does) ends all later waits of the CTA at once and makes its
-// outputs NaN.
+// operation never does) ends all later waits of the CTA, and of a pair's other CTA, at
+// once and makes their outputs NaN; a cluster that shares a tile reads every flag.
 #include <cmath>
 
 #include "matmul_common.cuh"
@@ -270,7 +270,7 @@ matmul_tc_kernel(TcP p, const __grid_constant__ CUtensorMap wmap, const __grid_c
                 const int y = tn * TILE + mine_n, t = tt * nt + (PAIR ? rank * part : 0);
                 for (int e = e0; e < e1; ++e) {
                     const uint32_t dst = ring + st * C::kRaw, bar = smem_addr(&sh.full[st]);
-                    bar_wait(smem_addr(&sh.empty[st]), phase, failed);
+                    bar_wait<PAIR>(smem_addr(&sh.empty[st]), phase, failed);
                     if constexpr (PAIR && !INT8) {
                         // the products wait for both CTAs' operands on the first one's barrier
                         if (rank == 0) bar_expect(bar, 2 * bytes, lead);
@@ -291,7 +291,7 @@ matmul_tc_kernel(TcP p, const __grid_constant__ CUtensorMap wmap, const __grid_c
             if constexpr (PAIR && !INT8) {
                 // the other CTA's last arrivals on this one's barriers
                 for (int i = 0; i < ST; ++i) {
-                    bar_wait(smem_addr(&sh.empty[st]), phase, failed);
+                    bar_wait<PAIR>(smem_addr(&sh.empty[st]), phase, failed);
                     if (++st == ST) {
                         st = 0;
                         phase ^= 1;
@@ -309,12 +309,12 @@ matmul_tc_kernel(TcP p, const __grid_constant__ CUtensorMap wmap, const __grid_c
             for (int i = first; i < tiles; i += step) {
                 for (int e = e0; e < e1; ++unit) {
                     const uint32_t buf = unit & 1, d = tmem + buf * NT;
-                    bar_wait(smem_addr(&sh.taken[buf]), ((unit >> 1) & 1) ^ 1, failed);
+                    bar_wait<PAIR>(smem_addr(&sh.taken[buf]), ((unit >> 1) & 1) ^ 1, failed);
                     tc_after();
                     const int end = min(e1, e + C::kUnit);
                     uint32_t more = 0;
                     for (int count = (end - e) * HALVES; count > 0; --count) {
-                        bar_wait(smem_addr(INT8 ? &sh.wide[st] : &sh.full[st]), phase, failed);
+                        bar_wait<PAIR>(smem_addr(INT8 ? &sh.wide[st] : &sh.full[st]), phase, failed);
                         tc_after();
                         const uint64_t at = st * (uint64_t)(BYTES >> 4);
 #pragma unroll
@@ -445,7 +445,7 @@ matmul_tc_kernel(TcP p, const __grid_constant__ CUtensorMap wmap, const __grid_c
                 for (int c = 0; c < H; ++c) acc[c] = 0u;
                 for (int e = e0; e < e1; e += C::kUnit, ++unit) {
                     const uint32_t buf = unit & 1;
-                    bar_wait(smem_addr(&sh.sum[buf]), (unit >> 1) & 1, failed);
+                    bar_wait<PAIR>(smem_addr(&sh.sum[buf]), (unit >> 1) & 1, failed);
                     tc_after();
                     if constexpr (H >= 32) {
                         // (h is a multiple of 16: the last columns may be those of nobody)
@@ -477,7 +477,7 @@ matmul_tc_kernel(TcP p, const __grid_constant__ CUtensorMap wmap, const __grid_c
                 }
             } else {
                 const uint32_t buf = unit & 1;
-                bar_wait(smem_addr(&sh.sum[buf]), (unit >> 1) & 1, failed);
+                bar_wait<PAIR>(smem_addr(&sh.sum[buf]), (unit >> 1) & 1, failed);
                 tc_after();
 #pragma unroll 1
                 for (int c = 0; c < h; c += CH) {
@@ -509,8 +509,8 @@ matmul_tc_kernel(TcP p, const __grid_constant__ CUtensorMap wmap, const __grid_c
         uint32_t n = group;
         for (; n < halves; n += C::kGroups) {
             const uint32_t st = (n >> 1) % ST, wd = n % WD;
-            bar_wait(smem_addr(&sh.full[st]), ((n >> 1) / ST) & 1, failed);
-            bar_wait(smem_addr(&sh.narrow[wd]), ((n / WD) & 1) ^ 1, failed);
+            bar_wait<PAIR>(smem_addr(&sh.full[st]), ((n >> 1) / ST) & 1, failed);
+            bar_wait<PAIR>(smem_addr(&sh.narrow[wd]), ((n / WD) & 1) ^ 1, failed);
             tc_after();
             const uint32_t entry = st * C::kRaw, half = n & 1;
             const uint32_t src = (from + entry) ^ (half << 6), dst = to + wd * C::kWide;
@@ -564,12 +564,12 @@ matmul_tc_kernel(TcP p, const __grid_constant__ CUtensorMap wmap, const __grid_c
         if constexpr (PAIR) {
             // the other CTA's last arrivals on this one's barriers
             n = halves;
-            for (int i = 0; i < WD; ++i, ++n) bar_wait(smem_addr(&sh.narrow[n % WD]), ((n / WD) & 1) ^ 1, failed);
+            for (int i = 0; i < WD; ++i, ++n) bar_wait<PAIR>(smem_addr(&sh.narrow[n % WD]), ((n / WD) & 1) ^ 1, failed);
         }
     }
     tc_before();
-    __syncthreads();
-    if (*failed) {
+    // (one answer for the CTA: the other one of a pair can set the flag at any time)
+    if (__syncthreads_or((int)*failed)) {
         // copies that nobody waited for end before the shared memory is given up
         for (const uint64_t t0 = now_ns(); now_ns() - t0 < 1000000ull;) {
         }

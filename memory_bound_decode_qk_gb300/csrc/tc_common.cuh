@@ -45,19 +45,34 @@ __device__ __forceinline__ uint64_t now_ns() {
     asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
     return t;
 }
+// Sets the flag at the same shared-memory address of the other CTA of a pair (clusters of
+// two), and lets nothing that follows be seen before it and this CTA's own flag.
+__device__ __forceinline__ void fail_pair(volatile uint32_t* failed) {
+    asm volatile(
+        "{\n\t.reg .u32 r, a;\n\t"
+        "mov.u32 r, %%cluster_ctarank;\n\t"
+        "xor.b32 r, r, 1;\n\t"
+        "mapa.shared::cluster.u32 a, %0, r;\n\t"
+        "st.shared::cluster.u32 [a], 1;\n\t"
+        "fence.acq_rel.cluster;\n\t}" ::"r"(smem_addr(const_cast<const uint32_t*>(failed)))
+        : "memory");
+}
 // Waits for the phase of `parity`; gives up after the limit, or at once if the
-// CTA has failed.
-__device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* failed) {
+// CTA has failed.  Of a pair that works on the same products both CTAs have then failed,
+// before the thread arrives or commits anywhere: neither stores what they made.
+template <bool PAIR = false>
+__device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* failed,
+                                         uint64_t limit = kWaitLimit) {
     if (bar_try(bar, parity)) return;
     const uint64_t t0 = now_ns();
     for (;;) {
         for (int i = 0; i < 16; ++i) {
             if (bar_try(bar, parity)) return;
         }
-        if (*failed) return;
-        if (now_ns() - t0 > kWaitLimit) break;
+        if (*failed || now_ns() - t0 > limit) break;
     }
     *failed = 1u;
+    if constexpr (PAIR) fail_pair(failed);
 }
 
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }

@@ -13,6 +13,7 @@
 #include <mutex>
 
 #include "../../include/edge_ops.h"
+#include "answers.h"
 #include "launch.h"
 
 namespace edge {
@@ -61,36 +62,26 @@ int resident_ctas(const void* fn, int threads) {
 }
 
 int resident_clusters(const void* fn, const cudaLaunchConfig_t& cfg, int n) {
-    struct Entry {
-        const void* fn;
-        int size, dev, clusters;
-    };
-    static std::mutex mu;
-    static Entry table[256];
-    static int used = 0;
+    static Answers<256> answers;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;
-    std::lock_guard<std::mutex> lock(mu);
-    for (int i = 0; i < used; ++i) {
-        if (table[i].fn == fn && table[i].size == n && table[i].dev == dev) return table[i].clusters;
-    }
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)n;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t one = {};
-    one.gridDim = dim3((unsigned)n);
-    one.blockDim = cfg.blockDim;
-    one.dynamicSmemBytes = cfg.dynamicSmemBytes;
-    one.attrs = attr;
-    one.numAttrs = 1;
-    int clusters = 0;
-    if (cudaOccupancyMaxActiveClusters(&clusters, fn, &one) != cudaSuccess) {
+    const int clusters = answers.get(fn, n, dev, [&] {
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)n;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t one = {};
+        one.gridDim = dim3((unsigned)n);
+        one.blockDim = cfg.blockDim;
+        one.dynamicSmemBytes = cfg.dynamicSmemBytes;
+        one.attrs = attr;
+        one.numAttrs = 1;
+        int found = 0;
+        if (cudaOccupancyMaxActiveClusters(&found, fn, &one) == cudaSuccess) return found;
         (void)cudaGetLastError();
-        clusters = 0;
-    }
-    if (used < 256) table[used++] = Entry{fn, n, dev, clusters};
-    return clusters;
+        return -1;
+    });
+    return clusters > 0 ? clusters : 0;
 }
 
 cudaError_t allow_smem(const void* fn, int bytes) {

@@ -189,7 +189,8 @@ int sm_count();
 int resident_ctas(const void* fn, int threads);
 
 // Clusters of `n` CTAs of kernel `fn` resident at the same time, launched as `cfg`
-// says (the occupancy calculator, cached per kernel, size and device).
+// says (the occupancy calculator, cached per kernel, size and device); 0 if it cannot be
+// asked just now.
 int resident_clusters(const void* fn, const cudaLaunchConfig_t& cfg, int n);
 
 // Lets kernel `fn` use `bytes` of dynamic shared memory (asked of the runtime

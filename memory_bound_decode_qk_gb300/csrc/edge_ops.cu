@@ -84,6 +84,19 @@ int resident_clusters(const void* fn, const cudaLaunchConfig_t& cfg, int n) {
     return clusters > 0 ? clusters : 0;
 }
 
+cudaError_t kernel_registers(const void* fn, int* registers) {
+    static Answers<128> answers;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    *registers = answers.get(fn, 0, dev, [&] {
+        cudaFuncAttributes f;
+        e = cudaFuncGetAttributes(&f, fn);
+        return e == cudaSuccess ? f.numRegs : -1;
+    });
+    return e;
+}
+
 cudaError_t allow_smem(const void* fn, int bytes) {
     if (bytes <= 40 * 1024) return cudaSuccess;  // 48 KB with the static part need no leave
     struct Entry {

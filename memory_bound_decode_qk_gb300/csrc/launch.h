@@ -193,6 +193,10 @@ int resident_ctas(const void* fn, int threads);
 // asked just now.
 int resident_clusters(const void* fn, const cudaLaunchConfig_t& cfg, int n);
 
+// Registers of a thread of kernel `fn` (cached per kernel and device).  An error if the
+// runtime does not say just now.
+cudaError_t kernel_registers(const void* fn, int* registers);
+
 // Lets kernel `fn` use `bytes` of dynamic shared memory (asked of the runtime
 // once per kernel and device).
 cudaError_t allow_smem(const void* fn, int bytes);

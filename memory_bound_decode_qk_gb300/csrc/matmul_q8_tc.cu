@@ -660,16 +660,15 @@ cudaError_t launch_tile(const MatmulP& m, const Cut& cut, cudaLaunchConfig_t cfg
     if (!operand_map(&wmap, m.w, m.n, m.k, kRows) || !operand_map(&amap, m.a, m.tokens, m.k, PAIR ? nt / 2 : nt)) {
         return cudaErrorInvalidValue;
     }
-    const cudaError_t e = allow_smem(fn, C::kSmem);
+    cudaError_t e = allow_smem(fn, C::kSmem);
     if (e != cudaSuccess) return e;
     if constexpr (INT8) {
         // the registers that the warps ask for have to be there, or they would wait for ever
-        static const bool there = [&] {
-            cudaFuncAttributes f;
-            constexpr int need = 4 * C::kRegsFew + C::kSumWarps * C::kRegsSums + 4 * C::kGroups * C::kRegsWide;
-            return cudaFuncGetAttributes(&f, fn) == cudaSuccess && f.numRegs * (C::kThreads / 32) >= need;
-        }();
-        if (!there) return cudaErrorInvalidConfiguration;
+        constexpr int need = 4 * C::kRegsFew + C::kSumWarps * C::kRegsSums + 4 * C::kGroups * C::kRegsWide;
+        int registers = 0;
+        e = kernel_registers(fn, &registers);
+        if (e != cudaSuccess) return e;
+        if (registers * (C::kThreads / 32) < need) return cudaErrorInvalidConfiguration;
     }
     cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kSmem;

@@ -44,6 +44,11 @@ cudaError_t cudaOccupancyMaxActiveClusters(int* n, const void*, const cudaLaunch
     *n = 76;
     return broken ? cudaErrorUnknown : cudaSuccess;
 }
+cudaError_t cudaFuncGetAttributes(cudaFuncAttributes* f, const void*) {
+    ++asked;
+    f->numRegs = 80;
+    return broken ? cudaErrorUnknown : cudaSuccess;
+}
 }
 """
 CLUSTERS = FAKES + r"""
@@ -55,6 +60,20 @@ int main() {
     ok = ok && clusters() == 76 && clusters() == 76 && asked == 3;
     device = 1;
     ok = ok && clusters() == 76 && asked == 4;
+    std::puts(ok ? "right" : "wrong");
+    return !ok;
+}
+"""
+REGISTERS = FAKES + r"""
+int main() {
+    int n = 0;
+    auto fails = [&] { return edge::kernel_registers(&device, &n) == cudaErrorUnknown; };
+    auto says = [&] { n = 0; return edge::kernel_registers(&device, &n) == cudaSuccess && n == 80; };
+    bool ok = fails() && fails() && asked == 2;
+    broken = false;
+    ok = ok && says() && says() && asked == 3;
+    device = 1;  // devices are told apart
+    ok = ok && says() && asked == 4;
     std::puts(ok ? "right" : "wrong");
     return !ok;
 }
@@ -77,6 +96,6 @@ def test_the_table(tmp_path):
     run(tmp_path, KEPT)
 
 
-@pytest.mark.parametrize("source", [CLUSTERS], ids=["clusters"])
+@pytest.mark.parametrize("source", [CLUSTERS, REGISTERS], ids=["clusters", "registers"])
 def test_failed_questions_are_asked_again(tmp_path, source):
     run(tmp_path, source, os.path.join(_build.CSRC, "edge_ops.cu"))

@@ -668,7 +668,7 @@ cudaError_t launch_tile(const MatmulP& m, const Cut& cut, cudaLaunchConfig_t cfg
         int registers = 0;
         e = kernel_registers(fn, &registers);
         if (e != cudaSuccess) return e;
-        if (registers * (C::kThreads / 32) < need) return cudaErrorInvalidConfiguration;
+        if (registers * (C::kThreads / 32) < need) return cudaErrorLaunchOutOfResources;
     }
     cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kSmem;
@@ -677,7 +677,7 @@ cudaError_t launch_tile(const MatmulP& m, const Cut& cut, cudaLaunchConfig_t cfg
     int64_t slots = (int64_t)sm_count() * C::kCtas;
     if constexpr (PAIR) {
         slots = resident_clusters(fn, cfg, 2);
-        if (slots < 1) return cudaErrorInvalidConfiguration;
+        if (slots < 1) return cudaErrorLaunchOutOfResources;
     } else {
         cluster = cut.split;
         while (cluster > 1 && tiles > resident_clusters(fn, cfg, cluster)) --cluster;
@@ -713,7 +713,7 @@ cudaError_t launch_tile(const MatmulP& m, const Cut& cut, cudaLaunchConfig_t cfg
 // 1024 tokens, 20.7 us with pairs of 160 tokens (70 tiles on 76 pairs) against 27.4 with
 // 256 (40 tiles) and 29.4 with 128 (80).
 template <bool INT8>
-Cut choose(const MatmulP& m) {
+Cut choose(const MatmulP& m, bool pairs) {
     const double sms = sm_count();
     const int entries = (m.k + kStep - 1) / kStep;
     const double memory = ((double)m.n * m.k + (double)m.tokens * m.k) / 5.5e6;
@@ -750,7 +750,7 @@ Cut choose(const MatmulP& m) {
             consider(Cut{false, nt, split});
         }
     }
-    for (int nt = 32; nt <= (INT8 ? 192 : 256); nt += 32) {
+    for (int nt = 32; pairs && nt <= (INT8 ? 192 : 256); nt += 32) {
         if (m.tokens <= 32 || (nt > 32 && m.tokens <= nt - 32)) break;
         consider(Cut{true, nt, 1});
     }
@@ -759,8 +759,15 @@ Cut choose(const MatmulP& m) {
 
 template <bool INT8>
 cudaError_t launch_kind(const MatmulP& m, cudaLaunchConfig_t cfg) {
-    const Cut cut = choose<INT8>(m);
-    if (cut.pair) return launch_tile<INT8, INT8 ? 192 : 256, true>(m, cut, cfg);
+    Cut cut = choose<INT8>(m, true);
+    if (cut.pair) {
+        const cudaError_t e = launch_tile<INT8, INT8 ? 192 : 256, true>(m, cut, cfg);
+        // no room for pairs (or none that the runtime knows of just now): single CTAs serve
+        // every call
+        if (e != cudaErrorLaunchOutOfResources) return e;
+        (void)cudaGetLastError();
+        cut = choose<INT8>(m, false);
+    }
     if (cut.nt == 16) return launch_tile<INT8, 16, false>(m, cut, cfg);
     if (cut.nt == 32) return launch_tile<INT8, 32, false>(m, cut, cfg);
     return launch_tile<INT8, 64, false>(m, cut, cfg);

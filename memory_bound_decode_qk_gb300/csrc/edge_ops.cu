@@ -181,7 +181,9 @@ bool checked_bytes(int64_t rows, int64_t cols, int64_t bytes, int64_t* out) {
 }
 
 edge_status finish(cudaError_t e) {
-    if (e == cudaSuccess) e = cudaGetLastError();
+    // (taken from the runtime in either case: the next call is not to find it there)
+    const cudaError_t last = cudaGetLastError();
+    if (e == cudaSuccess) e = last;
     if (e != cudaSuccess) {
         g_last_cuda_error = (int)e;
         return EDGE_ERR_CUDA;

@@ -32,3 +32,14 @@ def test_a_kernel_whose_registers_nobody_knows_is_not_launched(program):
     """int8 warps ask for registers, and would wait for ever if there were too few."""
     for cut in q8_cuts.cuts(program, [(64, 2560, 9728, True), (4096, 2560, 9728, True)], "r"):
         assert cut.status == 7 and cut.kernel == "none", cut
+
+
+def test_a_call_that_fails_leaves_no_error_for_the_next(program):
+    """A launch that the runtime refuses, then the same calls again."""
+    calls = [(1, 2560, 2560, True), (64, 2560, 9728, False), (5, 33, 47, True), (64, 2560, 9728, True)]
+    for call in calls:
+        bad, good, other = q8_cuts.cuts(program, [call + (2, 0, 1), call, calls[0]])
+        assert bad.status == 7 and bad.kernel == "none"
+        assert good.status == 0 and other.status == 0, (call, good, other)
+    bad, good = q8_cuts.cuts(program, [(64, 2560, 9728, True), (1, 2560, 2560, True)], "r")
+    assert bad.status == 7 and good.status == 0

@@ -684,7 +684,7 @@ def _explain_q8(x, name, shape, fp8, out, scales):
     dev = x.device
     if dev.type != "cuda":
         raise ValueError(f"{name} must be a CUDA tensor, not on {dev}")
-    if shape[-1] < 1:
+    if not shape or shape[-1] < 1:
         raise ValueError(f"{name} must have rows of at least one code, not shape {tuple(x.shape)}")
     _want(x, name, x.dtype, tuple(x.shape), dev)
     if out is not None:
@@ -708,7 +708,7 @@ def rmsnorm_q8(x, w=None, *, eps=1e-6, weight_offset=0, fp8=False, out=None, sca
     codes (uint8) with fp8=True, and an fp32 scale for each row.  w: [n].
     Returns (out, scales), out * scales[..., None] being the norm."""
     at, shape = x.get_device(), x.shape
-    n = shape[-1]
+    n = shape[-1] if shape else 0
     if not (_q8_fits(at, x, n, shape, fp8, out, scales) and
             (w is None or (w.shape == (n,) and _fits(at, x.dtype, w)))):
         _explain_q8(x, "x", shape, fp8, out, scales)
@@ -735,7 +735,7 @@ def add_rmsnorm_q8(x, residual, w=None, *, eps=1e-6, weight_offset=0, fp8=False,
                    scales=None, stream=None):
     """residual <- x + residual (rounded to the dtype); returns rmsnorm_q8 of it."""
     at, shape = x.get_device(), x.shape
-    n = shape[-1]
+    n = shape[-1] if shape else 0
     if not (_q8_fits(at, x, n, shape, fp8, out, scales) and residual.shape == shape and
             _fits(at, x.dtype, residual) and
             (w is None or (w.shape == (n,) and _fits(at, x.dtype, w)))):
@@ -765,7 +765,7 @@ def glu_act_q8(gate_up, act=SILU, *, fp8=False, out=None, scales=None, stream=No
     returns them: ([..., d], [...])."""
     if isinstance(act, str):
         act = _ACTS[act]
-    at, two_d = gate_up.get_device(), gate_up.shape[-1]
+    at, two_d = gate_up.get_device(), gate_up.shape[-1] if gate_up.shape else 0
     shape = gate_up.shape[:-1] + (two_d // 2,)
     if not (_q8_fits(at, gate_up, two_d // 2, shape, fp8, out, scales) and two_d % 2 == 0):
         _explain_q8(gate_up, "gate_up", shape, fp8, out, scales)
@@ -788,7 +788,7 @@ def glu_act_q8(gate_up, act=SILU, *, fp8=False, out=None, scales=None, stream=No
 def quantize_q8(x, *, fp8=False, out=None, scales=None, stream=None):
     """The rows of x ([..., n]) in 8 bits, as rmsnorm_q8 returns them."""
     at, shape = x.get_device(), x.shape
-    n = shape[-1]
+    n = shape[-1] if shape else 0
     if not _q8_fits(at, x, n, shape, fp8, out, scales):
         _explain_q8(x, "x", shape, fp8, out, scales)
     if not _here(at, stream):
@@ -811,12 +811,12 @@ def matmul_q8(a, w, a_scales, w_scales, *, bias=None, dtype=None, out=None, stre
     a: [..., k] and w: [n, k], both int8 or both E4M3 codes (uint8 or
     float8_e4m3fn); a_scales: [...], w_scales: [n] fp32; bias: [n].  The result
     ([..., n]) and bias have dtype `dtype` (out's, or bf16)."""
-    at, k, n = a.get_device(), a.shape[-1], w.shape[0]
+    at, k, n = a.get_device(), a.shape[-1] if a.shape else 0, w.shape[0] if w.shape else 0
     kind = _CODE_KIND.get(a.dtype)
     if dtype is None:
         dtype = torch.bfloat16 if out is None else out.dtype
     shape = a.shape[:-1] + (n,)
-    if not (at >= 0 and kind is not None and k > 0 and w.shape == (n, k) and a.is_contiguous() and
+    if not (at >= 0 and kind is not None and k > 0 and n > 0 and w.shape == (n, k) and a.is_contiguous() and
             _CODE_KIND.get(w.dtype) == kind and w.get_device() == at and w.is_contiguous() and
             a_scales.shape == shape[:-1] and w_scales.shape == (n,) and
             _fits(at, torch.float32, a_scales, w_scales) and
@@ -850,9 +850,9 @@ def _explain_matmul(a, w, a_scales, w_scales, bias, dtype, out):
         raise ValueError(f"a must be a CUDA tensor, not on {dev}")
     if a.dtype not in _CODE_KIND:
         raise TypeError(f"a must hold int8 or E4M3 codes, not {a.dtype}")
-    if w.dim() != 2 or a.shape[-1] < 1:
-        raise ValueError(f"a and w must be [..., k] and [n, k], not {tuple(a.shape)} and "
-                         f"{tuple(w.shape)}")
+    if w.dim() != 2 or a.dim() < 1 or a.shape[-1] < 1 or w.shape[0] < 1:
+        raise ValueError(f"a and w must be [..., k] and [n, k] with n and k at least 1, not "
+                         f"{tuple(a.shape)} and {tuple(w.shape)}")
     n, k = w.shape[0], a.shape[-1]
     same = w.dtype if _CODE_KIND.get(w.dtype) == _CODE_KIND[a.dtype] else a.dtype
     _want(a, "a", a.dtype, tuple(a.shape), dev)

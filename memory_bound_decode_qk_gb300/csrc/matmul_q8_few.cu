@@ -9,8 +9,9 @@
 // memory is passed.  The weights are the operand with 16 rows: a CTA owns 16 channels
 // and all of the summed dimension, cut over its warps, and each lane has 8 loads of 16
 // bytes in flight.  The warps' sums are added in a fixed order.  Measured on GB300, one
-// token, 6144 channels, 2560 terms (15.8 MB): E4M3 6.4 us (2.5 TB/s), int8 7.0; 2560 x
-// 9728: 8.4 (3.0 TB/s) and 10.8.
+// token, 6144 channels, 2560 terms (15.8 MB): E4M3 5.8 us (2.7 TB/s; 80 registers put two
+// CTAs of 10 warps on an SM, 304 of the 384), int8 6.4 (8 warps, all 384 at once); 2560 x
+// 2560: 3.1 and 5.3.
 //
 // int8 goes through fp16 as in matmul_q8_tc.cu: sums of at most 1024 terms are exact
 // in fp32 and then join an int32.
@@ -139,9 +140,20 @@ cudaError_t launch_kind(const MatmulP& p, cudaLaunchConfig_t cfg) {
 }  // namespace
 
 // At most 8 tokens and 16 MB of weights, rows and addresses on 16 bytes.  Measured on
-// GB300, one token in E4M3 against the kernel on tensor memory: 2.9 and 5.1 us (2560 x
-// 2560), 5.5 to 6.4 and 6.5 (6144 x 2560), 8.4 and 8.0 (2560 x 9728), 13.3 and 9.8
-// (19,456 x 2560).
+// GB300 against the kernel on tensor memory, us, E4M3 with one and eight tokens and int8 (the
+// same with one and eight):
+//                      E4M3 1       E4M3 8       int8
+//      512 x 2560    2.2   4.7    2.4   4.7    3.9   6.5
+//     2560 x 2560    3.1   5.3    3.3   5.3    5.3   7.1
+//     2560 x 4096    4.7   5.6    5.0   5.7    5.9   8.1
+//     6144 x 2560    5.8   6.1    6.2   6.1    6.4   8.6 to 8.9
+//   16,384 x 1024    5.0   5.1    5.2   4.9    7.2   6.4
+//     1600 x 9728    6.2   7.2    6.4   7.2   12.2   9.5
+//     2560 x 9728    8.5   8.7    8.8   8.7   13.1  10.8    (above 16 MB)
+//   19,456 x 2560   12.8  10.6   13.2  10.6   18.4  12.0    (above 16 MB)
+// Where the rule loses: few channels with a long sum, which the other kernel cuts over a
+// cluster and this one only over a CTA's warps (512 x 9728 5.7 and 5.4, int8 11.6 and 7.8;
+// 256 x 16,384 8.2 and 6.1, int8 18.5 and 9.3).
 bool matmul_few_suits(const MatmulP& m) {
     return m.tokens <= 8 && (int64_t)m.n * m.k <= (16 << 20) && m.k % 16 == 0 &&
            reinterpret_cast<uintptr_t>(m.a) % 16 == 0 && reinterpret_cast<uintptr_t>(m.w) % 16 == 0;

@@ -26,10 +26,12 @@
 // As in rows.cu a row stays in registers from its load to its store: a CTA is
 // (32 W) x R threads, W warps share a row and every load of a thread is issued
 // before any arithmetic.  The products are held in fp32 from the maximum to the
-// codes.  Measured with E4M3 codes: norm of 4096 x 4096 bf16 11.0 us (4.6 TB/s), with the
-// residual 19.5 (6.0), tanh-GELU gate of 4001 x 10,240 36.0 (5.7), 2500 x 4096 fp32
-// quantized 8.3 (6.1).  Rows longer than a CTA holds, or of a length or alignment that
-// 16-byte vectors do not suit, take a kernel of one CTA per row.
+// codes.  Measured with E4M3 and int8 codes: norm of 4096 x 4096 bf16 10.3 and 10.5 us (4.9
+// TB/s, 0.72 of a copy's rate: a CTA that reduces has no next row in flight), with the residual
+// 19.1 and 19.2 (6.1), tanh-GELU gate of 4001 x 10,240 35.8 and 36.8 (5.7), quantized 4096 x
+// 4096 bf16 9.0 and 9.2 (5.6), 2500 x 4096 fp32 8.1 and 8.2 (6.3).  Rows longer than a CTA
+// holds, or of a length or alignment that 16-byte vectors do not suit, take a kernel of one
+// CTA per row.
 #include "edge_common.cuh"
 #include "glu_math.cuh"
 #include "launch.h"
@@ -261,7 +263,7 @@ __global__ void __launch_bounds__(512) rows_q8_kernel(RowsQ8P p) {
 // longer row's are loaded and computed again for the codes.  8 squares are summed in fp32
 // and those sums in fp64 (a thread has up to 32,768 terms, and this GPU is slow in fp64:
 // with every square added there, 4096 rows of 4095 bf16 took 93 us, now 41).  Measured too:
-// tanh-GELU gate of 4001 rows of 10,239 84 us, 2500 rows of 4095 fp32 quantized 14.5.  An
+// tanh-GELU gate of 4001 rows of 10,239 84 us, 2500 rows of 4095 fp32 quantized 13.5.  An
 // element per load is the bound: 2 or 4 bytes where the aligned kernel has 16.
 template <typename T, int KIND>
 __global__ void __launch_bounds__(512, 2) rows_q8_any_kernel(RowsQ8P p) {
@@ -398,9 +400,12 @@ cudaError_t launch_kind(const RowsQ8Args& a, RowsQ8P& p, cudaStream_t s) {
         // Vectors per thread.  With few rows, or few vectors in all, as many warps to a row
         // as it fills (one vector each); else the number with the least cost for a vector: a
         // warp's reduction and divisions count for 0.88 of the work on one vector, spread
-        // over V, and lanes behind the row's end are lost (8, for the longest rows, leaves two
-        // CTAs of 16 warps on an SM).  Measured on GB300: the norm of
-        // 4096 rows of 4096 bf16 takes 11.0 us with V = 4, 12.9 with 2 and 17.0 with 1, of
+        // over V, and lanes behind the row's end are lost.  8 is for rows that 16 warps do not
+        // hold with 4: the products of 16-bit types take 81 to 124 registers a thread, so an
+        // SM has one such CTA (fp32 quantized 51, two), and the other choice is to read the
+        // row again, below.  Measured on GB300 (E4M3): 64 rows of 32,768 bf16 quantized 2.7 us
+        // against 12.2, normed 3.7 and 15.3; 1024 of 20,480 normed 23 and 52, SiLU gate 36 and
+        // 42.  Between 1 and 4: the norm of 4096 rows of 4096 bf16 takes 11.0 us with V = 4, 12.9 with 2 and 17.0 with 1, of
         // 1024 rows of 2560 (320 vectors, a sixth of the lanes lost with 3 or 4) 2.9 with 2 and
         // 3.4 with 4; the gate of 512 rows of 2048 2.4 with 1 and 3.0 with 4, of 4096 rows of
         // 9728 34.7 with 4, 39.9 with 3 and 47.4 with rows of 16 warps.

@@ -87,9 +87,11 @@ struct Inverse {
 };
 // E4M3 takes an IEEE division (and so does the step): a plain evaluation of the formulas
 // gives the same codes.  For int8 an approximate quotient h and the residual 127 - h m,
-// which a fused operation has without error, give 127 / m = h + (127 - h m) h / 127 to
-// 2^-44 of itself.  m is scaled so that its reciprocal is normal wherever the quotient is not
-// above the ceiling; a maximum that is infinite has inv = 0, NaN the ceiling.
+// which a fused operation rounds only once, give 127 / m = h + (127 - h m) h / 127 to 2^-44
+// of itself (to 2^-29 for m above 2^113, where the rest is subnormal: still less than the
+// rounding of a product).  m is scaled so that its reciprocal is normal wherever the
+// quotient is not above the ceiling; a maximum that is infinite has inv = 0, NaN the
+// ceiling.
 __device__ __forceinline__ Inverse inverse_of(float most, int fp8) {
     if (fp8) return {fminf(__fdiv_rn(448.0f, most), kInvCeiling), 0.0f};
     float h;

@@ -62,12 +62,12 @@ int main(int argc, char** argv) {
 
 def build(folder):
     """The program, in `folder`; returns its path."""
-    _build.build()
+    obj = os.path.join(_build.LIB_DIR, "obj")
+    names = ("edge_ops", "matmul_q8", "matmul_q8_few", "matmul_q8_tc")
+    _build.build(force=not all(os.path.exists(os.path.join(obj, n + ".cu.o")) for n in names))
     src, exe = os.path.join(folder, "cuts.cpp"), os.path.join(folder, "cuts")
     with open(src, "w") as f:
         f.write(MAIN)
-    obj = os.path.join(_build.LIB_DIR, "obj")
-    names = ("edge_ops", "matmul_q8", "matmul_q8_few", "matmul_q8_tc")
     cuda = os.path.join(os.path.dirname(os.path.dirname(_build.nvcc())), "include")
     r = subprocess.run(["g++", "-std=c++17", "-I", HERE, "-I", cuda, "-iquote", HERE, src,
                         *(os.path.join(obj, n + ".cu.o") for n in names), "-o", exe, "-pthread", "-no-pie",
